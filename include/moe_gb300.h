@@ -374,6 +374,102 @@ MOE_API moe_status moe_layer_fwd_host_fp8(const moe_shape* s, int64_t n_micro,
                                   const float* w2_scale, uint32_t* dev_status, void* ws,
                                   size_t ws_bytes, void* const* streams, void* const* events);
 
+/* ------------------------------------------------- grouped routing ----
+ * Routing with softmax or sigmoid scores, a bias for balance, and groups of
+ * experts, beside the plain softmax top-k of moe_route. Per token, with
+ * logits l over the E experts:
+ *   s_e = softmax(l)_e, or 1 / (1 + exp(-l_e))          scores
+ *   c_e = s_e + select_bias_e                           selection values
+ *   a group (E / n_groups consecutive experts) has the sum of its group_top
+ *   largest c as its value; the topk_groups groups of largest value are kept
+ *   idx = the k experts of largest c in the kept groups, largest first
+ *   w_j = scale * s_idx[j] / (sum over the chosen s if renormalize, else 1)
+ * Equal values go to the lower index. The bias takes no part in the weights.
+ * Which experts are chosen is what these formulas give in binary64 (fp32
+ * arithmetic decides only where its error cannot matter). A logit of -inf
+ * masks its expert: its score is 0 and it comes after every other expert (a
+ * group with fewer than group_top unmasked experts has value -inf); a token
+ * with fewer than k experts left gets masked ones, by index, at weight 0. A
+ * NaN or +inf logit sets MOE_DEV_NONFINITE and masks its expert too. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+typedef struct {
+  int32_t score;        /* MOE_SCORE_* */
+  int32_t n_groups;     /* 1 <= n_groups <= 32, divides E (1: no groups) */
+  int32_t topk_groups;  /* groups kept; k <= topk_groups * E / n_groups */
+  int32_t group_top;    /* 1 or 2, at most E / n_groups */
+  int32_t renormalize;  /* 0 or 1 */
+  float scale;          /* finite */
+} moe_route_config;
+
+/* Grouped routing of fp32 logits [T,E] (for instance moe_route's logits_out).
+ *   in : logits; select_bias [E] fp32 or NULL
+ *   out: topk_idx, topk_w [T,k]; routed_counts [E], P [E] (mean over tokens
+ *        of s_e / sum_e s_e) and aux [1] = E * sum_e routed_e/(T*k) * P_e,
+ *        each or all NULL (with none of them the statistics are not formed).
+ * ws as moe_route; the shape's H, h and capacity_factor take no part. */
+MOE_API moe_status moe_route_grouped(const moe_shape* s, const moe_route_config* cfg,
+                                     const float* logits, const float* select_bias,
+                                     int32_t* topk_idx, float* topk_w, int32_t* routed_counts,
+                                     float* P, float* aux, uint32_t* dev_status, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route_grouped with respect to the logits, the choice of
+ * experts taken as given.
+ *   in : logits [T,E], topk_idx [T,k] as the forward had and gave them;
+ *        grad_topk_w [T,k]; grad_aux [1] with routed_counts [E] (the
+ *        gradient of aux, routed_counts taken as constants), or NULL.
+ *   out: grad_logits [T,E], every element written; 0 at masked experts.
+ * An index outside [0,E) contributes nothing. n_groups, topk_groups and
+ * group_top take no part. Needs no workspace. */
+MOE_API moe_status moe_route_grouped_bwd(const moe_shape* s, const moe_route_config* cfg,
+                                         const float* logits, const int32_t* topk_idx,
+                                         const float* grad_topk_w, const float* grad_aux,
+                                         const int32_t* routed_counts, float* grad_logits,
+                                         void* stream);
+
+/* ----------------------------------------- microscaled 4-bit (MX4) ----
+ * 4-bit floating point in blocks of 32 consecutive values along K with one
+ * power-of-two scale per block (the OCP microscaling format MXFP4): elements
+ * e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), scales e8m0 (2^(byte-127),
+ * 255 = NaN). For a block with largest magnitude amax the scale's exponent is
+ * max(floor(log2 amax) - 2, -127) and an element is value / scale rounded to
+ * nearest even, magnitudes above 6 becoming 6. A block of zeros has byte 0; a
+ * block holding a NaN or an infinity has byte 255, which makes all of it NaN.
+ * Layouts (K a multiple of 64; codes two to a byte, even element low):
+ *   rows    x_q [rows, K/2], x_scale [ceil(K/128)][rows][4]: the bytes of
+ *           the blocks 4i .. 4i+3 of row r at [i][r] (0 past K)
+ *   weights Wq [E, N, K/2] (each output column a row), w_scale
+ *           [E][ceil(N/128)][ceil(K/128)][32][4][4]: block 4i+j of output
+ *           column n at [e][n/128][i][n%32][(n%128)/32][j] (0 past N or K) */
+
+/* bf16 rows x [rows,K] to MX4. n_rows: device, or NULL: rows at or past
+ * *n_rows are neither read nor written (e.g. offsets + E of a dispatch whose
+ * buffers hold T*k rows). 0 <= rows < 2^31, K a multiple of 64, <= 65536. */
+MOE_API moe_status moe_quantize_rows_mx4(int64_t rows, int64_t K, const moe_bf16* x,
+                                         const int32_t* n_rows, uint8_t* x_q, uint8_t* x_scale,
+                                         void* stream);
+
+/* MX4 rows back to bf16 [rows,K]: the values the codes stand for, exactly. */
+MOE_API moe_status moe_dequantize_rows_mx4(int64_t rows, int64_t K, const uint8_t* x_q,
+                                           const uint8_t* x_scale, moe_bf16* x, void* stream);
+
+/* Weights W [E,K,N] bf16 (as moe_expert_ffn takes them) to MX4, once per
+ * weight tensor. 1 <= E <= 256; K, N multiples of 64, <= 65536. */
+MOE_API moe_status moe_quantize_weights_mx4(int64_t E, int64_t K, int64_t N, const moe_bf16* W,
+                                            uint8_t* Wq, uint8_t* w_scale, void* stream);
+
+/* One grouped expert product over ragged expert-major rows on MX4 operands:
+ * D [rows,N] bf16, D[r] = x[r] . W[e]^T for offsets[e] <= r < offsets[e+1],
+ * through GELU-tanh first if gelu is 1; fp32 accumulation. Rows at or past
+ * offsets[E] are left as they were. dev_status is required. Sizes as above. */
+MOE_API moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N,
+                                       const uint8_t* x_q, const uint8_t* x_scale,
+                                       const int32_t* offsets, const uint8_t* Wq,
+                                       const uint8_t* w_scale, int gelu, moe_bf16* D,
+                                       uint32_t* dev_status, void* stream);
+
 /* ---------------------------------------------- expert parallelism ----
  * Experts spread over `world` ranks, rank g holding the E/world consecutive
  * experts g*E/world .. (g+1)*E/world - 1, and each token's rows sent to the

@@ -496,3 +496,141 @@ def comm_compute_ratio(h: int, dtype_bytes: int) -> float:
     """Bytes per FLOP of one token-expert: (2*H*dtype) / (4*H*h) = dtype / (2 h)
     (comm bottleneck 2.3)."""
     return dtype_bytes / (2.0 * h)
+
+
+# ----------------------------------------------------- grouped routing ----
+# Selection runs on c = s + bias in float64; a logit that is not finite masks
+# its expert (score 0, selection value -inf).
+
+def grouped_scores(logits: np.ndarray, score: str) -> np.ndarray:
+    l = np.asarray(logits, np.float64)
+    ok = np.isfinite(l)
+    if score == "sigmoid":
+        t = np.exp(-np.abs(np.where(ok, l, 0.0)))
+        s = np.where(l >= 0, 1.0 / (1.0 + t), t / (1.0 + t))
+    else:
+        m = np.where(ok, l, -np.inf).max(axis=1, keepdims=True)
+        m = np.where(np.isfinite(m), m, 0.0)
+        z = np.where(ok, np.exp(np.where(ok, l, m) - m), 0.0)
+        d = z.sum(axis=1, keepdims=True)
+        s = np.divide(z, d, out=np.zeros_like(z), where=d > 0)
+    return np.where(ok, s, 0.0)
+
+
+def route_grouped(logits, bias, k: int, score: str, n_groups: int = 1, topk_groups: int = 1,
+                  group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """(idx [T,k], w [T,k], scores [T,E]) of grouped routing."""
+    l = np.asarray(logits, np.float64)
+    T, E = l.shape
+    s = grouped_scores(l, score)
+    c = s + (0.0 if bias is None else np.asarray(bias, np.float64)[None, :])
+    c = np.where(np.isfinite(l), c, -np.inf)
+    size = E // n_groups
+    idx = np.empty((T, k), np.int64)
+    for t in range(T):
+        value = np.sort(c[t].reshape(n_groups, size), axis=1)[:, ::-1][:, :group_top].sum(axis=1)
+        kept = np.argsort(-value, kind="stable")[:topk_groups]
+        cand = np.sort(np.concatenate([np.arange(g * size, (g + 1) * size) for g in kept]))
+        idx[t] = cand[np.argsort(-c[t, cand], kind="stable")[:k]]
+    w = np.take_along_axis(s, idx, axis=1)
+    if renormalize:
+        d = w.sum(axis=1, keepdims=True)
+        w = np.divide(w, d, out=np.zeros_like(w), where=d > 0)
+    return idx, scale * w, s
+
+
+def route_grouped_loss(logits, idx, grad_w, score: str, renormalize: bool, scale: float,
+                       grad_aux: float = 0.0, routed=None) -> np.ndarray:
+    """The scalar whose gradient moe_route_grouped_bwd returns, per token."""
+    s = grouped_scores(logits, score)
+    T, E = s.shape
+    w = np.take_along_axis(s, idx, axis=1)
+    if renormalize:
+        w = w / w.sum(axis=1, keepdims=True)
+    loss = (scale * w * grad_w).sum(axis=1)
+    if routed is not None:
+        f = np.asarray(routed, np.float64) / (T * idx.shape[1])
+        loss = loss + grad_aux * E / T * ((s / s.sum(axis=1, keepdims=True)) * f).sum(axis=1)
+    return loss
+
+
+def route_grouped_grad(logits, idx, grad_w, score: str, renormalize: bool, scale: float,
+                       grad_aux: float = 0.0, routed=None) -> np.ndarray:
+    """d loss / d logits by the chain rule, term by term."""
+    s = grouped_scores(logits, score)
+    T, E = s.shape
+    k = idx.shape[1]
+    ds = np.zeros_like(s)           # d loss / d scores
+    rows = np.arange(T)[:, None]
+    w = np.take_along_axis(s, idx, axis=1)
+    if renormalize:
+        d = w.sum(axis=1, keepdims=True)
+        q = np.divide(w, d, out=np.zeros_like(w), where=d > 0)
+        dw = np.divide(scale * (grad_w - (q * grad_w).sum(axis=1, keepdims=True)), d,
+                       out=np.zeros_like(w), where=d > 0)
+    else:
+        dw = scale * grad_w
+    np.add.at(ds, (rows, idx), dw)
+    if routed is not None:
+        f = np.asarray(routed, np.float64)[None, :] / (T * k)
+        tot = s.sum(axis=1, keepdims=True)
+        p = np.divide(s, tot, out=np.zeros_like(s), where=tot > 0)
+        dp = grad_aux * E / T * f
+        ds = ds + np.divide(dp - (p * dp).sum(axis=1, keepdims=True), tot,
+                            out=np.zeros_like(s), where=tot > 0)
+    if score == "sigmoid":
+        return ds * s * (1.0 - s)
+    return s * (ds - (s * ds).sum(axis=1, keepdims=True))
+
+
+# ------------------------------------------------ microscaled 4 bits ----
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def quantize_mx4(a: np.ndarray):
+    """Rows [R, K] -> (codes [R, K], scale bytes [R, K/32]); codes 0-15, bit 3
+    the sign. Nearest magnitude; a value halfway between two goes to the even
+    code; a block with a NaN or infinity has byte 255 and codes 0."""
+    a = np.asarray(a, np.float64)
+    R, K = a.shape
+    b = a.reshape(R, K // 32, 32)
+    amax = np.abs(b).max(axis=2)
+    bad = ~np.isfinite(amax)
+    safe = np.where(bad | (amax == 0), 1.0, amax)
+    exp = np.maximum(np.frexp(safe)[1] - 3, -127)
+    exp = np.where(amax == 0, -127, exp)
+    mag = np.abs(np.where(bad[:, :, None], 0.0, b)) / np.exp2(exp.astype(np.float64))[:, :, None]
+    dist = np.abs(mag[..., None] - E2M1)
+    near = dist == dist.min(axis=-1, keepdims=True)
+    even = near & (np.arange(8) % 2 == 0)
+    code = np.where(near.sum(axis=-1) > 1, even.argmax(axis=-1), near.argmax(axis=-1))
+    code = code | (np.signbit(np.where(bad[:, :, None], 0.0, b)).astype(np.int64) << 3)
+    byte = np.where(bad, 255, exp + 127)
+    return code.reshape(R, K).astype(np.uint8), byte.astype(np.uint8)
+
+
+def mx4_values(code: np.ndarray, byte: np.ndarray) -> np.ndarray:
+    v = E2M1[code & 7] * np.where(code & 8, -1.0, 1.0)
+    s = np.where(byte == 255, np.nan, np.exp2(byte.astype(np.float64) - 127.0))
+    return v * np.repeat(s, 32, axis=1)
+
+
+def pack_mx4_rows(code: np.ndarray, byte: np.ndarray):
+    """-> q [R, K/2], scale [ceil(K/128), R, 4]."""
+    R, n = byte.shape
+    tk = -(-n // 4)
+    pad = np.zeros((R, tk * 4), np.uint8)
+    pad[:, :n] = byte
+    return code[:, 0::2] | (code[:, 1::2] << 4), np.ascontiguousarray(
+        pad.reshape(R, tk, 4).transpose(1, 0, 2))
+
+
+def pack_mx4_weight_scale(byte: np.ndarray) -> np.ndarray:
+    """Scale bytes of one expert [N, K/32] -> [ceil(N/128), ceil(K/128), 32, 4, 4]."""
+    N, n = byte.shape
+    out = np.zeros((-(-N // 128), -(-n // 4), 32, 4, 4), np.uint8)
+    for c in range(N):
+        for b in range(n):
+            out[c // 128, b // 4, c % 32, c % 128 // 32, b % 4] = byte[c, b]
+    return out

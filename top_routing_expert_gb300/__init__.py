@@ -26,6 +26,8 @@ __all__ = [
     "workspace_size_fp8", "moe_quantize_weights_fp8", "moe_layer_fwd_host_fp8", "moe_permute_fp8", "moe_expert_ffn_fp8",
     "moe_layer_fwd_fp8", "moe_combine_fp8", "Fp8Weights", "moe_expert_ffn_gathered",
     "moe_ep_permute", "moe_ep_regroup", "DevicePipeline", "moe_layer_fwd_pipelined",
+    "RouteConfig", "moe_route_grouped", "moe_route_grouped_bwd", "moe_quantize_rows_mx4",
+    "moe_dequantize_rows_mx4", "moe_quantize_weights_mx4", "moe_expert_gemm_mx4", "Mx4Weights",
     "Workspace", "DEV_BAD_INDEX", "DEV_DUP_INDEX",
     "DEV_NONFINITE", "DEV_TIMEOUT", "LAYER_NUM_EVENTS", "EXPORTED_SYMBOLS", "build",
 ]
@@ -40,7 +42,9 @@ EXPORTED_SYMBOLS = ["moe_abi_version", "moe_capacity", "moe_workspace_size", "mo
                     "moe_permute_fp8", "moe_expert_ffn_fp8", "moe_layer_fwd_fp8",
                     "moe_combine_fp8", "moe_expert_ffn_gathered", "moe_host_workspace_size_fp8",
                     "moe_layer_fwd_host_fp8", "moe_ep_permute", "moe_ep_regroup",
-                    "moe_pipelined_workspace_size", "moe_layer_fwd_pipelined"]
+                    "moe_pipelined_workspace_size", "moe_layer_fwd_pipelined",
+                    "moe_route_grouped", "moe_route_grouped_bwd", "moe_quantize_rows_mx4",
+                    "moe_dequantize_rows_mx4", "moe_quantize_weights_mx4", "moe_expert_gemm_mx4"]
 
 
 class MoeError(RuntimeError):
@@ -57,6 +61,25 @@ class MoeShape(ctypes.Structure):
     @classmethod
     def make(cls, T, H, E, k, h, cf) -> "MoeShape":
         return cls(int(T), int(H), int(E), int(k), int(h), float(cf))
+
+
+class RouteConfig(ctypes.Structure):
+    """How moe_route_grouped scores and chooses (moe_route_config in the
+    header): score "softmax" or "sigmoid"; n_groups groups of consecutive
+    experts of which topk_groups are kept by the sum of their group_top
+    largest selection values; weights renormalised over the chosen and
+    multiplied by scale."""
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, score="softmax", n_groups=1, topk_groups=1, group_top=1, renormalize=True,
+             scale=1.0) -> "RouteConfig":
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError(f'score must be "softmax" or "sigmoid", got {score!r}')
+        return cls(int(score == "sigmoid"), int(n_groups), int(topk_groups), int(group_top),
+                   int(bool(renormalize)), float(scale))
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -130,6 +153,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_ep_permute.argtypes = [S, I64, I64, _P, I64] + [_P] * 10 + [ctypes.c_size_t, _P]
     lib.moe_ep_regroup.restype = ctypes.c_int
     lib.moe_ep_regroup.argtypes = [I64, I64, I64, I64, ctypes.c_int] + [_P] * 5
+    R = ctypes.POINTER(RouteConfig)
+    lib.moe_route_grouped.restype = ctypes.c_int
+    lib.moe_route_grouped.argtypes = [S, R] + [_P] * 9 + [ctypes.c_size_t, _P]
+    lib.moe_route_grouped_bwd.restype = ctypes.c_int
+    lib.moe_route_grouped_bwd.argtypes = [S, R] + [_P] * 7
+    lib.moe_quantize_rows_mx4.restype = ctypes.c_int
+    lib.moe_quantize_rows_mx4.argtypes = [I64, I64] + [_P] * 5
+    lib.moe_dequantize_rows_mx4.restype = ctypes.c_int
+    lib.moe_dequantize_rows_mx4.argtypes = [I64, I64] + [_P] * 4
+    lib.moe_quantize_weights_mx4.restype = ctypes.c_int
+    lib.moe_quantize_weights_mx4.argtypes = [I64, I64, I64] + [_P] * 4
+    lib.moe_expert_gemm_mx4.restype = ctypes.c_int
+    lib.moe_expert_gemm_mx4.argtypes = [I64] * 4 + [_P] * 5 + [ctypes.c_int] + [_P] * 3
     _lib = lib
     return lib
 
@@ -168,6 +204,7 @@ def _need_table(T: int, H: int, E: int, k: int, h: int) -> dict:
     A = T * k
     return {
         "x": T * H, "y": T * H, "gate": H * E, "gate_bias": E, "noise_u": T * E,
+        "select_bias": E, "grad_topk_w": A, "grad_aux": 1, "grad_logits": T * E,
         "logits": T * E, "logits_out": T * E, "scores_out": T * E,
         "topk_idx": A, "topk_w": A, "dest_row": A, "src_token": A,
         "routed_counts": E, "P": E, "kept_counts": E, "offsets": E + 1,
@@ -629,6 +666,131 @@ def moe_layer_fwd_fp8(shape, x, gate, gate_bias, q: Fp8Weights, y, aux=None, top
         a(P, torch.float32, "P"), a(kept_counts, torch.int32, "kept_counts"),
         a(offsets, torch.int32, "offsets"), a(dest_row, torch.int32, "dest_row"),
         a(dev_status, torch.int32, "dev_status"), wp, wn, _stream(stream), ev))
+
+
+# ---------------------------------------------------- grouped routing ----
+
+def moe_route_grouped(shape, cfg: RouteConfig, logits, select_bias, topk_idx, topk_w,
+                      routed_counts=None, P=None, aux=None, dev_status=None,
+                      ws: Workspace | None = None, stream=None):
+    """Routing of fp32 logits [T, E] with softmax or sigmoid scores, a
+    selection bias (or None) and groups of experts, as cfg says."""
+    a = _Args(shape)
+    s = a.shape
+    wp, wn = _ws(ws, s)
+    _check("moe_route_grouped", load_library().moe_route_grouped(
+        ctypes.byref(s), ctypes.byref(cfg), a(logits, torch.float32, "logits"),
+        a(select_bias, torch.float32, "select_bias"), a(topk_idx, torch.int32, "topk_idx"),
+        a(topk_w, torch.float32, "topk_w"), a(routed_counts, torch.int32, "routed_counts"),
+        a(P, torch.float32, "P"), a(aux, torch.float32, "aux"),
+        a(dev_status, torch.int32, "dev_status"), wp, wn, _stream(stream)))
+
+
+def moe_route_grouped_bwd(shape, cfg: RouteConfig, logits, topk_idx, grad_topk_w, grad_logits,
+                          grad_aux=None, routed_counts=None, stream=None):
+    """Gradient of moe_route_grouped with respect to the logits, from the
+    gradients of topk_w and (with routed_counts) of aux."""
+    a = _Args(shape)
+    s = a.shape
+    _check("moe_route_grouped_bwd", load_library().moe_route_grouped_bwd(
+        ctypes.byref(s), ctypes.byref(cfg), a(logits, torch.float32, "logits"),
+        a(topk_idx, torch.int32, "topk_idx"), a(grad_topk_w, torch.float32, "grad_topk_w"),
+        a(grad_aux, torch.float32, "grad_aux"), a(routed_counts, torch.int32, "routed_counts"),
+        a(grad_logits, torch.float32, "grad_logits"), _stream(stream)))
+
+
+# ------------------------------------------------- microscaled 4-bit ----
+
+def _mx4_rows(x_q, x_scale):
+    """rows and K of MX4 rows: x_q [rows, K/2], x_scale [ceil(K/128), rows, 4]."""
+    if x_q.dim() != 2:
+        raise ValueError("x_q must be [rows, K/2]")
+    rows, K = x_q.shape[0], 2 * x_q.shape[1]
+    if tuple(x_scale.shape) != ((K + 127) // 128, rows, 4):
+        raise ValueError(f"x_scale must be [ceil(K/128), rows, 4] = "
+                         f"[{(K + 127) // 128}, {rows}, 4], got {list(x_scale.shape)}")
+    return rows, K
+
+
+def _mx4_weights(Wq, w_scale):
+    """E, K and N of MX4 weights: Wq [E, N, K/2], w_scale [E, ceil(N/128),
+    ceil(K/128), 32, 4, 4]."""
+    if Wq.dim() != 3:
+        raise ValueError("Wq must be [E, N, K/2]")
+    E, N, K = Wq.shape[0], Wq.shape[1], 2 * Wq.shape[2]
+    want = (E, (N + 127) // 128, (K + 127) // 128, 32, 4, 4)
+    if tuple(w_scale.shape) != want:
+        raise ValueError(f"w_scale must be {list(want)}, got {list(w_scale.shape)}")
+    return E, K, N
+
+
+def moe_quantize_rows_mx4(x, x_q, x_scale, n_rows=None, stream=None):
+    """x [rows, K] bf16 -> x_q [rows, K/2] and x_scale [ceil(K/128), rows, 4]
+    (uint8). n_rows (int32, one element on the device): rows at or past it
+    are left out."""
+    rows, K = _mx4_rows(x_q, x_scale)
+    if tuple(x.shape) != (rows, K):
+        raise ValueError(f"x must be [rows, K] = [{rows}, {K}], got {list(x.shape)}")
+    _check("moe_quantize_rows_mx4", load_library().moe_quantize_rows_mx4(
+        rows, K, _ptr(x, torch.bfloat16, "x"), _ptr(n_rows, torch.int32, "n_rows", 1),
+        _ptr(x_q, torch.uint8, "x_q"), _ptr(x_scale, torch.uint8, "x_scale"), _stream(stream)))
+
+
+def moe_dequantize_rows_mx4(x_q, x_scale, x, stream=None):
+    """MX4 rows -> x [rows, K] bf16, the values they stand for."""
+    rows, K = _mx4_rows(x_q, x_scale)
+    if tuple(x.shape) != (rows, K):
+        raise ValueError(f"x must be [rows, K] = [{rows}, {K}], got {list(x.shape)}")
+    _check("moe_dequantize_rows_mx4", load_library().moe_dequantize_rows_mx4(
+        rows, K, _ptr(x_q, torch.uint8, "x_q"), _ptr(x_scale, torch.uint8, "x_scale"),
+        _ptr(x, torch.bfloat16, "x"), _stream(stream)))
+
+
+def moe_quantize_weights_mx4(W, Wq, w_scale, stream=None):
+    """W [E, K, N] bf16 -> Wq [E, N, K/2] and w_scale [E, ceil(N/128),
+    ceil(K/128), 32, 4, 4] (uint8)."""
+    E, K, N = _mx4_weights(Wq, w_scale)
+    if tuple(W.shape) != (E, K, N):
+        raise ValueError(f"W must be [E, K, N] = [{E}, {K}, {N}], got {list(W.shape)}")
+    _check("moe_quantize_weights_mx4", load_library().moe_quantize_weights_mx4(
+        E, K, N, _ptr(W, torch.bfloat16, "W"), _ptr(Wq, torch.uint8, "Wq"),
+        _ptr(w_scale, torch.uint8, "w_scale"), _stream(stream)))
+
+
+class Mx4Weights:
+    """The expert weights W1 [E,H,h] and W2 [E,h,H] in the MX4 form: W1q
+    [E,h,H/2], W2q [E,H,h/2] and their block scales w1_scale, w2_scale."""
+
+    def __init__(self, W1, W2, stream=None):
+        def one(W):
+            E, K, N = W.shape
+            q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device)
+            s = torch.empty((E, (N + 127) // 128, (K + 127) // 128, 32, 4, 4), dtype=torch.uint8,
+                            device=W.device)
+            moe_quantize_weights_mx4(W, q, s, stream)
+            return q, s
+
+        self.W1q, self.w1_scale = one(W1)
+        self.W2q, self.w2_scale = one(W2)
+
+
+def moe_expert_gemm_mx4(x_q, x_scale, offsets, Wq, w_scale, out, gelu=False, dev_status=None,
+                        stream=None):
+    """out [rows, N] bf16 = the rows' products with their expert's weights
+    (segments offsets [E+1]), through GELU-tanh if gelu. dev_status (int32,
+    one element) is required."""
+    rows, K = _mx4_rows(x_q, x_scale)
+    E, Kw, N = _mx4_weights(Wq, w_scale)
+    if K != Kw:
+        raise ValueError(f"x_q has K = {K}, Wq has K = {Kw}")
+    if tuple(out.shape) != (rows, N):
+        raise ValueError(f"out must be [rows, N] = [{rows}, {N}], got {list(out.shape)}")
+    _check("moe_expert_gemm_mx4", load_library().moe_expert_gemm_mx4(
+        E, rows, K, N, _ptr(x_q, torch.uint8, "x_q"), _ptr(x_scale, torch.uint8, "x_scale"),
+        _ptr(offsets, torch.int32, "offsets", E + 1), _ptr(Wq, torch.uint8, "Wq"),
+        _ptr(w_scale, torch.uint8, "w_scale"), 1 if gelu else 0,
+        _ptr(out, torch.bfloat16, "out"), _ptr(dev_status, torch.int32, "dev_status", 1),
+        _stream(stream)))
 
 
 # ------------------------------------------------- expert parallelism ----

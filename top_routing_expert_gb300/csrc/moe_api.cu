@@ -68,6 +68,9 @@ struct Ws {
   int32_t* kept;
   int32_t* offsets;
   int32_t* cap;  // expert parallelism: this rank's capacity per expert
+  int32_t* grouped_cnt;   // grouped routing: [E][blocks] counts, their prefix, sums of p
+  int32_t* grouped_base;
+  float* grouped_p;
   uint32_t* status;
   uint32_t* ticket;
   int32_t* topk_idx;
@@ -137,6 +140,10 @@ size_t layout(const Dims& d, uint8_t* base, Ws* w, bool fp8 = false) {
   v.x_perm = static_cast<uint16_t*>(take(A * d.H * 2));
   v.act = static_cast<uint16_t*>(take(A * d.h * 2));
   v.y_perm = static_cast<uint16_t*>(take(A * d.H * 2));
+  const size_t EB = static_cast<size_t>(d.E) * route_grouped_blocks(d.T, d.E);
+  v.grouped_cnt = static_cast<int32_t*>(take(EB * 4));
+  v.grouped_base = static_cast<int32_t*>(take(EB * 4));
+  v.grouped_p = static_cast<float*>(take(EB * 4));
   v.x_scale = nullptr;
   v.act_q = nullptr;
   v.act_scale = nullptr;
@@ -273,14 +280,16 @@ bool tmap_bf16_experts(CUtensorMap* m, const void* ptr, uint64_t N, uint64_t K, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A byte (e4m3) row-major matrix [outer, inner] in 128 x 128 boxes (one
-// 128-byte swizzle row of K per box row); inner must be a multiple of 16.
-bool tmap_u8_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer) {
+// A byte (e4m3, or two 4-bit codes) row-major matrix [outer, inner] in boxes
+// of 128 bytes x box_outer rows (one 128-byte swizzle row of K per box row);
+// inner must be a multiple of 16.
+bool tmap_u8_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
+                uint32_t box_outer = 128) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t gdim[2] = {inner, outer};
   const cuuint64_t gstride[1] = {inner};
-  const cuuint32_t box[2] = {128, 128};
+  const cuuint32_t box[2] = {128, box_outer};
   const cuuint32_t estride[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), gdim, gstride, box,
             estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1318,6 +1327,198 @@ moe_status moe_layer_fwd_host_fp8(const moe_shape* s, int64_t n_micro,
   const Fp8Weights q{W1q, w1_scale, W2q, w2_scale};
   return layer_fwd_host(s, n_micro, x_host, y_host, aux_host, gate, gate_bias, nullptr, nullptr,
                         &q, dev_status, ws, ws_bytes, streams, events);
+}
+
+// ------------------------------------------------------ grouped routing ----
+
+static moe_status check_route_config(const moe_shape* s, const moe_route_config* c) {
+  if (c == nullptr) return MOE_ERR_NULL;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
+  if (c->n_groups < 1 || s->E % c->n_groups != 0) return MOE_ERR_SHAPE;
+  if (c->n_groups > 32) return MOE_ERR_UNSUPPORTED;
+  const int64_t per_group = s->E / c->n_groups;
+  if (c->topk_groups < 1 || c->topk_groups > c->n_groups) return MOE_ERR_SHAPE;
+  if (c->group_top < 1 || c->group_top > 2 || c->group_top > per_group) return MOE_ERR_SHAPE;
+  if (s->top_k > c->topk_groups * per_group) return MOE_ERR_SHAPE;
+  if ((c->renormalize != 0 && c->renormalize != 1) || !isfinite(c->scale)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+moe_status moe_route_grouped(const moe_shape* s, const moe_route_config* cfg, const float* logits,
+                             const float* select_bias, int32_t* topk_idx, float* topk_w,
+                             int32_t* routed_counts, float* P, float* aux, uint32_t* dev_status,
+                             void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_shape(s));
+  MOE_TRY(check_route_config(s, cfg));
+  MOE_REQUIRE(logits);
+  MOE_REQUIRE(topk_idx);
+  MOE_REQUIRE(topk_w);
+  MOE_OPTIONAL(select_bias);
+  MOE_OPTIONAL(routed_counts);
+  MOE_OPTIONAL(P);
+  MOE_OPTIONAL(aux);
+  MOE_OPTIONAL(dev_status);
+  const Dims d = dims_of(s);
+  Ws w;
+  MOE_TRY(carve(s, d, ws, ws_bytes, &w));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d.T == 0) {
+    if (routed_counts) MOE_CUDA(cudaMemsetAsync(routed_counts, 0, sizeof(int32_t) * d.E, st));
+    if (P) MOE_CUDA(cudaMemsetAsync(P, 0, sizeof(float) * d.E, st));
+    if (aux) MOE_CUDA(cudaMemsetAsync(aux, 0, sizeof(float), st));
+    return MOE_OK;
+  }
+  const bool stats = routed_counts != nullptr || P != nullptr || aux != nullptr;
+  GroupedArgs a;
+  a.T = d.T;
+  a.E = d.E;
+  a.k = d.k;
+  a.score = cfg->score;
+  a.n_groups = cfg->n_groups;
+  a.topk_groups = cfg->topk_groups;
+  a.group_top = cfg->group_top;
+  a.renormalize = cfg->renormalize;
+  a.scale = cfg->scale;
+  a.logits = logits;
+  a.bias = select_bias;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.tile_cnt = stats ? w.grouped_cnt : nullptr;
+  a.ppart = w.grouped_p;
+  a.ticket = w.ticket;
+  a.dev_status = dev_status ? dev_status : w.status;
+  MOE_CUDA(launch_route_grouped(a, st));
+  if (!stats) return MOE_OK;
+  ScanArgs sc;
+  sc.T = d.T;
+  sc.E = d.E;
+  sc.k = d.k;
+  sc.n_tiles = route_grouped_blocks(d.T, d.E);
+  sc.C = d.C;
+  sc.tile_cnt = w.grouped_cnt;
+  sc.tile_base = w.grouped_base;
+  sc.ppart = w.grouped_p;
+  sc.routed = routed_counts ? routed_counts : w.routed;
+  sc.P = P ? P : w.P;
+  sc.aux = aux;
+  sc.kept = nullptr;
+  sc.offsets = nullptr;
+  sc.ticket = w.ticket;
+  MOE_CUDA(launch_scan(sc, st));
+  return MOE_OK;
+}
+
+moe_status moe_route_grouped_bwd(const moe_shape* s, const moe_route_config* cfg,
+                                 const float* logits, const int32_t* topk_idx,
+                                 const float* grad_topk_w, const float* grad_aux,
+                                 const int32_t* routed_counts, float* grad_logits, void* stream) {
+  MOE_TRY(check_shape(s));
+  MOE_TRY(check_route_config(s, cfg));
+  MOE_REQUIRE(logits);
+  MOE_REQUIRE(topk_idx);
+  MOE_REQUIRE(grad_topk_w);
+  MOE_REQUIRE(grad_logits);
+  MOE_OPTIONAL(grad_aux);
+  if (grad_aux != nullptr) MOE_REQUIRE(routed_counts);
+  if (s->T == 0) return MOE_OK;
+  GroupedBwdArgs a;
+  a.T = static_cast<int>(s->T);
+  a.E = static_cast<int>(s->E);
+  a.k = static_cast<int>(s->top_k);
+  a.score = cfg->score;
+  a.renormalize = cfg->renormalize;
+  a.scale = cfg->scale;
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.grad_w = grad_topk_w;
+  a.grad_aux = grad_aux;
+  a.routed = routed_counts;
+  a.grad_logits = grad_logits;
+  MOE_CUDA(launch_route_grouped_bwd(a, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+// ------------------------------------------------------ microscaled 4-bit ----
+
+static moe_status check_mx4(int64_t rows, int64_t K) {
+  if (rows < 0 || K <= 0) return MOE_ERR_SHAPE;
+  if (K % 64 != 0 || K > kMaxDim || rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_quantize_rows_mx4(int64_t rows, int64_t K, const moe_bf16* x, const int32_t* n_rows,
+                                 uint8_t* x_q, uint8_t* x_scale, void* stream) {
+  MOE_TRY(check_mx4(rows, K));
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(x);
+  MOE_REQUIRE(x_q);
+  MOE_REQUIRE(x_scale);
+  if (n_rows != nullptr && (reinterpret_cast<uintptr_t>(n_rows) & 3u) != 0) return MOE_ERR_ALIGN;
+  MOE_CUDA(launch_quantize_rows_mx4(x, x_q, x_scale, n_rows, rows, static_cast<int>(K), num_sms(),
+                                    static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_dequantize_rows_mx4(int64_t rows, int64_t K, const uint8_t* x_q,
+                                   const uint8_t* x_scale, moe_bf16* x, void* stream) {
+  MOE_TRY(check_mx4(rows, K));
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(x_q);
+  MOE_REQUIRE(x_scale);
+  MOE_REQUIRE(x);
+  MOE_CUDA(launch_dequantize_rows_mx4(x_q, x_scale, x, rows, static_cast<int>(K), num_sms(),
+                                      static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_quantize_weights_mx4(int64_t E, int64_t K, int64_t N, const moe_bf16* W,
+                                    uint8_t* Wq, uint8_t* w_scale, void* stream) {
+  if (E <= 0 || K <= 0 || N <= 0) return MOE_ERR_SHAPE;
+  if (E > kMaxExperts || K % 64 != 0 || N % 64 != 0 || K > kMaxDim || N > kMaxDim)
+    return MOE_ERR_UNSUPPORTED;
+  MOE_REQUIRE(W);
+  MOE_REQUIRE(Wq);
+  MOE_REQUIRE(w_scale);
+  MOE_CUDA(launch_quantize_weights_mx4(W, Wq, w_scale, static_cast<int>(E), static_cast<int>(K),
+                                       static_cast<int>(N), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N, const uint8_t* x_q,
+                               const uint8_t* x_scale, const int32_t* offsets, const uint8_t* Wq,
+                               const uint8_t* w_scale, int gelu, moe_bf16* D, uint32_t* dev_status,
+                               void* stream) {
+  if (E <= 0 || N <= 0) return MOE_ERR_SHAPE;
+  MOE_TRY(check_mx4(rows, K));
+  if (E > kMaxExperts || N % 64 != 0 || N > kMaxDim) return MOE_ERR_UNSUPPORTED;
+  if (gelu != 0 && gelu != 1) return MOE_ERR_SHAPE;
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(x_q);
+  MOE_REQUIRE(x_scale);
+  MOE_REQUIRE(offsets);
+  MOE_REQUIRE(Wq);
+  MOE_REQUIRE(w_scale);
+  MOE_REQUIRE(D);
+  MOE_REQUIRE(dev_status);
+  Mx4GemmArgs a;
+  a.offsets = offsets;
+  a.E = static_cast<int>(E);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.rows = static_cast<int>(rows);
+  a.x_scale = x_scale;
+  a.w_scale = w_scale;
+  a.D = D;
+  a.gelu = gelu;
+  a.tile_tokens = mx4_tile_tokens(rows, a.E);
+  a.stages = 0;
+  a.dev_status = dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  CUtensorMap tm_w, tm_x;
+  if (!tmap_u8_2d(&tm_w, Wq, K / 2, static_cast<uint64_t>(E) * N)) return MOE_ERR_CUDA;
+  if (!tmap_u8_2d(&tm_x, x_q, K / 2, rows, a.tile_tokens)) return MOE_ERR_CUDA;
+  MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, a, num_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
 }
 
 }  // extern "C"

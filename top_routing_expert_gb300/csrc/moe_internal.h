@@ -93,6 +93,34 @@ struct CombineArgs {
   uint16_t* y;
 };
 
+// Grouped routing (csrc/moe_route_grouped.cu): its blocks' partial counts and
+// probability sums are [E][blocks], as the routing tiles' are.
+constexpr int kGroupedMaxBlocks = 608;
+struct GroupedArgs {
+  int T, E, k;
+  int score, n_groups, topk_groups, group_top, renormalize;
+  float scale;
+  const float* logits;   // [T,E]
+  const float* bias;     // [E] or nullptr
+  int32_t* topk_idx;     // [T,k]
+  float* topk_w;         // [T,k]
+  int32_t* tile_cnt;     // [E][blocks] or nullptr (no statistics)
+  float* ppart;          // [E][blocks]
+  uint32_t* ticket;      // reset to 0 (used by the scan)
+  uint32_t* dev_status;
+};
+struct GroupedBwdArgs {
+  int T, E, k;
+  int score, renormalize;
+  float scale;
+  const float* logits;     // [T,E]
+  const int32_t* topk_idx; // [T,k]
+  const float* grad_w;     // [T,k]
+  const float* grad_aux;   // [1] or nullptr
+  const int32_t* routed;   // [E], with grad_aux
+  float* grad_logits;      // [T,E]
+};
+
 // TMEM columns the router allocates: a power of two >= 32 covering E_pad.
 __host__ __device__ inline int route_tmem_cols(int E_pad) {
   int c = 32;
@@ -115,6 +143,20 @@ struct GemmArgs {
   const int32_t* a_rows;   // optional: A row r is row a_rows[r] of the A tensor (a gather,
   int a_src_rows;          //   by TMA, from a tensor of a_src_rows rows); CTA-pair kernel
   int stages;              // CTA-pair kernel: pipeline depth (set by its launcher)
+  uint32_t* dev_status;
+  uint64_t timeout_ns;
+};
+
+// 4-bit grouped product (csrc/moe_gemm_mx4.cu).
+struct Mx4GemmArgs {
+  const int32_t* offsets;   // [E+1] row segments
+  int E, K, N, rows;
+  const uint8_t* x_scale;   // [ceil(K/128)][rows][4] e8m0
+  const uint8_t* w_scale;   // [E][ceil(N/128)][ceil(K/128)][512] e8m0
+  uint16_t* D;              // [rows, N] bf16
+  int gelu;
+  int tile_tokens;
+  int stages;               // set by the launcher
   uint32_t* dev_status;
   uint64_t timeout_ns;
 };
@@ -177,6 +219,20 @@ size_t route_smem_bytes(int E_pad, int stages, int gate_mode, int kbps);
 cudaError_t launch_route_gemm(const CUtensorMap& tm_x, const CUtensorMap& tm_gate,
                               const RouteArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_route_logits(const RouteArgs& a, cudaStream_t st);
+int route_grouped_blocks(int T, int E);
+cudaError_t launch_route_grouped(const GroupedArgs& a, cudaStream_t st);
+cudaError_t launch_route_grouped_bwd(const GroupedBwdArgs& a, cudaStream_t st);
+cudaError_t launch_quantize_rows_mx4(const uint16_t* x, uint8_t* q, uint8_t* scale,
+                                     const int32_t* n_rows, int64_t rows, int K, int num_sms,
+                                     cudaStream_t st);
+cudaError_t launch_dequantize_rows_mx4(const uint8_t* q, const uint8_t* scale, uint16_t* x,
+                                       int64_t rows, int K, int num_sms, cudaStream_t st);
+cudaError_t launch_quantize_weights_mx4(const uint16_t* W, uint8_t* Wq, uint8_t* w_scale, int E,
+                                        int K, int N, cudaStream_t st);
+// Token tile of the 4-bit grouped product: a multiple of 16, at most 240.
+int mx4_tile_tokens(int64_t rows, int E);
+cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                                   const Mx4GemmArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_rank(const RankArgs& a, cudaStream_t st);
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_gather(const GatherArgs& a, int num_sms, cudaStream_t st);
