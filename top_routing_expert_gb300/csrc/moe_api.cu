@@ -296,6 +296,21 @@ bool tmap_u8_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A matrix [outer, inner] of 32-bit words read in boxes of whole rows, as they
+// lie in memory (no swizzle); inner at most 256 and a multiple of 4.
+bool tmap_u32_rows(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
+                   uint32_t box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t gdim[2] = {inner, outer};
+  const cuuint64_t gstride[1] = {inner * 4};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(inner), box_outer};
+  const cuuint32_t estride[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), gdim, gstride, box,
+            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------------- stages ----
 
 struct RouteOut {
@@ -1514,10 +1529,16 @@ moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N, co
   a.stages = 0;
   a.dev_status = dev_status;
   a.timeout_ns = wait_timeout_ns();
-  CUtensorMap tm_w, tm_x;
+  const bool pair = mx4_use_pair(rows, a.E);
+  CUtensorMap tm_w, tm_x, tm_ws;
   if (!tmap_u8_2d(&tm_w, Wq, K / 2, static_cast<uint64_t>(E) * N)) return MOE_ERR_CUDA;
-  if (!tmap_u8_2d(&tm_x, x_q, K / 2, rows, a.tile_tokens)) return MOE_ERR_CUDA;
-  MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, a, num_sms(), static_cast<cudaStream_t>(stream)));
+  if (!tmap_u8_2d(&tm_x, x_q, K / 2, rows, pair ? a.tile_tokens / 2 : a.tile_tokens))
+    return MOE_ERR_CUDA;
+  // the 512-byte blocks of the weights' scales, two at a time
+  if (!tmap_u32_rows(&tm_ws, w_scale, 128, static_cast<uint64_t>(E) * ((N + 127) / 128) * ((K + 127) / 128), 2))
+    return MOE_ERR_CUDA;
+  MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, tm_ws, a, pair, num_sms(),
+                                  static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -12,12 +12,18 @@
 //
 // Scales reach TMEM by tcgen05.cp from shared memory, 128 rows x 4 scales (512
 // bytes) at a time. Those of the weights lie in that order in memory and come
-// by bulk copies; those of the tokens start at any row (a segment need not
-// begin at a multiple of anything), so one warp copies them word by word
-// (cp.async, 4 bytes, coalesced in memory) to their places.
+// by TMA; those of the tokens start at any row (a segment need not begin at a
+// multiple of anything), so two warps fetch them into registers, coalesced and
+// stages ahead, and store them word by word in their places.
 //
-// Roles (256 threads): warp 0 = TMA producer, warp 1 = UMMA issuer, warp 2 =
-// token scales, warp 3 = TMEM allocation, warps 4-7 = epilogue.
+// Roles (384 threads): warp 0 = TMA producer, warp 1 = UMMA issuer and TMEM
+// allocation, warps 2-3 = token scales, warps 4-11 = epilogue (two to a TMEM
+// lane quadrant, taking chunks of 32 tokens in turn).
+//
+// Few rows per expert run on single CTAs (M = 128), more on CTA pairs
+// (cta_group::2, M = 256: each CTA holds its 128 columns of W and half of the
+// tile's tokens), which halves the tokens' share of L2 and shared-memory
+// traffic.
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -31,20 +37,64 @@ constexpr int kMaxTokens = 240;          // two accumulators of 240 columns + sc
 constexpr uint32_t kWBytes = kBM * 128;  // 16 KB
 constexpr uint32_t kWScaleBytes = 1024;  // 2 x 512
 constexpr int kMaxStages = 10;
-constexpr int kThreads = 256;
+constexpr int kScaleWarps = 2;
+constexpr int kTokenWords = (kMaxTokens + 31) / 32;  // scale words per lane, block and tile
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSfW = 480;  // 2 x 4 columns
 constexpr uint32_t kTmemSfX = 488;  // 2 x 8 columns
 
 __host__ __device__ constexpr uint32_t x_scale_blocks(int nt) { return static_cast<uint32_t>(nt + 127) / 128; }
-__host__ __device__ constexpr uint32_t stage_bytes(int nt) {
-  return kWBytes + static_cast<uint32_t>(nt) * 128 + kWScaleBytes + 2 * 512 * x_scale_blocks(nt);
+__host__ __device__ constexpr uint32_t stage_bytes(int nt, bool pair) {
+  return kWBytes + static_cast<uint32_t>(nt) * (pair ? 64 : 128) + kWScaleBytes +
+         2 * 512 * x_scale_blocks(nt);
 }
 
 __device__ __forceinline__ float gelu_tanh_f(float u) {
   // 0.5 u (1 + tanh(z)) = u / (1 + exp(-2 z)),  z = sqrt(2/pi) (u + 0.044715 u^3)
   const float z2 = 1.5957691216057308f * fmaf(0.044715f * u, u * u, u);
   return __fdividef(u, 1.0f + __expf(-z2));
+}
+
+// One warp's 32 output columns x up to 32 tokens (n of them valid) from TMEM
+// columns taddr.. to D. The accumulator has output columns in lanes and tokens
+// in columns; it is read as 8x8 fragments, which go transposed through 2 KB of
+// the warp's shared memory (16-byte pieces, XOR-swizzled so that neither side
+// conflicts) and leave as 64-byte row pieces, 16 bytes a lane.
+__device__ __forceinline__ void store_chunk(uint32_t taddr, uint32_t stage, uint16_t* d, int pitch,
+                                            int n, int gelu, int lane) {
+  uint32_t a[16], b[16];
+  tmem_ld_16x256b_x4(taddr, a);
+  tmem_ld_16x256b_x4(taddr + (16u << 16), b);
+  tmem_ld_wait();
+  if (gelu) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      a[i] = __float_as_uint(gelu_tanh_f(__uint_as_float(a[i])));
+      b[i] = __float_as_uint(gelu_tanh_f(__uint_as_float(b[i])));
+    }
+  }
+  auto pack = [](uint32_t lo, uint32_t hi) {
+    return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+  };
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t t = 8u * g + (lane & 7), c = static_cast<uint32_t>(lane) >> 3;
+    stmatrix_x4_trans(stage + 64u * t + 16u * (c ^ ((t >> 1) & 3u)), pack(a[4 * g], a[4 * g + 1]),
+                      pack(a[4 * g + 2], a[4 * g + 3]), pack(b[4 * g], b[4 * g + 1]),
+                      pack(b[4 * g + 2], b[4 * g + 3]));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t = 8u * i + (static_cast<uint32_t>(lane) >> 2), c = lane & 3;
+    const uint4 v = ld_shared_v4(stage + 64u * t + 16u * (c ^ ((t >> 1) & 3u)));
+    if (static_cast<int>(t) < n)
+      st_global_cs_v4(d + static_cast<size_t>(t) * pitch + 8 * c, v);
+  }
+  __syncwarp();
 }
 
 struct Tile {
@@ -54,7 +104,7 @@ struct Tile {
 // Tile order: groups of 8 token tiles, all column tiles of a group before the
 // next group, token tiles innermost (they share the weights in L2).
 __device__ __forceinline__ Tile decode(int L, const int* prefix, const int* offs, int E, int total_t,
-                                       int n_tiles_n, int nt) {
+                                       int n_tiles_n, int nt, int bm = kBM) {
   constexpr int group = 8;
   const int per_group = group * n_tiles_n;
   const int g = L / per_group;
@@ -71,52 +121,14 @@ __device__ __forceinline__ Tile decode(int L, const int* prefix, const int* offs
   t.e = lo;
   t.row0 = offs[lo] + (tt - prefix[lo]) * nt;
   t.row_end = offs[lo + 1];
-  t.n0 = (r / gsz) * kBM;
+  t.n0 = (r / gsz) * bm;
   return t;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    expert_gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_w,
-                           const __grid_constant__ CUtensorMap tm_x, Mx4GemmArgs p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_up_1024(smem_raw);
-  const int nst = p.stages, NT = p.tile_tokens;
-  const uint32_t sb = stage_bytes(NT);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(nst) * sb);
-  uint64_t* empty = full + nst;
-  uint64_t* tfull = empty + nst;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  uint32_t* abort_flag = tmem_slot + 1;
-  int* offs = reinterpret_cast<int*>(abort_flag + 1);  // [E+1]
-  int* prefix = offs + (p.E + 1);                      // [E+1]
-
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int E = p.E;
-  if (warp == 3) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
-  if (warp == 2 && lane == 0) {
-    for (int s = 0; s < nst; ++s) {
-      mbar_init(&full[s], 1 + 32);  // the producer's bytes and the scale warp's lanes
-      mbar_init(&empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 128);
-    }
-    mbar_init(drain, 1);
-    *abort_flag = 0u;
-    fence_barrier_init();
-  }
-  if (warp == 1 && lane == 0) {
-    tma_prefetch_desc(&tm_w);
-    tma_prefetch_desc(&tm_x);
-  }
-  grid_dependency_wait();
-  grid_launch_dependents();
+// Segment offsets, held to the buffer and non-decreasing, and the prefix of the
+// experts' token tiles. All threads; followed by a barrier of the caller's.
+__device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, int* prefix, int nt) {
+  const int tid = threadIdx.x, lane = tid & 31, E = p.E;
   for (int i = tid; i <= E; i += kThreads) {
     const int v = p.offsets[i];
     offs[i] = v < 0 ? 0 : (v > p.rows ? p.rows : v);  // rows outside the buffer are never touched
@@ -125,11 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0)
     for (int i = 1; i <= E; ++i) offs[i] = offs[i] < offs[i - 1] ? offs[i - 1] : offs[i];
   __syncthreads();
-  if (warp == 0) {
+  if (tid < 32) {
     int carry = 0;
     for (int b = 0; b < E; b += 32) {
       const int e = b + lane;
-      const int n = e < E ? (offs[e + 1] - offs[e] + NT - 1) / NT : 0;
+      const int n = e < E ? (offs[e + 1] - offs[e] + nt - 1) / nt : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -141,17 +153,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) prefix[E] = carry;
   }
+}
+
+// kPair: a tile is 256 output columns (128 per CTA of a cluster pair) x up to
+// tile_tokens tokens; each CTA loads half of the tokens' codes and all of their
+// scales, and the leader (rank 0) issues the UMMAs, so stage barriers of both
+// CTAs' copies live there. Otherwise a tile is 128 columns of one CTA.
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_w,
+                           const __grid_constant__ CUtensorMap tm_x,
+                           const __grid_constant__ CUtensorMap tm_ws, Mx4GemmArgs p) {
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kTileN = kBM * kCtas;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_up_1024(smem_raw);
+  const int nst = p.stages, NT = p.tile_tokens;
+  const uint32_t sb = stage_bytes(NT, kPair);
+  const uint32_t xbytes = static_cast<uint32_t>(NT) * 128 / kCtas;  // a multiple of 1024
+  uint8_t* staging = smem + static_cast<size_t>(nst) * sb;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kChunkBytes);
+  uint64_t* empty = full + nst;
+  uint64_t* tfull = empty + nst;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint64_t* xbar = drain + 1;  // pair leader: the peer's count of loaded stages has arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
+  uint32_t* abort_flag = tmem_slot + 1;
+  uint32_t* peer_issued = abort_flag + 1;
+  int* offs = reinterpret_cast<int*>(peer_issued + 1);  // [E+1]
+  int* prefix = offs + (p.E + 1);                       // [E+1]
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = p.E;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
+  if (warp == 1) {
+    if constexpr (kPair) {
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  if (warp == 2 && lane == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(&full[s], 1 + kCtas * kScaleWarps);  // the bytes, and the scale warps
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kCtas * 32 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(xbar, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_ws);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  load_offsets(p, offs, prefix, NT);
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // barriers initialised before any remote use
   tc_fence_after();
 
   const uint32_t tmem_base = *tmem_slot;
   const int total_t = prefix[E];
-  const int n_tiles_n = (p.N + kBM - 1) / kBM;
+  const int n_tiles_n = (p.N + kTileN - 1) / kTileN;
   const int total = total_t * n_tiles_n;
   const int nk = (p.K + kStageK - 1) / kStageK;   // stages per tile
   const int nkb = (p.K + 127) / 128;              // 128-deep scale blocks
   const WaitCtl wc{abort_flag, p.dev_status, p.timeout_ns};
+  // A wait that gives up stops the peer CTA too.
+  const uint32_t peer_abort = kPair ? mapa_shared(smem_u32(abort_flag), rank ^ 1u) : 0u;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_wait(bar, parity, wc)) return true;
+    if constexpr (kPair) st_u32_cluster(peer_abort, 1u);
+    return false;
+  };
+  const uint32_t full0 = kPair ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -160,23 +248,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int issued = 0;
       bool aborted = false;
-      for (int L = blockIdx.x; L < total && !aborted; L += gridDim.x) {
-        const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT);
-        const uint8_t* ws = p.w_scale +
-            (static_cast<size_t>(c.e) * n_tiles_n + c.n0 / kBM) * nkb * 512;
+      const uint32_t bytes = kWBytes + xbytes + kWScaleBytes;  // per CTA and stage
+      for (int L = unit; L < total && !aborted; L += units) {
+        const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
+        const int half = ((min(NT, c.row_end - c.row0) + 15) & ~15) >> 1;
+        const int n0 = c.n0 + static_cast<int>(rank) * kBM;
+        const int x_row = c.row0 + (kPair ? static_cast<int>(rank) * half : 0);
+        // scale blocks of this CTA's 128 columns (past N or K: others', unused)
+        const int s_row = (c.e * ((p.N + kBM - 1) / kBM) + n0 / kBM) * nkb;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+          if (!wait(&empty[stage], phase ^ 1u)) {
             aborted = true;
             break;
           }
           uint8_t* sw = smem + static_cast<size_t>(stage) * sb;
           uint8_t* sx = sw + kWBytes;
-          uint8_t* ssw = sx + NT * 128;
-          const uint32_t sc = 512u * static_cast<uint32_t>(min(2, nkb - 2 * kb));
-          mbar_arrive_expect_tx(&full[stage], kWBytes + static_cast<uint32_t>(NT) * 128 + sc);
-          tma_load_2d(sw, &tm_w, &full[stage], kb * 128, c.e * p.N + c.n0);
-          tma_load_2d(sx, &tm_x, &full[stage], kb * 128, c.row0);
-          bulk_load(ssw, ws + static_cast<size_t>(kb) * 1024, sc, &full[stage]);
+          if (leader) mbar_arrive_expect_tx(&full[stage], kCtas * bytes);
+          if constexpr (kPair) {
+            const uint32_t bar = full0 + 8u * static_cast<uint32_t>(stage);
+            tma_load_2d_pair(sw, &tm_w, bar, kb * 128, c.e * p.N + n0);
+            tma_load_2d_pair(sx, &tm_x, bar, kb * 128, x_row);
+            tma_load_2d_pair(sx + xbytes, &tm_ws, bar, 0, s_row + 2 * kb);
+          } else {
+            tma_load_2d(sw, &tm_w, &full[stage], kb * 128, c.e * p.N + n0);
+            tma_load_2d(sx, &tm_x, &full[stage], kb * 128, x_row);
+            tma_load_2d(sx + xbytes, &tm_ws, &full[stage], 0, s_row + 2 * kb);
+          }
           ++issued;
           if (++stage == nst) {
             stage = 0;
@@ -184,143 +281,221 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (aborted) {
-        // copies in flight land before the CTA exits
-        int s = stage;
-        uint32_t ph = phase;
-        for (int d = 0; d < nst && d < issued; ++d) {
-          if (--s < 0) {
-            s = nst - 1;
-            ph ^= 1u;
+      // Every load issued lands before any CTA can exit. In a pair the peer
+      // reports how many stages it loaded, and the leader makes the byte
+      // accounting of each stage still in flight whole before it waits for it
+      // (after an abort one CTA may have loaded stages that the other did not).
+      if (kPair && !leader) {
+        st_async_u32_cluster(mapa_shared(smem_u32(peer_issued), 0), static_cast<uint32_t>(issued),
+                             mapa_shared(smem_u32(xbar), 0));
+      } else {
+        int theirs = issued;
+        if constexpr (kPair) {
+          mbar_arrive_expect_tx(xbar, 4);
+          if (mbar_wait_drain(xbar, 0, p.timeout_ns + kDrainLimitNs)) {
+            // the peer cannot load more than a ring ahead of what this CTA armed
+            theirs = min(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(peer_issued)),
+                         issued + nst);
+          } else {
+            atomicOr(p.dev_status, MOE_DEV_TIMEOUT);
           }
-          mbar_wait_drain(&full[s], ph, kDrainLimitNs);
+        }
+        const int hi = max(issued, theirs);
+        for (int i = max(0, hi - nst); i < hi; ++i) {
+          uint64_t* b = &full[i % nst];
+          if (i >= issued)
+            mbar_arrive_expect_tx(b, bytes);  // armed here for the peer's half alone
+          else if (i >= theirs)
+            mbar_complete_tx(b, bytes);       // the peer's half will never come
+          mbar_wait_drain(b, static_cast<uint32_t>(i / nst) & 1u, kDrainLimitNs);
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (leader) {
       // ------------------------------------------------- UMMA issuer ----
+      // The whole warp runs this converged and one elected lane issues: the
+      // descriptors then stay in uniform registers. From a branch on lane 0
+      // each tcgen05 instruction took about 44 clocks to issue, ten a stage
+      // against the 480 clocks of its four UMMAs; elected, about 10.
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool aborted = false;
-      for (int L = blockIdx.x; L < total && !aborted; L += gridDim.x) {
-        const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT);
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t w_desc = smem_desc_sw128(s0, 16u, 1024u);
+      const uint64_t x_desc = smem_desc_sw128(s0 + kWBytes, 16u, 1024u);
+      const uint64_t ws_desc = smem_desc_plain(s0 + kWBytes + xbytes, 128u);
+      const uint64_t xs_desc = smem_desc_plain(s0 + kWBytes + xbytes + kWScaleBytes, 128u);
+      const uint32_t sf_w = tmem_base + kTmemSfW, sf_x = tmem_base + kTmemSfX;
+      const bool wide = NT > 128;  // two blocks of token scales
+      for (int L = unit; L < total && !aborted; L += units) {
+        const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
         const int n_tok = min(NT, c.row_end - c.row0);
-        const uint32_t idesc = idesc_mxf4_e8m0(kBM, static_cast<uint32_t>((n_tok + 15) & ~15));
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) break;
+        const uint32_t idesc = idesc_mxf4_e8m0(kTileN, static_cast<uint32_t>((n_tok + 15) & ~15));
+        if (!__all_sync(0xffffffffu, wait(&tempty[acc], acc_phase ^ 1u))) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kMaxTokens);
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&full[stage], phase, wc)) {
+          // cluster scope: the peer's scale warps arrive here too
+          if (!__all_sync(0xffffffffu, mbar_wait<kPair>(&full[stage], phase, wc))) {
+            if constexpr (kPair) st_u32_cluster(peer_abort, 1u);
             aborted = true;
             break;
           }
-          fence_proxy_async();  // the scale warp's copies, before tcgen05.cp reads them
+          fence_proxy_async();  // the scale warps' stores, before tcgen05.cp reads them
           tc_fence_after();
-          const uint32_t aw = smem_u32(smem + static_cast<size_t>(stage) * sb);
-          const uint32_t ax = aw + kWBytes;
-          const uint32_t asw = ax + static_cast<uint32_t>(NT) * 128;
-          const uint32_t asx = asw + kWScaleBytes;
-          const uint32_t xb = x_scale_blocks(NT);
-          const int steps = min(4, (p.K - kb * kStageK) / 64);
-          for (int h = 0; 2 * h < steps; ++h) {
-            tmem_cp_32x128b(tmem_base + kTmemSfW + 4u * h, smem_desc_plain(asw + 512u * h, 128u));
-            for (uint32_t q = 0; q < xb; ++q)
-              tmem_cp_32x128b(tmem_base + kTmemSfX + 8u * h + 4u * q,
-                              smem_desc_plain(asx + 512u * (xb * h + q), 128u));
+          if (elect_one()) {
+            const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(stage) * (sb >> 4));
+            auto scales = [&](uint32_t h) {  // of 128 k
+              tmem_cp<kPair>(sf_w + 4u * h, ws_desc + so + 32u * h);
+              if (wide) {
+                tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 64u * h);
+                tmem_cp<kPair>(sf_x + 8u * h + 4u, xs_desc + so + 64u * h + 32u);
+              } else {
+                tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 32u * h);
+              }
+            };
+            auto mma = [&](uint32_t s, uint32_t add) {  // of 64 k: scale bytes 0-1 or 2-3
+              umma_mxf4<kPair>(d_tmem, w_desc + so + 2u * s, x_desc + so + 2u * s,
+                               idesc | ((s & 1u) << 5) | ((s & 1u) << 30), sf_w + 4u * (s >> 1),
+                               sf_x + 8u * (s >> 1), add);
+            };
+            const uint32_t add = kb != 0 ? 1u : 0u;
+            if (p.K - kb * kStageK >= kStageK) {
+              scales(0);
+              scales(1);
+              mma(0, add);
+              mma(1, 1u);
+              mma(2, 1u);
+              mma(3, 1u);
+            } else {  // the last stage, 64 to 192 deep
+              const int steps = (p.K - kb * kStageK) / 64;
+              scales(0);
+              mma(0, add);
+              if (steps > 1) mma(1, 1u);
+              if (steps > 2) {
+                scales(1);
+                mma(2, 1u);
+              }
+            }
+            if constexpr (kPair) umma_commit_pair_multicast(&empty[stage], 0x3);
+            else umma_commit(&empty[stage]);
           }
-          for (int s = 0; s < steps; ++s) {
-            const uint32_t h = static_cast<uint32_t>(s >> 1);
-            const uint32_t id = static_cast<uint32_t>(s & 1) * 2u;  // scale bytes 0-1 or 2-3
-            umma_mxf4(d_tmem, smem_desc_sw128(aw + 32u * s, 16u, 1024u),
-                      smem_desc_sw128(ax + 32u * s, 16u, 1024u), idesc | (id << 4) | (id << 29),
-                      tmem_base + kTmemSfW + 4u * h, tmem_base + kTmemSfX + 8u * h,
-                      (kb | s) != 0 ? 1u : 0u);
-          }
-          umma_commit(&empty[stage]);
+          __syncwarp();
           if (++stage == nst) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (aborted) break;
-        umma_commit(&tfull[acc]);
+        if (elect_one()) {
+          if constexpr (kPair) umma_commit_pair_multicast(&tfull[acc], 0x3);
+          else umma_commit(&tfull[acc]);
+        }
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       // every UMMA issued must finish before TMEM is released
-      umma_commit(drain);
+      if (elect_one()) {
+        if constexpr (kPair) umma_commit_pair(drain);
+        else umma_commit(drain);
+      }
+      __syncwarp();
       mbar_wait_drain(drain, 0, kDrainLimitNs);
     }
-  } else if (warp == 2) {
+  } else if (warp < 2 + kScaleWarps) {
     // ---------------------------------------------------- token scales ----
+    // Each of the two warps has one of a stage's two 128-deep blocks. Words are
+    // fetched kAhead stages before their place in shared memory is free (the
+    // loads' latency passes meanwhile), then stored and released.
+    constexpr int kAhead = 4;
+    const int h = warp - 2;
+    const uint32_t* xs = reinterpret_cast<const uint32_t*>(p.x_scale);
+    const uint32_t dst0 = smem_u32(smem) + kWBytes + xbytes + kWScaleBytes +
+                          512u * x_scale_blocks(NT) * static_cast<uint32_t>(h) + 16u * lane;
+    const int n_stages = (total > unit ? (total - 1 - unit) / units + 1 : 0) * nk;
+    int fL = unit, fkb = 0;  // the next stage to fetch
+    const uint32_t* f_src = nullptr;
+    int f_tok = 0;
+    auto fetch = [&](uint32_t(&v)[kTokenWords]) {
+      if (fL >= total) return;
+      if (fkb == 0) {
+        const Tile c = decode(fL, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
+        f_tok = min(NT, c.row_end - c.row0);
+        f_src = xs + static_cast<size_t>(h) * p.rows + c.row0;
+      }
+      const bool in = 2 * fkb + h < nkb;
+#pragma unroll
+      for (int m = 0; m < kTokenWords; ++m)
+        v[m] = in && 32 * m + lane < f_tok ? __ldg(f_src + 32 * m + lane) : 0u;
+      f_src += 2 * static_cast<size_t>(p.rows);
+      if (++fkb == nk) {
+        fkb = 0;
+        fL += units;
+      }
+    };
+    uint32_t v[kAhead][kTokenWords];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(v[a]);
     int stage = 0;
     uint32_t phase = 0;
     bool aborted = false;
-    const uint32_t* xs = reinterpret_cast<const uint32_t*>(p.x_scale);
-    const uint32_t xb = x_scale_blocks(NT);
-    for (int L = blockIdx.x; L < total && !aborted; L += gridDim.x) {
-      const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT);
-      const int n_tok = min(NT, c.row_end - c.row0);
-      for (int kb = 0; kb < nk; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
-          aborted = true;
-          break;
-        }
-        const uint32_t dst = smem_u32(smem + static_cast<size_t>(stage) * sb) + kWBytes +
-                             static_cast<uint32_t>(NT) * 128 + kWScaleBytes;
-        for (int h = 0; h < 2 && 2 * kb + h < nkb; ++h) {
-          const uint32_t* src = xs + static_cast<size_t>(2 * kb + h) * p.rows + c.row0;
-          // token i of a block of 128: lane i % 32 of TMEM, word i / 32
-          for (int i = lane; i < n_tok; i += 32)
-            cp_async_4(dst + 512u * (xb * h + static_cast<uint32_t>(i >> 7)) + 16u * (i & 31) +
-                           4u * ((i >> 5) & 3),
-                       src + i);
-        }
-        cp_async_arrive(&full[stage]);
-        if (++stage == nst) {
-          stage = 0;
-          phase ^= 1u;
+    for (int i = 0; i < n_stages && !aborted; i += kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (i + a < n_stages && !aborted) {
+          if (!__all_sync(0xffffffffu, wait(&empty[stage], phase ^ 1u))) {
+            aborted = true;
+          } else {
+            // token t of a block of 128: TMEM lane t % 32, word t / 32
+            const uint32_t dst = dst0 + static_cast<uint32_t>(stage) * sb;
+#pragma unroll
+            for (int m = 0; m < kTokenWords; ++m)
+              if (32 * m < NT) st_shared_u32(dst + 512u * (m >> 2) + 4u * (m & 3), v[a][m]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (kPair) mbar_arrive_cluster_release(full0 + 8u * static_cast<uint32_t>(stage));
+              else mbar_arrive(&full[stage]);
+            }
+            fetch(v[a]);
+            if (++stage == nst) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
         }
       }
     }
-    cp_async_wait_all();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------ epilogue ----
-    // warp w reads TMEM lanes 32 (w % 4) .. + 31: output columns
-    const int q = warp & 3;
+    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t stage_addr = smem_u32(staging + (warp - 4) * kChunkBytes);
+    const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int L = blockIdx.x; L < total; L += gridDim.x) {
-      const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT);
+    for (int L = unit; L < total; L += units) {
+      const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
       const int n_tok = min(NT, c.row_end - c.row0);
-      if (!mbar_wait(&tfull[acc], acc_phase, wc)) break;
+      if (!wait(&tfull[acc], acc_phase)) break;
+      __syncwarp();
       tc_fence_after();
-      const int n = c.n0 + 32 * q + lane;
+      const int n = c.n0 + static_cast<int>(rank) * kBM + 32 * q;
       const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                               static_cast<uint32_t>(acc * kMaxTokens);
-      if (c.n0 + 32 * q < p.N) {
-        uint16_t* d = p.D + static_cast<size_t>(c.row0) * p.N + n;
-        for (int j = 0; j < n_tok; j += 16) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(t_base + static_cast<uint32_t>(j), r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (j + i < n_tok) {
-              float v = __uint_as_float(r[i]);
-              if (p.gelu) v = gelu_tanh_f(v);
-              d[static_cast<size_t>(j + i) * p.N] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            }
-        }
-      }
+      if (n < p.N)
+        for (int j = 32 * half; j < n_tok; j += 64)
+          store_chunk(t_base + static_cast<uint32_t>(j), stage_addr,
+                      p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N, n_tok - j, p.gelu, lane);
       tc_fence_before();
-      mbar_arrive(&tempty[acc]);
+      if constexpr (kPair) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(acc));
+      else mbar_arrive(&tempty[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
@@ -330,13 +505,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither CTA leaves while the peer may still signal it
   tc_fence_after();
-  if (warp == 3) tmem_dealloc(tmem_base, kTmemCols);
+  if (warp == 1) {
+    if constexpr (kPair) tmem_dealloc_pair(tmem_base, kTmemCols);
+    else tmem_dealloc(tmem_base, kTmemCols);
+  }
 }
 
-size_t smem_bytes(int E, int stages, int nt) {
-  return 1024 + static_cast<size_t>(stages) * stage_bytes(nt) + 8 * (2 * stages + 5) + 8 +
-         8 * static_cast<size_t>(E + 1);
+size_t smem_bytes(int E, int stages, int nt, bool pair) {
+  return 1024 + static_cast<size_t>(stages) * stage_bytes(nt, pair) + kEpiWarps * kChunkBytes +
+         8 * (2 * stages + 6) + 16 + 8 * static_cast<size_t>(E + 1);
 }
 
 }  // namespace
@@ -348,8 +527,12 @@ int mx4_tile_tokens(int64_t rows, int E) {
   return want < kMaxTokens ? static_cast<int>(want) : kMaxTokens;
 }
 
-cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                                   const Mx4GemmArgs& a, int num_sms, cudaStream_t st) {
+bool mx4_use_pair(int64_t rows, int E) { return rows >= 64 * static_cast<int64_t>(E); }
+
+template <bool kPair>
+static cudaError_t launch_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                              const CUtensorMap& tm_ws, const Mx4GemmArgs& a, int num_sms,
+                              cudaStream_t st) {
   int dev = 0, optin = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -357,13 +540,35 @@ cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& t
   if (err != cudaSuccess) return err;
   Mx4GemmArgs args = a;
   args.stages = kMaxStages;
-  while (args.stages > 2 && smem_bytes(a.E, args.stages, a.tile_tokens) > static_cast<size_t>(optin))
+  while (args.stages > 2 &&
+         smem_bytes(a.E, args.stages, a.tile_tokens, kPair) > static_cast<size_t>(optin))
     --args.stages;
-  const size_t smem = smem_bytes(a.E, args.stages, a.tile_tokens);
-  err = cudaFuncSetAttribute(expert_gemm_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+  const size_t smem = smem_bytes(a.E, args.stages, a.tile_tokens, kPair);
+  err = cudaFuncSetAttribute(expert_gemm_mx4_kernel<kPair>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  return launch_pdl(expert_gemm_mx4_kernel, dim3(num_sms), dim3(kThreads), smem, st, tm_w, tm_x, args);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * (num_sms / 2) : num_sms), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, expert_gemm_mx4_kernel<kPair>, tm_w, tm_x, tm_ws, args);
+}
+
+cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                                   const CUtensorMap& tm_ws, const Mx4GemmArgs& a, bool pair,
+                                   int num_sms, cudaStream_t st) {
+  return pair ? launch_mx4<true>(tm_w, tm_x, tm_ws, a, num_sms, st)
+              : launch_mx4<false>(tm_w, tm_x, tm_ws, a, num_sms, st);
 }
 
 }  // namespace moe

@@ -231,8 +231,11 @@ cudaError_t launch_quantize_weights_mx4(const uint16_t* W, uint8_t* Wq, uint8_t*
                                         int K, int N, cudaStream_t st);
 // Token tile of the 4-bit grouped product: a multiple of 16, at most 240.
 int mx4_tile_tokens(int64_t rows, int E);
+// Whether it runs as the CTA-pair kernel (token boxes of half a tile).
+bool mx4_use_pair(int64_t rows, int E);
 cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                                   const Mx4GemmArgs& a, int num_sms, cudaStream_t st);
+                                   const CUtensorMap& tm_ws, const Mx4GemmArgs& a, bool pair,
+                                   int num_sms, cudaStream_t st);
 cudaError_t launch_rank(const RankArgs& a, cudaStream_t st);
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_gather(const GatherArgs& a, int num_sms, cudaStream_t st);
