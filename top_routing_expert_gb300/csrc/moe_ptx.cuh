@@ -574,10 +574,11 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// Arrive (release) on an mbarrier of the cluster, and the wait that acquires
-// what the arriving threads of either CTA wrote.
-__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+// Arrive on an mbarrier of the cluster by its shared::cluster address, ordering
+// this CTA's earlier accesses (release at CTA scope). At cluster scope the
+// release waits for every load the thread has in flight.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
