@@ -21,9 +21,7 @@
 // lane quadrant, taking chunks of 32 tokens in turn).
 //
 // Few rows per expert run on single CTAs (M = 128), more on CTA pairs
-// (cta_group::2, M = 256: each CTA holds its 128 columns of W and half of the
-// tile's tokens), which halves the tokens' share of L2 and shared-memory
-// traffic.
+// (cta_group::2, M = 256).
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -47,8 +45,11 @@ constexpr uint32_t kTmemSfW = 480;  // 2 x 4 columns
 constexpr uint32_t kTmemSfX = 488;  // 2 x 8 columns
 
 __host__ __device__ constexpr uint32_t x_scale_blocks(int nt) { return static_cast<uint32_t>(nt + 127) / 128; }
+// A stage: the weights' codes (128 rows, twice in a pair), the tokens' (half of
+// them in a pair), the weights' scales, the tokens' scales; every part is a
+// multiple of 1024 bytes.
 __host__ __device__ constexpr uint32_t stage_bytes(int nt, bool pair) {
-  return kWBytes + static_cast<uint32_t>(nt) * (pair ? 64 : 128) + kWScaleBytes +
+  return (kWBytes + kWScaleBytes) * (pair ? 2 : 1) + static_cast<uint32_t>(nt) * (pair ? 64 : 128) +
          2 * 512 * x_scale_blocks(nt);
 }
 
@@ -171,17 +172,25 @@ __device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, in
   }
 }
 
-// kPair: a tile is 256 output columns (128 per CTA of a cluster pair) x up to
-// tile_tokens tokens; each CTA loads half of the tokens' codes and all of their
-// scales, and the leader (rank 0) issues the UMMAs, so stage barriers of both
-// CTAs' copies live there. Otherwise a tile is 128 columns of one CTA.
+// kPair: a tile is 512 output columns x up to tile_tokens tokens on a cluster
+// pair, as two sub-tiles A and B of 256 columns (128 per CTA) that share the
+// tokens of a stage, each with an accumulator of its own. Per CTA a stage then
+// brings 49 KB for 960 clocks of UMMAs, 51 bytes a clock of the 64 or so that
+// an SM takes in from L2 (one 256-column sub-tile alone: 34 KB for 480, 71).
+// Each CTA loads half of the tokens' codes and all of their scales, and the
+// leader (rank 0) issues the UMMAs, so stage barriers of both CTAs' copies live
+// there. At a tile's ends the UMMAs of A run ahead of those of B by a stage, so
+// that one accumulator is drained while the other is computed.
+// Otherwise a tile is 128 columns of one CTA, its accumulators used in turn.
 template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_w,
                            const __grid_constant__ CUtensorMap tm_x,
                            const __grid_constant__ CUtensorMap tm_ws, Mx4GemmArgs p) {
   constexpr int kCtas = kPair ? 2 : 1;
-  constexpr int kTileN = kBM * kCtas;
+  constexpr int kSubs = kPair ? 2 : 1;           // sub-tiles per tile
+  constexpr int kSubN = kBM * kCtas;             // columns of a sub-tile, M of the UMMA
+  constexpr int kTileN = kSubN * kSubs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_up_1024(smem_raw);
   const int nst = p.stages, NT = p.tile_tokens;
@@ -264,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int issued = 0;
       bool aborted = false;
-      const uint32_t bytes = kWBytes + xbytes + kWScaleBytes;  // per CTA and stage
+      const uint32_t bytes = kSubs * (kWBytes + kWScaleBytes) + xbytes;  // per CTA and stage
+      const int s_none = E * ((p.N + kBM - 1) / kBM) * nkb;  // past the end: reads as zeros
       for (int L = unit; L < total && !aborted; L += units) {
         const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
         const int half = ((min(NT, c.row_end - c.row0) + 15) & ~15) >> 1;
@@ -278,13 +288,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           uint8_t* sw = smem + static_cast<size_t>(stage) * sb;
-          uint8_t* sx = sw + kWBytes;
+          uint8_t* sx = sw + kSubs * kWBytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], kCtas * bytes);
           if constexpr (kPair) {
             const uint32_t bar = full0 + 8u * static_cast<uint32_t>(stage);
             tma_load_2d_pair(sw, &tm_w, bar, kb * 128, c.e * p.N + n0);
             tma_load_2d_pair(sx, &tm_x, bar, kb * 128, x_row);
             tma_load_2d_pair(sx + xbytes, &tm_ws, bar, 0, s_row + 2 * kb);
+            // sub-tile B, if N reaches that far (else zeros, without memory traffic)
+            const bool b = c.n0 + kSubN < p.N;
+            tma_load_2d_pair(sw + kWBytes, &tm_w, bar, kb * 128, b ? c.e * p.N + n0 + kSubN : E * p.N);
+            tma_load_2d_pair(sx + xbytes + kWScaleBytes, &tm_ws, bar, 0,
+                             b ? s_row + (kSubN / kBM) * nkb + 2 * kb : s_none);
           } else {
             tma_load_2d(sw, &tm_w, &full[stage], kb * 128, c.e * p.N + n0);
             tma_load_2d(sx, &tm_x, &full[stage], kb * 128, x_row);
@@ -336,23 +351,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       // against the 480 clocks of its four UMMAs; elected, about 10.
       int stage = 0;
       uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      int acc = 0;             // the accumulator of sub-tile A
+      uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
       bool aborted = false;
       const uint32_t s0 = smem_u32(smem);
       const uint64_t w_desc = smem_desc_sw128(s0, 16u, 1024u);
-      const uint64_t x_desc = smem_desc_sw128(s0 + kWBytes, 16u, 1024u);
-      const uint64_t ws_desc = smem_desc_plain(s0 + kWBytes + xbytes, 128u);
-      const uint64_t xs_desc = smem_desc_plain(s0 + kWBytes + xbytes + kWScaleBytes, 128u);
+      const uint64_t x_desc = smem_desc_sw128(s0 + kSubs * kWBytes, 16u, 1024u);
+      const uint64_t ws_desc = smem_desc_plain(s0 + kSubs * kWBytes + xbytes, 128u);
+      const uint64_t xs_desc =
+          smem_desc_plain(s0 + kSubs * (kWBytes + kWScaleBytes) + xbytes, 128u);
       const uint32_t sf_w = tmem_base + kTmemSfW, sf_x = tmem_base + kTmemSfX;
       const bool wide = NT > 128;  // two blocks of token scales
+      uint32_t idesc = 0;
+      // the UMMAs of sub-tile `sub` for K block kb, which lies in ring slot `st`,
+      // into accumulator `a`; `release`: the slot is free once they are done
+      auto issue = [&](int st, int kb, uint32_t sub, int a, bool release) {
+        if (elect_one()) {
+          const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(st) * (sb >> 4));
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kMaxTokens);
+          const uint64_t wd = w_desc + so + sub * (kWBytes >> 4);
+          const uint64_t wsd = ws_desc + so + sub * (kWScaleBytes >> 4);
+          auto scales = [&](uint32_t h) {  // of 128 k
+            tmem_cp<kPair>(sf_w + 4u * h, wsd + 32u * h);
+            if (wide) {
+              tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 64u * h);
+              tmem_cp<kPair>(sf_x + 8u * h + 4u, xs_desc + so + 64u * h + 32u);
+            } else {
+              tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 32u * h);
+            }
+          };
+          auto mma = [&](uint32_t q, uint32_t add) {  // of 64 k: scale bytes 0-1 or 2-3
+            umma_mxf4<kPair>(d_tmem, wd + 2u * q, x_desc + so + 2u * q,
+                             idesc | ((q & 1u) << 5) | ((q & 1u) << 30), sf_w + 4u * (q >> 1),
+                             sf_x + 8u * (q >> 1), add);
+          };
+          const uint32_t add = kb != 0 ? 1u : 0u;
+          if (p.K - kb * kStageK >= kStageK) {
+            scales(0);
+            scales(1);
+            mma(0, add);
+            mma(1, 1u);
+            mma(2, 1u);
+            mma(3, 1u);
+          } else {  // the last block, 64 to 192 deep
+            const int steps = (p.K - kb * kStageK) / 64;
+            scales(0);
+            mma(0, add);
+            if (steps > 1) mma(1, 1u);
+            if (steps > 2) {
+              scales(1);
+              mma(2, 1u);
+            }
+          }
+          if (release) {
+            if constexpr (kPair) umma_commit_pair_multicast(&empty[st], 0x3);
+            else umma_commit(&empty[st]);
+          }
+        }
+        __syncwarp();
+      };
+      auto finish = [&](int a) {  // accumulator a is complete
+        if (elect_one()) {
+          if constexpr (kPair) umma_commit_pair_multicast(&tfull[a], 0x3);
+          else umma_commit(&tfull[a]);
+        }
+        __syncwarp();
+      };
+      auto acquire = [&](int a) -> bool {  // accumulator a has been drained
+        const bool ok = __all_sync(0xffffffffu, wait(&tempty[a], ((acc_phase >> a) & 1u) ^ 1u));
+        acc_phase ^= 1u << a;
+        tc_fence_after();
+        return ok;
+      };
       for (int L = unit; L < total && !aborted; L += units) {
         const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
         const int n_tok = min(NT, c.row_end - c.row0);
-        const uint32_t idesc = idesc_mxf4_e8m0(kTileN, static_cast<uint32_t>((n_tok + 15) & ~15));
-        if (!__all_sync(0xffffffffu, wait(&tempty[acc], acc_phase ^ 1u))) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kMaxTokens);
+        idesc = idesc_mxf4_e8m0(kSubN, static_cast<uint32_t>((n_tok + 15) & ~15));
+        const bool b = kPair && c.n0 + kSubN < p.N;
+        if (!acquire(acc)) break;
+        int b_kb = 0, b_stage = stage;  // the next K block of B
         for (int kb = 0; kb < nk; ++kb) {
           // cluster scope: the peer's scale warps arrive here too
           if (!__all_sync(0xffffffffu, mbar_wait<kPair>(&full[stage], phase, wc))) {
@@ -362,59 +439,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();  // the scale warps' stores, before tcgen05.cp reads them
           tc_fence_after();
-          if (elect_one()) {
-            const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(stage) * (sb >> 4));
-            auto scales = [&](uint32_t h) {  // of 128 k
-              tmem_cp<kPair>(sf_w + 4u * h, ws_desc + so + 32u * h);
-              if (wide) {
-                tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 64u * h);
-                tmem_cp<kPair>(sf_x + 8u * h + 4u, xs_desc + so + 64u * h + 32u);
-              } else {
-                tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 32u * h);
-              }
-            };
-            auto mma = [&](uint32_t s, uint32_t add) {  // of 64 k: scale bytes 0-1 or 2-3
-              umma_mxf4<kPair>(d_tmem, w_desc + so + 2u * s, x_desc + so + 2u * s,
-                               idesc | ((s & 1u) << 5) | ((s & 1u) << 30), sf_w + 4u * (s >> 1),
-                               sf_x + 8u * (s >> 1), add);
-            };
-            const uint32_t add = kb != 0 ? 1u : 0u;
-            if (p.K - kb * kStageK >= kStageK) {
-              scales(0);
-              scales(1);
-              mma(0, add);
-              mma(1, 1u);
-              mma(2, 1u);
-              mma(3, 1u);
-            } else {  // the last stage, 64 to 192 deep
-              const int steps = (p.K - kb * kStageK) / 64;
-              scales(0);
-              mma(0, add);
-              if (steps > 1) mma(1, 1u);
-              if (steps > 2) {
-                scales(1);
-                mma(2, 1u);
-              }
-            }
-            if constexpr (kPair) umma_commit_pair_multicast(&empty[stage], 0x3);
-            else umma_commit(&empty[stage]);
-          }
-          __syncwarp();
+          issue(stage, kb, 0u, acc, !b);
+          if (kb == nk - 1) finish(acc);
           if (++stage == nst) {
             stage = 0;
             phase ^= 1u;
           }
+          // B follows, but A goes first through the tile's first two blocks and its last two
+          if (b && ((kb != 0 && kb != nk - 2) || kb == nk - 1)) {
+            if (b_kb == 0 && !acquire(1)) {
+              aborted = true;
+              break;
+            }
+            for (; b_kb <= kb; ++b_kb) {
+              issue(b_stage, b_kb, 1u, 1, true);
+              if (++b_stage == nst) b_stage = 0;
+            }
+          }
         }
         if (aborted) break;
-        if (elect_one()) {
-          if constexpr (kPair) umma_commit_pair_multicast(&tfull[acc], 0x3);
-          else umma_commit(&tfull[acc]);
-        }
-        __syncwarp();
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        if (b) finish(1);
+        if constexpr (!kPair) acc ^= 1;
       }
       // every UMMA issued must finish before TMEM is released
       if (elect_one()) {
@@ -432,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kAhead = 4;
     const int h = warp - 2;
     const uint32_t* xs = reinterpret_cast<const uint32_t*>(p.x_scale);
-    const uint32_t dst0 = smem_u32(smem) + kWBytes + xbytes + kWScaleBytes +
+    const uint32_t dst0 = smem_u32(smem) + kSubs * (kWBytes + kWScaleBytes) + xbytes +
                           512u * x_scale_blocks(NT) * static_cast<uint32_t>(h) + 16u * lane;
     const int n_stages = (total > unit ? (total - 1 - unit) / units + 1 : 0) * nk;
     int fL = unit, fkb = 0;  // the next stage to fetch
@@ -498,27 +543,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stage_addr = smem_u32(staging + (warp - 4) * kChunkBytes);
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int L = unit; L < total; L += units) {
+    uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
+    bool aborted = false;
+    for (int L = unit; L < total && !aborted; L += units) {
       const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
       const int n_tok = min(NT, c.row_end - c.row0);
-      if (!wait(&tfull[acc], acc_phase)) break;
-      __syncwarp();
-      tc_fence_after();
-      const int n = c.n0 + static_cast<int>(rank) * kBM + 32 * q;
-      const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                              static_cast<uint32_t>(acc * kMaxTokens);
-      if (n < p.N)
-        for (int j = 32 * half; j < n_tok; j += 64)
-          store_chunk(t_base + static_cast<uint32_t>(j), stage_addr,
-                      p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N, n_tok - j, p.gelu, lane);
-      tc_fence_before();
-      if constexpr (kPair) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(acc));
-      else mbar_arrive(&tempty[acc]);
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
+      for (int sub = 0; sub < kSubs; ++sub) {
+        if (sub > 0 && c.n0 + kSubN >= p.N) break;
+        const int a = kPair ? sub : acc;
+        if (!wait(&tfull[a], (acc_phase >> a) & 1u)) {
+          aborted = true;
+          break;
+        }
+        acc_phase ^= 1u << a;
+        __syncwarp();
+        tc_fence_after();
+        const int n = c.n0 + sub * kSubN + static_cast<int>(rank) * kBM + 32 * q;
+        const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                static_cast<uint32_t>(a * kMaxTokens);
+        if (n < p.N)
+          for (int j = 32 * half; j < n_tok; j += 64)
+            store_chunk(t_base + static_cast<uint32_t>(j), stage_addr,
+                        p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N, n_tok - j, p.gelu,
+                        lane);
+        tc_fence_before();
+        if constexpr (kPair) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(a));
+        else mbar_arrive(&tempty[a]);
       }
+      if constexpr (!kPair) acc ^= 1;
     }
   }
   __syncwarp();
@@ -559,7 +611,7 @@ static cudaError_t launch_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
   if (err != cudaSuccess) return err;
   Mx4GemmArgs args = a;
   args.stages = kMaxStages;
-  while (args.stages > 2 &&
+  while (args.stages > 3 &&  // the pair holds up to three slots at a tile's end
          smem_bytes(a.E, args.stages, a.tile_tokens, kPair) > static_cast<size_t>(optin))
     --args.stages;
   const size_t smem = smem_bytes(a.E, args.stages, a.tile_tokens, kPair);
