@@ -114,6 +114,11 @@ __device__ __forceinline__ void store_chunk(uint32_t taddr, uint32_t stage, uint
   __syncwarp();
 }
 
+// A value that is the same in all lanes of the warp, made known as such: it and
+// what is computed from it stay in uniform registers, which tcgen05
+// instructions take their operands from.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 struct Tile {
   int e, row0, row_end, n0;
 };
@@ -172,6 +177,64 @@ __device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, in
   }
 }
 
+// What the UMMAs of one K block of a sub-tile read; all uniform.
+struct Block {
+  uint64_t w, x, ws, xs;    // descriptors: codes and scales, of the weights and the tokens
+  uint32_t d;               // accumulator
+  uint32_t sf_w, sf_x;      // scales in TMEM
+  uint32_t idesc0, idesc1;  // for scale bytes 0-1 and 2-3 of a word
+  uint32_t add;             // 0: the accumulator starts here
+};
+
+// Issues a K block of 256: its scales to TMEM, then four UMMAs of 64 (which wait
+// for them in order). Called by the whole warp; straight-line code, so that one
+// elected lane issues an instruction about every 20 clocks (with the branches on
+// sizes inside, about 36, too slow for 120-clock UMMAs with their scales).
+template <bool kPair, bool kWide>
+__device__ __forceinline__ void issue_block(const Block& b, uint64_t* release) {
+  if (elect_one()) {
+    tmem_cp<kPair>(b.sf_w, b.ws);
+    tmem_cp<kPair>(b.sf_x, b.xs);
+    if constexpr (kWide) {  // more than 128 tokens: two blocks of scales
+      tmem_cp<kPair>(b.sf_x + 4u, b.xs + 32u);
+      tmem_cp<kPair>(b.sf_x + 8u, b.xs + 64u);
+      tmem_cp<kPair>(b.sf_x + 12u, b.xs + 96u);
+    } else {
+      tmem_cp<kPair>(b.sf_x + 8u, b.xs + 32u);
+    }
+    tmem_cp<kPair>(b.sf_w + 4u, b.ws + 32u);
+    umma_mxf4<kPair>(b.d, b.w, b.x, b.idesc0, b.sf_w, b.sf_x, b.add);
+    umma_mxf4<kPair>(b.d, b.w + 2u, b.x + 2u, b.idesc1, b.sf_w, b.sf_x, 1u);
+    umma_mxf4<kPair>(b.d, b.w + 4u, b.x + 4u, b.idesc0, b.sf_w + 4u, b.sf_x + 8u, 1u);
+    umma_mxf4<kPair>(b.d, b.w + 6u, b.x + 6u, b.idesc1, b.sf_w + 4u, b.sf_x + 8u, 1u);
+    if (release != nullptr) {
+      if constexpr (kPair) umma_commit_pair_multicast(release, 0x3);
+      else umma_commit(release);
+    }
+  }
+  __syncwarp();
+}
+
+// The last K block of a tile when it is 64, 128 or 192 deep.
+template <bool kPair>
+__device__ __noinline__ void issue_tail(const Block& b, int steps, bool wide, uint64_t* release) {
+  if (elect_one()) {
+    for (uint32_t h = 0; 2 * h < static_cast<uint32_t>(steps); ++h) {
+      tmem_cp<kPair>(b.sf_w + 4u * h, b.ws + 32u * h);
+      tmem_cp<kPair>(b.sf_x + 8u * h, b.xs + (wide ? 64u : 32u) * h);
+      if (wide) tmem_cp<kPair>(b.sf_x + 8u * h + 4u, b.xs + 64u * h + 32u);
+    }
+    for (uint32_t q = 0; q < static_cast<uint32_t>(steps); ++q)
+      umma_mxf4<kPair>(b.d, b.w + 2u * q, b.x + 2u * q, (q & 1u) ? b.idesc1 : b.idesc0,
+                       b.sf_w + 4u * (q >> 1), b.sf_x + 8u * (q >> 1), q == 0 ? b.add : 1u);
+    if (release != nullptr) {
+      if constexpr (kPair) umma_commit_pair_multicast(release, 0x3);
+      else umma_commit(release);
+    }
+  }
+  __syncwarp();
+}
+
 // kPair: a tile is 512 output columns x up to tile_tokens tokens on a cluster
 // pair, as two sub-tiles A and B of 256 columns (128 per CTA) that share the
 // tokens of a stage, each with an accumulator of its own. Per CTA a stage then
@@ -209,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* offs = reinterpret_cast<int*>(peer_issued + 1);  // [E+1]
   int* prefix = offs + (p.E + 1);                       // [E+1]
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int E = p.E;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -250,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) cluster_sync();  // barriers initialised before any remote use
   tc_fence_after();
 
-  const uint32_t tmem_base = *tmem_slot;
-  const int total_t = prefix[E];
+  const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
+  const int total_t = uniform(prefix[E]);
   const int n_tiles_n = (p.N + kTileN - 1) / kTileN;
   const int total = total_t * n_tiles_n;
   const int nk = (p.K + kStageK - 1) / kStageK;   // stages per tile
@@ -366,49 +429,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the UMMAs of sub-tile `sub` for K block kb, which lies in ring slot `st`,
       // into accumulator `a`; `release`: the slot is free once they are done
       auto issue = [&](int st, int kb, uint32_t sub, int a, bool release) {
-        if (elect_one()) {
-          const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(st) * (sb >> 4));
-          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kMaxTokens);
-          const uint64_t wd = w_desc + so + sub * (kWBytes >> 4);
-          const uint64_t wsd = ws_desc + so + sub * (kWScaleBytes >> 4);
-          auto scales = [&](uint32_t h) {  // of 128 k
-            tmem_cp<kPair>(sf_w + 4u * h, wsd + 32u * h);
-            if (wide) {
-              tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 64u * h);
-              tmem_cp<kPair>(sf_x + 8u * h + 4u, xs_desc + so + 64u * h + 32u);
-            } else {
-              tmem_cp<kPair>(sf_x + 8u * h, xs_desc + so + 32u * h);
-            }
-          };
-          auto mma = [&](uint32_t q, uint32_t add) {  // of 64 k: scale bytes 0-1 or 2-3
-            umma_mxf4<kPair>(d_tmem, wd + 2u * q, x_desc + so + 2u * q,
-                             idesc | ((q & 1u) << 5) | ((q & 1u) << 30), sf_w + 4u * (q >> 1),
-                             sf_x + 8u * (q >> 1), add);
-          };
-          const uint32_t add = kb != 0 ? 1u : 0u;
-          if (p.K - kb * kStageK >= kStageK) {
-            scales(0);
-            scales(1);
-            mma(0, add);
-            mma(1, 1u);
-            mma(2, 1u);
-            mma(3, 1u);
-          } else {  // the last block, 64 to 192 deep
-            const int steps = (p.K - kb * kStageK) / 64;
-            scales(0);
-            mma(0, add);
-            if (steps > 1) mma(1, 1u);
-            if (steps > 2) {
-              scales(1);
-              mma(2, 1u);
-            }
-          }
-          if (release) {
-            if constexpr (kPair) umma_commit_pair_multicast(&empty[st], 0x3);
-            else umma_commit(&empty[st]);
-          }
+        const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(st) * (sb >> 4));
+        Block k;
+        k.w = w_desc + so + sub * (kWBytes >> 4);
+        k.x = x_desc + so;
+        k.ws = ws_desc + so + sub * (kWScaleBytes >> 4);
+        k.xs = xs_desc + so;
+        k.d = tmem_base + static_cast<uint32_t>(a * kMaxTokens);
+        k.sf_w = sf_w;
+        k.sf_x = sf_x;
+        k.idesc0 = idesc;
+        k.idesc1 = idesc | (2u << 4) | (2u << 29);
+        k.add = kb != 0 ? 1u : 0u;
+        uint64_t* bar = release ? &empty[st] : nullptr;
+        const int steps = (p.K - kb * kStageK) / 64;
+        if (steps >= 4) {
+          if (wide) issue_block<kPair, true>(k, bar);
+          else issue_block<kPair, false>(k, bar);
+        } else {
+          issue_tail<kPair>(k, steps, wide, bar);
         }
-        __syncwarp();
       };
       auto finish = [&](int a) {  // accumulator a is complete
         if (elect_one()) {
@@ -425,9 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int L = unit; L < total && !aborted; L += units) {
         const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
-        const int n_tok = min(NT, c.row_end - c.row0);
+        const int n_tok = uniform(min(NT, c.row_end - c.row0));
         idesc = idesc_mxf4_e8m0(kSubN, static_cast<uint32_t>((n_tok + 15) & ~15));
-        const bool b = kPair && c.n0 + kSubN < p.N;
+        const bool b = kPair && uniform(c.n0) + kSubN < p.N;
         if (!acquire(acc)) break;
         int b_kb = 0, b_stage = stage;  // the next K block of B
         for (int kb = 0; kb < nk; ++kb) {
