@@ -41,8 +41,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemSfW = 480;  // 2 x 4 columns
-constexpr uint32_t kTmemSfX = 488;  // 2 x 8 columns
+constexpr uint32_t kTmemSfX = 480;  // scales of a K block: the tokens', 2 x 8 columns,
+constexpr uint32_t kTmemSfW = 496;  // and the weights', 2 x 4 columns per sub-tile
 
 __host__ __device__ constexpr uint32_t x_scale_blocks(int nt) { return static_cast<uint32_t>(nt + 127) / 128; }
 // A stage: the weights' codes (128 rows, twice in a pair), the tokens' (half of
@@ -59,6 +59,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // GELU-tanh of two values: 0.5 u (1 + tanh z) = u / (1 + 2^(-2 log2(e) z)), z =
 // sqrt(2/pi) (u + 0.044715 u^3). The two quotients share one reciprocal, so a
 // value takes 1.5 special-function operations (4 a clock and SM sub-partition),
@@ -70,18 +76,16 @@ __device__ __forceinline__ void gelu_tanh_x2(uint32_t& x, uint32_t& y) {
   const float pu = u * fmaf(u * u, -0.10294324f, -2.3022082f);
   const float pv = v * fmaf(v * v, -0.10294324f, -2.3022082f);
   const float a = 1.0f + exp2_approx(fminf(pu, 60.0f)), b = 1.0f + exp2_approx(fminf(pv, 60.0f));
-  const float r = __fdividef(1.0f, a * b);
+  const float r = rcp_approx(a * b);
   x = __float_as_uint(u * (r * b));
   y = __float_as_uint(v * (r * a));
 }
 
-// One warp's 32 output columns x up to 32 tokens (n of them valid) from TMEM
-// columns taddr.. to D. The accumulator has output columns in lanes and tokens
-// in columns; it is read as 8x8 fragments, which go transposed through 2 KB of
-// the warp's shared memory (16-byte pieces, XOR-swizzled so that neither side
-// conflicts) and leave as 64-byte row pieces, 16 bytes a lane.
-__device__ __forceinline__ void store_chunk(uint32_t taddr, uint32_t stage, uint16_t* d, int pitch,
-                                            int n, int gelu, int lane) {
+// The epilogue's two halves, for one warp's 32 output columns x 32 tokens. The
+// accumulator has output columns in lanes and tokens in columns; it is read as
+// 8x8 fragments and rounded to bf16, two tokens to a register (m[4g + c]: tokens
+// 8g .. 8g + 7, columns 8c .. 8c + 7).
+__device__ __forceinline__ void load_chunk(uint32_t taddr, int gelu, uint32_t (&m)[16]) {
   uint32_t a[16], b[16];
   tmem_ld_16x256b_x4(taddr, a);
   tmem_ld_16x256b_x4(taddr + (16u << 16), b);
@@ -93,15 +97,23 @@ __device__ __forceinline__ void store_chunk(uint32_t taddr, uint32_t stage, uint
       gelu_tanh_x2(b[i], b[i + 1]);
     }
   }
-  auto pack = [](uint32_t lo, uint32_t hi) {
-    return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
-  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[(i >> 1) * 4 + (i & 1)] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+    m[(i >> 1) * 4 + 2 + (i & 1)] = pack_bf16x2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+  }
+}
+
+// To D (n of the tokens valid): the fragments go transposed through 2 KB of the
+// warp's shared memory, in 16-byte pieces XOR-swizzled so that neither side has
+// bank conflicts, and leave as 64-byte row pieces, 16 bytes a lane.
+__device__ __forceinline__ void store_chunk(const uint32_t (&m)[16], uint32_t stage, uint16_t* d,
+                                            int pitch, int n, int lane) {
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const uint32_t t = 8u * g + (lane & 7), c = static_cast<uint32_t>(lane) >> 3;
-    stmatrix_x4_trans(stage + 64u * t + 16u * (c ^ ((t >> 1) & 3u)), pack(a[4 * g], a[4 * g + 1]),
-                      pack(a[4 * g + 2], a[4 * g + 3]), pack(b[4 * g], b[4 * g + 1]),
-                      pack(b[4 * g + 2], b[4 * g + 3]));
+    stmatrix_x4_trans(stage + 64u * t + 16u * (c ^ ((t >> 1) & 3u)), m[4 * g], m[4 * g + 1],
+                      m[4 * g + 2], m[4 * g + 3]);
   }
   __syncwarp();
 #pragma unroll
@@ -211,6 +223,37 @@ __device__ __forceinline__ void issue_block(const Block& b, uint64_t* release) {
       if constexpr (kPair) umma_commit_pair_multicast(release, 0x3);
       else umma_commit(release);
     }
+  }
+  __syncwarp();
+}
+
+// A K block of both sub-tiles (b: sub-tile A's, whose descriptors and addresses
+// lead to B's), with the tokens' scales copied once.
+template <bool kWide>
+__device__ __forceinline__ void issue_block_ab(const Block& b, uint32_t d_b, uint64_t* release) {
+  constexpr uint32_t kW = kWBytes >> 4, kS = kWScaleBytes >> 4;
+  if (elect_one()) {
+    tmem_cp<true>(b.sf_w, b.ws);
+    tmem_cp<true>(b.sf_x, b.xs);
+    if constexpr (kWide) {
+      tmem_cp<true>(b.sf_x + 4u, b.xs + 32u);
+      tmem_cp<true>(b.sf_x + 8u, b.xs + 64u);
+      tmem_cp<true>(b.sf_x + 12u, b.xs + 96u);
+    } else {
+      tmem_cp<true>(b.sf_x + 8u, b.xs + 32u);
+    }
+    tmem_cp<true>(b.sf_w + 4u, b.ws + 32u);
+    tmem_cp<true>(b.sf_w + 8u, b.ws + kS);
+    tmem_cp<true>(b.sf_w + 12u, b.ws + kS + 32u);
+    umma_mxf4<true>(b.d, b.w, b.x, b.idesc0, b.sf_w, b.sf_x, b.add);
+    umma_mxf4<true>(b.d, b.w + 2u, b.x + 2u, b.idesc1, b.sf_w, b.sf_x, 1u);
+    umma_mxf4<true>(b.d, b.w + 4u, b.x + 4u, b.idesc0, b.sf_w + 4u, b.sf_x + 8u, 1u);
+    umma_mxf4<true>(b.d, b.w + 6u, b.x + 6u, b.idesc1, b.sf_w + 4u, b.sf_x + 8u, 1u);
+    umma_mxf4<true>(d_b, b.w + kW, b.x, b.idesc0, b.sf_w + 8u, b.sf_x, b.add);
+    umma_mxf4<true>(d_b, b.w + kW + 2u, b.x + 2u, b.idesc1, b.sf_w + 8u, b.sf_x, 1u);
+    umma_mxf4<true>(d_b, b.w + kW + 4u, b.x + 4u, b.idesc0, b.sf_w + 12u, b.sf_x + 8u, 1u);
+    umma_mxf4<true>(d_b, b.w + kW + 6u, b.x + 6u, b.idesc1, b.sf_w + 12u, b.sf_x + 8u, 1u);
+    umma_commit_pair_multicast(release, 0x3);
   }
   __syncwarp();
 }
@@ -428,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t idesc = 0;
       // the UMMAs of sub-tile `sub` for K block kb, which lies in ring slot `st`,
       // into accumulator `a`; `release`: the slot is free once they are done
-      auto issue = [&](int st, int kb, uint32_t sub, int a, bool release) {
+      auto block = [&](int st, int kb, uint32_t sub, int a) {
         const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(st) * (sb >> 4));
         Block k;
         k.w = w_desc + so + sub * (kWBytes >> 4);
@@ -436,11 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         k.ws = ws_desc + so + sub * (kWScaleBytes >> 4);
         k.xs = xs_desc + so;
         k.d = tmem_base + static_cast<uint32_t>(a * kMaxTokens);
-        k.sf_w = sf_w;
+        k.sf_w = sf_w + 8u * sub;
         k.sf_x = sf_x;
         k.idesc0 = idesc;
         k.idesc1 = idesc | (2u << 4) | (2u << 29);
         k.add = kb != 0 ? 1u : 0u;
+        return k;
+      };
+      auto issue = [&](int st, int kb, uint32_t sub, int a, bool release) {
+        const Block k = block(st, kb, sub, a);
         uint64_t* bar = release ? &empty[st] : nullptr;
         const int steps = (p.K - kb * kStageK) / 64;
         if (steps >= 4) {
@@ -479,14 +526,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();  // the scale warps' stores, before tcgen05.cp reads them
           tc_fence_after();
+          // B follows A at once, but A goes first through the tile's first two blocks
+          // and its last two
+          const bool hold = b && ((kb == 0 && nk > 1) || kb == nk - 2);
+          if (kPair && b && !hold && b_kb == kb && kb != 0 && kb != nk - 1) {
+            const Block k = block(stage, kb, 0u, 0);
+            if (wide) issue_block_ab<true>(k, k.d + kMaxTokens, &empty[stage]);
+            else issue_block_ab<false>(k, k.d + kMaxTokens, &empty[stage]);
+            ++b_kb;
+            if (++stage == nst) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            b_stage = stage;
+            continue;
+          }
           issue(stage, kb, 0u, acc, !b);
           if (kb == nk - 1) finish(acc);
           if (++stage == nst) {
             stage = 0;
             phase ^= 1u;
           }
-          // B follows, but A goes first through the tile's first two blocks and its last two
-          if (b && ((kb != 0 && kb != nk - 2) || kb == nk - 1)) {
+          if (b && !hold) {
             if (b_kb == 0 && !acquire(1)) {
               aborted = true;
               break;
@@ -601,14 +662,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = c.n0 + sub * kSubN + static_cast<int>(rank) * kBM + 32 * q;
         const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                                 static_cast<uint32_t>(a * kMaxTokens);
-        if (n < p.N)
-          for (int j = 32 * half; j < n_tok; j += 64)
-            store_chunk(t_base + static_cast<uint32_t>(j), stage_addr,
-                        p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N, n_tok - j, p.gelu,
-                        lane);
+        // Everything is read out of TMEM and the accumulator handed back before
+        // anything is stored: its next use waits for the reads alone.
+        constexpr int kChunks = (kMaxTokens + 63) / 64;
+        uint32_t m[kChunks][16];
+        const bool any = n < p.N;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int j = 64 * i + 32 * half;
+          if (any && j < n_tok) load_chunk(t_base + static_cast<uint32_t>(j), p.gelu, m[i]);
+        }
         tc_fence_before();
         if constexpr (kPair) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(a));
         else mbar_arrive(&tempty[a]);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int j = 64 * i + 32 * half;
+          if (any && j < n_tok)
+            store_chunk(m[i], stage_addr, p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N,
+                        n_tok - j, lane);
+        }
       }
       if constexpr (!kPair) acc ^= 1;
     }
