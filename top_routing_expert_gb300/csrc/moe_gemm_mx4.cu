@@ -159,6 +159,29 @@ __device__ __forceinline__ Tile decode(int L, const int* prefix, const int* offs
   return t;
 }
 
+// The tiles unit, unit + units, ... of one warp, in order. Decoding one takes
+// several hundred clocks (divisions, a search): the lanes decode 32 at a time.
+struct Tiles {
+  const int *prefix, *offs;
+  int E, total_t, total, n_tiles_n, nt, bm, unit, units;
+  int i = 0;      // the next tile is unit + i * units
+  Tile mine;
+  // Called by the whole warp; false after the last tile. The result is uniform.
+  __device__ __forceinline__ bool next(Tile& t) {
+    if (unit + i * units >= total) return false;
+    if ((i & 31) == 0) {
+      const int L = unit + (i + static_cast<int>(threadIdx.x & 31)) * units;
+      if (L < total) mine = decode(L, prefix, offs, E, total_t, n_tiles_n, nt, bm);
+    }
+    t.e = __shfl_sync(0xffffffffu, mine.e, i & 31);
+    t.row0 = __shfl_sync(0xffffffffu, mine.row0, i & 31);
+    t.row_end = __shfl_sync(0xffffffffu, mine.row_end, i & 31);
+    t.n0 = __shfl_sync(0xffffffffu, mine.n0, i & 31);
+    ++i;
+    return true;
+  }
+};
+
 // Segment offsets, held to the buffer and non-decreasing, and the prefix of the
 // experts' token tiles. All threads; followed by a barrier of the caller's.
 __device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, int* prefix, int nt) {
@@ -362,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = total_t * n_tiles_n;
   const int nk = (p.K + kStageK - 1) / kStageK;   // stages per tile
   const int nkb = (p.K + 127) / 128;              // 128-deep scale blocks
+  Tiles tiles{prefix, offs, E, total_t, total, n_tiles_n, NT, kTileN, unit, units};
+  Tile c;
   const WaitCtl wc{abort_flag, p.dev_status, p.timeout_ns};
   // A wait that gives up stops the peer CTA too.
   const uint32_t peer_abort = kPair ? mapa_shared(smem_u32(abort_flag), rank ^ 1u) : 0u;
@@ -373,26 +398,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t full0 = kPair ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------ TMA producer ----
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
-      bool aborted = false;
-      const uint32_t bytes = kSubs * (kWBytes + kWScaleBytes) + xbytes;  // per CTA and stage
-      const int s_none = E * ((p.N + kBM - 1) / kBM) * nkb;  // past the end: reads as zeros
-      for (int L = unit; L < total && !aborted; L += units) {
-        const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
-        const int half = ((min(NT, c.row_end - c.row0) + 15) & ~15) >> 1;
-        const int n0 = c.n0 + static_cast<int>(rank) * kBM;
-        const int x_row = c.row0 + (kPair ? static_cast<int>(rank) * half : 0);
-        // scale blocks of this CTA's 128 columns (past N or K: others', unused)
-        const int s_row = (c.e * ((p.N + kBM - 1) / kBM) + n0 / kBM) * nkb;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!wait(&empty[stage], phase ^ 1u)) {
-            aborted = true;
-            break;
-          }
+    // ------------------------------------------------ TMA producer ----
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    bool aborted = false;
+    const uint32_t bytes = kSubs * (kWBytes + kWScaleBytes) + xbytes;  // per CTA and stage
+    const int s_none = E * ((p.N + kBM - 1) / kBM) * nkb;  // past the end: reads as zeros
+    while (!aborted && tiles.next(c)) {
+      const int half = ((min(NT, c.row_end - c.row0) + 15) & ~15) >> 1;
+      const int n0 = c.n0 + static_cast<int>(rank) * kBM;
+      const int x_row = c.row0 + (kPair ? static_cast<int>(rank) * half : 0);
+      // scale blocks of this CTA's 128 columns (past N or K: others', unused)
+      const int s_row = (c.e * ((p.N + kBM - 1) / kBM) + n0 / kBM) * nkb;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!__all_sync(0xffffffffu, wait(&empty[stage], phase ^ 1u))) {
+          aborted = true;
+          break;
+        }
+        if (elect_one()) {
           uint8_t* sw = smem + static_cast<size_t>(stage) * sb;
           uint8_t* sx = sw + kSubs * kWBytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], kCtas * bytes);
@@ -411,13 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(sx, &tm_x, &full[stage], kb * 128, x_row);
             tma_load_2d(sx + xbytes, &tm_ws, &full[stage], 0, s_row + 2 * kb);
           }
-          ++issued;
-          if (++stage == nst) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
+    }
+    if (lane == 0) {
       // Every load issued lands before any CTA can exit. In a pair the peer
       // reports how many stages it loaded, and the leader makes the byte
       // accounting of each stage still in flight whole before it waits for it
@@ -510,11 +537,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return ok;
       };
-      for (int L = unit; L < total && !aborted; L += units) {
-        const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
-        const int n_tok = uniform(min(NT, c.row_end - c.row0));
+      while (!aborted && tiles.next(c)) {
+        const int n_tok = min(NT, c.row_end - c.row0);
         idesc = idesc_mxf4_e8m0(kSubN, static_cast<uint32_t>((n_tok + 15) & ~15));
-        const bool b = kPair && uniform(c.n0) + kSubN < p.N;
+        const bool b = kPair && c.n0 + kSubN < p.N;
         if (!acquire(acc)) break;
         int b_kb = 0, b_stage = stage;  // the next K block of B
         for (int kb = 0; kb < nk; ++kb) {
@@ -581,25 +607,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t dst0 = smem_u32(smem) + kSubs * (kWBytes + kWScaleBytes) + xbytes +
                           512u * x_scale_blocks(NT) * static_cast<uint32_t>(h) + 16u * lane;
     const int n_stages = (total > unit ? (total - 1 - unit) / units + 1 : 0) * nk;
-    int fL = unit, fkb = 0;  // the next stage to fetch
+    int fkb = 0;  // the next K block to fetch, of the current tile
+    bool f_more = true;
     const uint32_t* f_src = nullptr;
     int f_tok = 0;
     auto fetch = [&](uint32_t(&v)[kTokenWords]) {
-      if (fL >= total) return;
-      if (fkb == 0) {
-        const Tile c = decode(fL, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
+      if (fkb == 0 && f_more) {
+        f_more = tiles.next(c);
         f_tok = min(NT, c.row_end - c.row0);
         f_src = xs + static_cast<size_t>(h) * p.rows + c.row0;
       }
+      if (!f_more) return;
       const bool in = 2 * fkb + h < nkb;
 #pragma unroll
       for (int m = 0; m < kTokenWords; ++m)
         v[m] = in && 32 * m + lane < f_tok ? __ldg(f_src + 32 * m + lane) : 0u;
       f_src += 2 * static_cast<size_t>(p.rows);
-      if (++fkb == nk) {
-        fkb = 0;
-        fL += units;
-      }
+      if (++fkb == nk) fkb = 0;
     };
     uint32_t v[kAhead][kTokenWords];
 #pragma unroll
@@ -646,13 +670,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
     bool aborted = false;
-    for (int L = unit; L < total && !aborted; L += units) {
-      const Tile c = decode(L, prefix, offs, E, total_t, n_tiles_n, NT, kTileN);
+    while (!aborted && tiles.next(c)) {
       const int n_tok = min(NT, c.row_end - c.row0);
       for (int sub = 0; sub < kSubs; ++sub) {
         if (sub > 0 && c.n0 + kSubN >= p.N) break;
         const int a = kPair ? sub : acc;
-        if (!wait(&tfull[a], (acc_phase >> a) & 1u)) {
+        if (!__all_sync(0xffffffffu, wait(&tfull[a], (acc_phase >> a) & 1u))) {
           aborted = true;
           break;
         }
