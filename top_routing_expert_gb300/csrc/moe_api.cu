@@ -1530,14 +1530,16 @@ moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N, co
   a.dev_status = dev_status;
   a.timeout_ns = wait_timeout_ns();
   const bool pair = mx4_use_pair(rows, a.E);
-  CUtensorMap tm_w, tm_x, tm_ws;
+  CUtensorMap tm_w, tm_x, tm_ws, tm_d;
   if (!tmap_u8_2d(&tm_w, Wq, K / 2, static_cast<uint64_t>(E) * N)) return MOE_ERR_CUDA;
   if (!tmap_u8_2d(&tm_x, x_q, K / 2, rows, pair ? a.tile_tokens / 2 : a.tile_tokens))
     return MOE_ERR_CUDA;
   // the 512-byte blocks of the weights' scales, two at a time
   if (!tmap_u32_rows(&tm_ws, w_scale, 128, static_cast<uint64_t>(E) * ((N + 127) / 128) * ((K + 127) / 128), 2))
     return MOE_ERR_CUDA;
-  MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, tm_ws, a, pair, num_sms(),
+  // stores of 32 rows x 64 columns
+  if (!tmap_bf16_2d(&tm_d, D, N, rows, 64, 32)) return MOE_ERR_CUDA;
+  MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, tm_ws, tm_d, a, pair, num_sms(),
                                   static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }

@@ -39,7 +39,7 @@ constexpr int kScaleWarps = 2;
 constexpr int kTokenWords = (kMaxTokens + 31) / 32;  // scale words per lane, block and tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp
+constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp (two share theirs)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSfX = 480;  // scales of a K block: the tokens', 2 x 8 columns,
 constexpr uint32_t kTmemSfW = 496;  // and the weights', 2 x 4 columns per sub-tile
@@ -72,13 +72,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // the denominators stays finite: the result there is below 2^-56, not smaller.
 __device__ __forceinline__ void gelu_tanh_x2(uint32_t& x, uint32_t& y) {
   const float u = __uint_as_float(x), v = __uint_as_float(y);
-  // -2 log2(e) sqrt(2/pi) and that times 0.044715
-  const float pu = u * fmaf(u * u, -0.10294324f, -2.3022082f);
-  const float pv = v * fmaf(v * v, -0.10294324f, -2.3022082f);
-  const float a = 1.0f + exp2_approx(fminf(pu, 60.0f)), b = 1.0f + exp2_approx(fminf(pv, 60.0f));
+  const uint64_t uv = f32x2(u, v);
+  // -2 log2(e) sqrt(2/pi) (0.044715 u^2 + 1) u
+  const uint64_t e2 = f32x2_mul(uv, f32x2_fma(f32x2_mul(uv, uv), f32x2(-0.10294324f, -0.10294324f),
+                                              f32x2(-2.3022082f, -2.3022082f)));
+  float pu, pv, a, b;
+  f32x2_get(e2, pu, pv);
+  const uint64_t ab = f32x2_add(f32x2(exp2_approx(fminf(pu, 60.0f)), exp2_approx(fminf(pv, 60.0f))),
+                                f32x2(1.0f, 1.0f));
+  f32x2_get(ab, a, b);
   const float r = rcp_approx(a * b);
-  x = __float_as_uint(u * (r * b));
-  y = __float_as_uint(v * (r * a));
+  f32x2_get(f32x2_mul(uv, f32x2_mul(f32x2(r, r), f32x2(b, a))), a, b);
+  x = __float_as_uint(a);
+  y = __float_as_uint(b);
 }
 
 // The epilogue's two halves, for one warp's 32 output columns x 32 tokens. The
@@ -104,26 +110,28 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, int gelu, uint32_t (&
   }
 }
 
-// To D (n of the tokens valid): the fragments go transposed through 2 KB of the
-// warp's shared memory, in 16-byte pieces XOR-swizzled so that neither side has
-// bank conflicts, and leave as 64-byte row pieces, 16 bytes a lane.
-__device__ __forceinline__ void store_chunk(const uint32_t (&m)[16], uint32_t stage, uint16_t* d,
-                                            int pitch, int n, int lane) {
+// To shared memory, transposed: [32 tokens][64 columns] of two warps (this one's
+// columns first or second by `hq`), 128-byte rows in TMA's 128-byte swizzle,
+// which also keeps the 16-byte pieces of eight tokens in different banks.
+__device__ __forceinline__ void stage_chunk(const uint32_t (&m)[16], uint32_t stage, int hq,
+                                            int lane) {
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const uint32_t t = 8u * g + (lane & 7), c = static_cast<uint32_t>(lane) >> 3;
-    stmatrix_x4_trans(stage + 64u * t + 16u * (c ^ ((t >> 1) & 3u)), m[4 * g], m[4 * g + 1],
+    const uint32_t t = lane & 7, c = 4u * hq + (static_cast<uint32_t>(lane) >> 3);
+    stmatrix_x4_trans(stage + 1024u * g + 128u * t + 16u * (c ^ t), m[4 * g], m[4 * g + 1],
                       m[4 * g + 2], m[4 * g + 3]);
   }
-  __syncwarp();
+}
+
+// The first n (under 32) tokens of a staged chunk to D, each warp half of them.
+__device__ __forceinline__ void store_rows(uint32_t stage, uint16_t* d, int pitch, int n, int hq,
+                                           int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t t = 8u * i + (static_cast<uint32_t>(lane) >> 2), c = lane & 3;
-    const uint4 v = ld_shared_v4(stage + 64u * t + 16u * (c ^ ((t >> 1) & 3u)));
-    if (static_cast<int>(t) < n)
-      st_global_cs_v4(d + static_cast<size_t>(t) * pitch + 8 * c, v);
+    const uint32_t t = 16u * hq + 4u * i + (static_cast<uint32_t>(lane) >> 3), c = lane & 7;
+    const uint4 v = ld_shared_v4(stage + 128u * t + 16u * (c ^ (t & 7u)));
+    if (static_cast<int>(t) < n) st_global_cs_v4(d + static_cast<size_t>(t) * pitch + 8 * c, v);
   }
-  __syncwarp();
 }
 
 // A value that is the same in all lanes of the warp, made known as such: it and
@@ -315,7 +323,8 @@ template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm_mx4_kernel(const __grid_constant__ CUtensorMap tm_w,
                            const __grid_constant__ CUtensorMap tm_x,
-                           const __grid_constant__ CUtensorMap tm_ws, Mx4GemmArgs p) {
+                           const __grid_constant__ CUtensorMap tm_ws,
+                           const __grid_constant__ CUtensorMap tm_d, Mx4GemmArgs p) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kSubs = kPair ? 2 : 1;           // sub-tiles per tile
   constexpr int kSubN = kBM * kCtas;             // columns of a sub-tile, M of the UMMA
@@ -370,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_ws);
+    tma_prefetch_desc(&tm_d);
   }
   grid_dependency_wait();
   grid_launch_dependents();
@@ -663,9 +673,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ epilogue ----
-    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t stage_addr = smem_u32(staging + (warp - 4) * kChunkBytes);
+    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns; two
+    // neighbours stage 32 tokens x 64 columns together, and one of their threads
+    // stores them by TMA (64-byte rows from each warp's own lanes made the large
+    // product 6 % slower)
+    const int q = warp & 3, half = (warp - 4) >> 2, hq = q & 1;
+    const int bar_id = 1 + ((warp - 4) >> 1);
+    const bool issuer = hq == 0 && lane == 0;
+    const uint32_t stage_addr = smem_u32(staging + ((warp - 4) >> 1) * 2 * kChunkBytes);
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
@@ -675,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int sub = 0; sub < kSubs; ++sub) {
         if (sub > 0 && c.n0 + kSubN >= p.N) break;
         const int a = kPair ? sub : acc;
-        if (!__all_sync(0xffffffffu, wait(&tfull[a], (acc_phase >> a) & 1u))) {
+        // both warps of a pair go on, or neither
+        if (!pair_barrier_and(bar_id, wait(&tfull[a], (acc_phase >> a) & 1u))) {
           aborted = true;
           break;
         }
@@ -701,13 +717,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           const int j = 64 * i + 32 * half;
-          if (any && j < n_tok)
-            store_chunk(m[i], stage_addr, p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N,
-                        n_tok - j, lane);
+          if (any && j < n_tok) {  // the same for both warps: N is a multiple of 64
+            if (issuer) tma_store_wait_read();
+            pair_barrier(bar_id);
+            stage_chunk(m[i], stage_addr, hq, lane);
+            fence_proxy_async();
+            pair_barrier(bar_id);
+            if (n_tok - j >= 32) {
+              if (issuer) tma_store_2d(&tm_d, stage_addr, n, c.row0 + j);
+            } else {  // rows past the segment belong to the next expert
+              store_rows(stage_addr, p.D + static_cast<size_t>(c.row0 + j) * p.N + n - 32 * hq, p.N,
+                         n_tok - j, hq, lane);
+            }
+          }
         }
       }
       if constexpr (!kPair) acc ^= 1;
     }
+    if (issuer) tma_store_wait();
   }
   __syncwarp();
   tc_fence_before();
@@ -738,8 +765,8 @@ bool mx4_use_pair(int64_t rows, int E) { return rows >= 64 * static_cast<int64_t
 
 template <bool kPair>
 static cudaError_t launch_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                              const CUtensorMap& tm_ws, const Mx4GemmArgs& a, int num_sms,
-                              cudaStream_t st) {
+                              const CUtensorMap& tm_ws, const CUtensorMap& tm_d,
+                              const Mx4GemmArgs& a, int num_sms, cudaStream_t st) {
   int dev = 0, optin = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -768,14 +795,14 @@ static cudaError_t launch_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, expert_gemm_mx4_kernel<kPair>, tm_w, tm_x, tm_ws, args);
+  return cudaLaunchKernelEx(&cfg, expert_gemm_mx4_kernel<kPair>, tm_w, tm_x, tm_ws, tm_d, args);
 }
 
 cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                                   const CUtensorMap& tm_ws, const Mx4GemmArgs& a, bool pair,
-                                   int num_sms, cudaStream_t st) {
-  return pair ? launch_mx4<true>(tm_w, tm_x, tm_ws, a, num_sms, st)
-              : launch_mx4<false>(tm_w, tm_x, tm_ws, a, num_sms, st);
+                                   const CUtensorMap& tm_ws, const CUtensorMap& tm_d,
+                                   const Mx4GemmArgs& a, bool pair, int num_sms, cudaStream_t st) {
+  return pair ? launch_mx4<true>(tm_w, tm_x, tm_ws, tm_d, a, num_sms, st)
+              : launch_mx4<false>(tm_w, tm_x, tm_ws, tm_d, a, num_sms, st);
 }
 
 }  // namespace moe

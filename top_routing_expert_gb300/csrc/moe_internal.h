@@ -234,8 +234,8 @@ int mx4_tile_tokens(int64_t rows, int E);
 // Whether it runs as the CTA-pair kernel (token boxes of half a tile).
 bool mx4_use_pair(int64_t rows, int E);
 cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                                   const CUtensorMap& tm_ws, const Mx4GemmArgs& a, bool pair,
-                                   int num_sms, cudaStream_t st);
+                                   const CUtensorMap& tm_ws, const CUtensorMap& tm_d,
+                                   const Mx4GemmArgs& a, bool pair, int num_sms, cudaStream_t st);
 cudaError_t launch_rank(const RankArgs& a, cudaStream_t st);
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_gather(const GatherArgs& a, int num_sms, cudaStream_t st);
