@@ -404,7 +404,7 @@ typedef struct {
 } moe_route_config;
 
 /* Grouped routing of fp32 logits [T,E] (for instance moe_route's logits_out).
- *   in : logits; select_bias [E] fp32 or NULL
+ *   in : logits; select_bias [E] fp32, finite, or NULL
  *   out: topk_idx, topk_w [T,k]; routed_counts [E], P [E] (mean over tokens
  *        of s_e / sum_e s_e) and aux [1] = E * sum_e routed_e/(T*k) * P_e,
  *        each or all NULL (with none of them the statistics are not formed).
@@ -421,7 +421,7 @@ MOE_API moe_status moe_route_grouped(const moe_shape* s, const moe_route_config*
  *        grad_topk_w [T,k]; grad_aux [1] with routed_counts [E] (the
  *        gradient of aux, routed_counts taken as constants), or NULL.
  *   out: grad_logits [T,E], every element written; 0 at masked experts.
- * An index outside [0,E) contributes nothing. n_groups, topk_groups and
+ * An index outside [0,E) contributes nothing; a token's others are distinct. n_groups, topk_groups and
  * group_top take no part. Needs no workspace. */
 MOE_API moe_status moe_route_grouped_bwd(const moe_shape* s, const moe_route_config* cfg,
                                          const float* logits, const int32_t* topk_idx,

@@ -27,23 +27,34 @@ constexpr int kV = 8;          // experts per lane
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLowest = 3.402823466e38f;  // -kLowest: fp32's lowest value
 
-// Keys order selection values as unsigned integers: the float's bits made
-// monotonic, their lowest 3 bits replaced by 7 - slot so that a lane's keys
-// differ and carry the slot. Smaller keys mark experts that come after every
-// regular one: masked experts of kept groups by index (16 + 255 - e, whose
-// lowest 3 bits are 7 - slot too), then experts of other groups (7 - slot).
-__device__ __forceinline__ uint32_t key_masked(int e) { return 16u + static_cast<uint32_t>(255 - e); }
-__device__ __forceinline__ uint32_t key_of(float c, int slot) {
-  const uint32_t u = __float_as_uint(c);
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return (o & ~7u) | static_cast<uint32_t>(7 - slot);
+// Keys order selection values as floats: the lowest 3 bits replaced by 7 - slot,
+// so that a lane's keys differ and carry the slot. Keys below kRegular mark
+// experts that come after every other one: masked experts of kept groups, by
+// index (their bits end in 7 - slot too), then experts that are not to be had.
+constexpr float kRegular = -2.9e38f;
+__device__ __forceinline__ float key_of(float c, int slot) {
+  return __uint_as_float((__float_as_uint(c) & ~7u) | static_cast<uint32_t>(7 - slot));
 }
-__device__ __forceinline__ bool key_regular(uint32_t key) { return key >= 512u; }
-__device__ __forceinline__ float key_value(uint32_t key) {
-  const uint32_t o = key & ~7u;
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+__device__ __forceinline__ float key_masked(int e) {  // -3.0e38 and a little below
+  return __uint_as_float(0xff61b000u + 8u * static_cast<uint32_t>(e) + static_cast<uint32_t>(7 - (e & 7)));
 }
+__device__ __forceinline__ float key_out(int slot) {  // -3.3e38 and a little below
+  return __uint_as_float(0xff784000u + static_cast<uint32_t>(7 - slot));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <int L, class T, class Op>
 __device__ __forceinline__ T lanes_reduce(T v, Op op) {
@@ -57,17 +68,242 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (L == 32) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
   return lanes_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
-template <int L>
-__device__ __forceinline__ uint32_t lanes_max_u32(uint32_t v) {
-  if constexpr (L == 32) return __reduce_max_sync(kFull, v);
-  return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-}
-
 __device__ __forceinline__ bool masked(float l) { return !(fabsf(l) < CUDART_INF_F); }
 
-// The lane's 8 logits of row t; masked past E or T.
+// ------------------------------------------------------------- fp64 ----
+// The choice of one token in fp64, by a whole warp (lane l: experts l, l + 32,
+// ...), then its weights. fp64 instructions run at 1/64 of the fp32 rate, so
+// comparisons are made on the values' bits as ordered integers.
+__device__ __forceinline__ long long order64(double v) {
+  const long long b = __double_as_longlong(v);
+  return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+
+// The k chosen experts in pick[] (shared memory) to outputs; lanes sub, sub + L,
+// ... of the token take slots sub, sub + L, ...; logits from `row`; softmax
+// scores are exp(l - m) iz.
+template <int L>
+__device__ __forceinline__ void write_slots(const GroupedArgs& a, int64_t t, const int* pick,
+                                            const float* row, float m, float iz, int sub, bool write,
+                                            int* cnt) {
+  constexpr int kPer = (kMaxTopK + L - 1) / L;
+  constexpr int kLanes = L < kMaxTopK ? L : kMaxTopK;  // lanes that hold slots
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  int e[kPer];
+  float x[kPer], w[kPer];
+  float top = -CUDART_INF_F;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int j = sub + q * L;
+    const bool in = j < a.k;
+    e[q] = in ? pick[j] : 0;
+    x[q] = in ? row[e[q]] : -CUDART_INF_F;
+    if (masked(x[q])) x[q] = -CUDART_INF_F;
+    top = fmaxf(top, x[q]);
+  }
+  float f = a.scale;
+  if (a.renormalize) {
+    // Weights are ratios then: softmax scores are taken relative to the largest
+    // chosen logit, and so are sigmoid scores far below zero (where 1 + exp(l)
+    // is 1), which would underflow.
+    top = lanes_reduce<kLanes>(top, [](float u, float v) { return fmaxf(u, v); });
+    const bool ratio = softmax || top < -40.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const float y = ratio ? exp2_approx((x[q] - top) * kLog2e) : rcp_approx(1.f + exp2_approx(-x[q] * kLog2e));
+      w[q] = x[q] == -CUDART_INF_F ? 0.f : y;
+      sum += w[q];
+    }
+    sum = lanes_sum<kLanes>(sum);
+    f = sum > 0.f ? f * rcp_approx(sum) : 0.f;
+  } else {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const float y = softmax ? exp2_approx((x[q] - m) * kLog2e) * iz
+                              : rcp_approx(1.f + exp2_approx(-x[q] * kLog2e));
+      w[q] = x[q] == -CUDART_INF_F ? 0.f : y;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int j = sub + q * L;
+    if (write && j < a.k) {
+      a.topk_idx[t * a.k + j] = e[q];
+      a.topk_w[t * a.k + j] = w[q] * f;
+      if (cnt != nullptr) atomicAdd(&cnt[e[q]], 1);
+    }
+  }
+}
+
+struct ExactScratch {     // shared memory of one warp
+  long long* cs;          // [kMaxExperts]: ordered fp64 values
+  float* cf;              // [kMaxExperts]: fp32 values
+  uint8_t* list;          // [kMaxExperts]: experts to evaluate
+  int* pick;              // [kMaxTopK]
+};
+
+__device__ __noinline__ double score64(float x, float m, bool softmax) {
+  const double y = exp(softmax ? static_cast<double>(x) - static_cast<double>(m) : -static_cast<double>(x));
+  return softmax ? y : 1.0 / (1.0 + y);
+}
+
+// Only experts that may matter are evaluated in fp64: those whose fp32 value is
+// within `slack` of the group_top-th of their group, then those within it of a
+// lower bound of the kept groups' k-th. All others rank below them whatever the
+// error. (A softmax with a bias needs its fp64 sum too, hence all exponentials.)
+// Few tokens come here, on any SM, so the code is kept short: fetching
+// instructions for the first time costs more than running them.
+__device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const ExactScratch& sc,
+                                         int* cnt) {
+  const int lane = threadIdx.x & 31;
+  const int E = a.E, S = a.E / a.n_groups;
+  const float* row = a.logits + static_cast<int64_t>(t) * E;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const bool all = softmax && a.bias != nullptr;
+  const long long kInf = order64(-CUDART_INF);
+  const long long kNever = -0x7fffffffffffffffll - 1;  // not evaluated: below -inf
+  float m = -CUDART_INF_F, smax = 0.f, z = 0.f, big = 0.f;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    const float x = row[e];
+    sc.cf[e] = masked(x) ? -CUDART_INF_F : x;
+    m = fmaxf(m, sc.cf[e]);
+  }
+  m = lanes_max<32>(m);
+  if (m == -CUDART_INF_F) m = 0.f;  // nothing unmasked
+  double z64 = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {  // cf: the scores, -inf where masked
+    const float x = sc.cf[e];
+    sc.cs[e] = x == -CUDART_INF_F ? kInf : kNever;
+    if (x != -CUDART_INF_F) {
+      const float y = softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
+      sc.cf[e] = y;
+      z += y;
+      smax = fmaxf(smax, y);
+      if (all) z64 += score64(x, m, true);
+    }
+  }
+  z = lanes_sum<32>(z);
+  smax = lanes_max<32>(smax);
+  const float iz = softmax && z > 0.f ? 1.f / z : 0.f;
+  if (all) z64 = lanes_reduce<32>(z64, [](double x, double y) { return x + y; });
+  // softmax scores are compared as exp(l - m) where nothing is added to them
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32)
+    if (a.bias != nullptr && sc.cf[e] != -CUDART_INF_F) {
+      sc.cf[e] = fmaf(sc.cf[e], all ? iz : 1.f, a.bias[e]);
+      big = fmaxf(big, fabsf(sc.cf[e]));
+    }
+  big = fmaxf(lanes_max<32>(big), all ? smax * iz : smax);
+  // fp32 errors are within 2^-18 of the largest value (2^-14 where the logits are
+  // so low that exp's argument is what errs)
+  const float slack = big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
+  __syncwarp();
+  uint32_t kept = 0xffffffffu;
+  int n = 0;
+  // phase 0 settles the groups, phase 1 the experts
+#pragma unroll 1
+  for (int phase = a.n_groups > 1 ? 0 : 1; phase < 2; ++phase) {
+    float bound = -CUDART_INF_F;  // lane g: of group g
+    if (phase == 0) {
+      if (lane < a.n_groups) {
+        float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+          const float v = sc.cf[lane * S + q];
+          v2 = fmaxf(v2, fminf(v, v1));
+          v1 = fmaxf(v1, v);
+        }
+        bound = a.group_top == 2 ? v2 : v1;
+      }
+    } else {
+      // the k-th largest of the lanes' own maxima
+      float own = -CUDART_INF_F;
+#pragma unroll 1
+      for (int e = lane; e < E; e += 32)
+        if ((kept >> (a.n_groups > 1 ? e / S : 0)) & 1u) own = fmaxf(own, sc.cf[e]);
+#pragma unroll 1
+      for (int j = 0; j < a.k; ++j) {
+        bound = lanes_max<32>(own);
+        const unsigned who = __ballot_sync(kFull, own == bound);
+        if (lane == __ffs(static_cast<int>(who)) - 1) own = -CUDART_INF_F;
+      }
+    }
+    // the candidates, in order of their index
+    n = 0;
+#pragma unroll 1
+    for (int b = 0; b < E; b += 32) {
+      const int e = b + lane, g = e < E && a.n_groups > 1 ? e / S : 0;
+      const float lim = phase == 0 ? __shfl_sync(kFull, bound, g) : bound;
+      const bool in = e < E && sc.cf[e] >= lim - slack && (phase == 0 || ((kept >> g) & 1u));
+      const unsigned who = __ballot_sync(kFull, in);
+      if (in) sc.list[n + __popc(who & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
+      n += __popc(who);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int q = lane; q < n; q += 32) {
+      const int e = sc.list[q];
+      if (sc.cs[e] == kNever) {
+        double v = score64(row[e], m, softmax);
+        if (all) v /= z64;
+        if (a.bias != nullptr) v += static_cast<double>(a.bias[e]);
+        sc.cs[e] = order64(v);
+      }
+    }
+    __syncwarp();
+    if (phase == 0) {
+      long long v1 = kInf, v2 = kInf;
+      if (lane < a.n_groups) {
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+          const long long v = sc.cs[lane * S + q];
+          v2 = max(v2, min(v, v1));
+          v1 = max(v1, v);
+        }
+        if (a.group_top == 2)  // order64 is its own inverse
+          v1 = order64(__longlong_as_double(order64(__longlong_as_double(v1))) +
+                       __longlong_as_double(order64(__longlong_as_double(v2))));
+      }
+      int ahead = 0;
+#pragma unroll 1
+      for (int h = 0; h < a.n_groups; ++h) {
+        const long long o = __shfl_sync(kFull, v1, h);
+        ahead += (o > v1 || (o == v1 && h < lane)) ? 1 : 0;
+      }
+      kept = __ballot_sync(kFull, lane < a.n_groups && ahead < a.topk_groups);
+    }
+  }
+  // the candidates' ranks: ties go to the lower index, which comes first here
+#pragma unroll 1
+  for (int q = lane; q < n; q += 32) {
+    const int e = sc.list[q];
+    const long long v = sc.cs[e];
+    int rank = 0;
+#pragma unroll 1
+    for (int r = 0; r < n; ++r) {
+      const long long o = sc.cs[sc.list[r]];
+      rank += (o > v || (o == v && r < q)) ? 1 : 0;
+    }
+    if (rank < a.k) sc.pick[rank] = e;
+  }
+  __syncwarp();
+  write_slots<32>(a, t, sc.pick, row, m, iz, lane, true, cnt);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------- kernel ----
+
+// The lane's 8 logits of row t, the type's lowest value past E or T.
 template <int L>
 __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64_t t, bool valid,
                                          int E, int sub, float (&l)[kV]) {
@@ -76,7 +312,7 @@ __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64
   if ((E & 3) == 0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float4 v = make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+      float4 v = make_float4(-kLowest, -kLowest, -kLowest, -kLowest);
       if (valid && e0 + 4 * h < E) v = __ldg(reinterpret_cast<const float4*>(row + e0 + 4 * h));
       l[4 * h] = v.x;
       l[4 * h + 1] = v.y;
@@ -85,238 +321,267 @@ __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) l[i] = valid && e0 + i < E ? __ldg(row + e0 + i) : -CUDART_INF_F;
+    for (int i = 0; i < kV; ++i) l[i] = valid && e0 + i < E ? __ldg(row + e0 + i) : -kLowest;
   }
 }
 
-// ------------------------------------------------------------- fp64 ----
-// The same token decided in fp64: slot j's expert ends up in lane j of the
-// token's lanes (and in every 8th lane when L < 8, see `pick`).
-template <int L>
-__device__ __noinline__ void route_exact(const GroupedArgs& a, const float (&l)[kV], int sub,
-                                         double* cs, double* gv, int* pick) {
-  double c[kV];
-  double m = -CUDART_INF;
-  if (a.score == MOE_SCORE_SOFTMAX) {
+// Masked experts of the lane (bits), their logits set to the lowest value. A
+// multiply-add per pair of logits finds whether there is any.
+__device__ __forceinline__ uint32_t find_masked(float (&l)[kV], uint32_t& status) {
+  uint64_t chk = f32x2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
-      if (!masked(l[i])) m = fmax(m, static_cast<double>(l[i]));
-    m = lanes_reduce<L>(m, [](double x, double y) { return fmax(x, y); });
-  }
-  double z = 0.0;
+  for (int i = 0; i < kV; i += 2) chk = f32x2_fma(f32x2(l[i], l[i + 1]), f32x2(0.f, 0.f), chk);
+  float c0, c1;
+  f32x2_get(chk, c0, c1);
+  if (!__any_sync(kFull, !(c0 + c1 == 0.f))) return 0u;
+  uint32_t mk = 0u;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const double x = l[i];
+  for (int i = 0; i < kV; ++i)
     if (masked(l[i])) {
-      c[i] = 0.0;
-    } else if (a.score == MOE_SCORE_SOFTMAX) {
-      c[i] = exp(x - m);
-      z += c[i];
-    } else {
-      c[i] = 1.0 / (1.0 + exp(-x));
+      mk |= 1u << i;
+      if (l[i] != -CUDART_INF_F) status |= MOE_DEV_NONFINITE;
+      l[i] = -kLowest;
     }
-  }
-  if (a.score == MOE_SCORE_SOFTMAX) {
-    z = lanes_reduce<L>(z, [](double x, double y) { return x + y; });
-#pragma unroll
-    for (int i = 0; i < kV; ++i) c[i] = z > 0.0 ? c[i] / z : 0.0;
-  }
-#pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int e = sub * kV + i;
-    if (masked(l[i])) c[i] = -CUDART_INF;
-    else if (a.bias != nullptr && e < a.E) c[i] += static_cast<double>(a.bias[e]);
-    if (e < a.E) cs[e] = c[i];
-  }
-  __syncwarp();
-  uint32_t kept = 0xffffffffu;
-  const int S = a.E / a.n_groups;
-  if (a.n_groups > 1) {
-    for (int g = sub; g < a.n_groups; g += L) {
-      double v1 = -CUDART_INF, v2 = -CUDART_INF;
-      for (int q = 0; q < S; ++q) {
-        const double v = cs[g * S + q];
-        if (v > v1) {
-          v2 = v1;
-          v1 = v;
-        } else if (v > v2) {
-          v2 = v;
-        }
-      }
-      gv[g] = a.group_top == 2 ? v1 + v2 : v1;
-    }
-    __syncwarp();
-    kept = 0u;
-    for (int g = sub; g < a.n_groups; g += L) {
-      int ahead = 0;
-      for (int h = 0; h < a.n_groups; ++h)
-        ahead += (gv[h] > gv[g] || (gv[h] == gv[g] && h < g)) ? 1 : 0;
-      if (ahead < a.topk_groups) kept |= 1u << g;
-    }
-    kept = lanes_reduce<L>(kept, [](uint32_t x, uint32_t y) { return x | y; });
-  }
-  uint32_t left = 0;
-#pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int e = sub * kV + i;
-    if (e < a.E && ((kept >> (a.n_groups > 1 ? e / S : 0)) & 1u)) left |= 1u << i;
-  }
-  for (int j = 0; j < a.k; ++j) {
-    double best = -CUDART_INF;
-    int at = 1 << 20;
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-      if ((left >> i) & 1u) {
-        const int e = sub * kV + i;
-        if (at == (1 << 20) || c[i] > best) {
-          best = c[i];
-          at = e;
-        }
-      }
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-      const double ob = __shfl_xor_sync(kFull, best, o);
-      const int oa = __shfl_xor_sync(kFull, at, o);
-      const bool take = oa != (1 << 20) && (at == (1 << 20) || ob > best || (ob == best && oa < at));
-      if (take) {
-        best = ob;
-        at = oa;
-      }
-    }
-    if (at / kV == sub) left &= ~(1u << (at % kV));
-    if (sub == 0) pick[j] = at;
-  }
-  __syncwarp();
+  return mk;
 }
 
-// ------------------------------------------------------------- kernel ----
+// The lane's scores in pairs (softmax: exp(l - m), not yet divided by their sum
+// over the row), 0 where masked.
+template <int L>
+__device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool softmax,
+                                       uint64_t (&s)[kV / 2], float& m) {
+  m = 0.f;
+  float x[kV];
+  if (softmax) {
+    m = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
+    m = lanes_max<L>(m);
+#pragma unroll
+    for (int i = 0; i < kV; i += 2)
+      f32x2_get(f32x2_mul(f32x2_add(f32x2(l[i], l[i + 1]), f32x2(-m, -m)), f32x2(kLog2e, kLog2e)), x[i],
+                x[i + 1]);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) x[i] = exp2_approx(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kV; i += 2) {
+      float y0, y1;
+      f32x2_get(f32x2_mul(f32x2(l[i], l[i + 1]), f32x2(-kLog2e, -kLog2e)), y0, y1);
+      f32x2_get(f32x2_add(f32x2(exp2_approx(y0), exp2_approx(y1)), f32x2(1.f, 1.f)), y0, y1);
+      x[i] = rcp_approx(y0);
+      x[i + 1] = rcp_approx(y1);
+    }
+  }
+  if (mk != 0u) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+      if ((mk >> i) & 1u) x[i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kV; i += 2) s[i / 2] = f32x2(x[i], x[i + 1]);
+}
+__device__ __forceinline__ float pairs_sum(const uint64_t (&s)[kV / 2]) {
+  float a, b;
+  f32x2_get(f32x2_add(f32x2_add(s[0], s[1]), f32x2_add(s[2], s[3])), a, b);
+  return a + b;
+}
 
 template <int L>
-__global__ void __launch_bounds__(kThreads) route_grouped_kernel(GroupedArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) route_grouped_kernel(const __grid_constant__ GroupedArgs a) {
   constexpr int kTok = 32 / L;                       // tokens per warp
-  constexpr int kGmax = L * kV < 32 ? L * kV : 32;   // groups per token at most
-  __shared__ double sh_c[kWarps][kTok * L * kV];
-  __shared__ double sh_g[kWarps][kTok * kGmax];
-  __shared__ int sh_pick[kWarps][kTok * kMaxTopK];
-  __shared__ float sh_p[kWarps][kTok][L * kV];
-  __shared__ int sh_cnt[L * kV];
+  constexpr int kCols = L * kV;
+  constexpr int kGmax = kCols < 32 ? kCols : 32;     // groups per token at most
+  constexpr int kList = 32;                          // tokens a warp puts off
+  // per warp: logits and selection values of its tokens; route_exact's values
+  __shared__ __align__(16) float sh_row[kWarps][2][kTok][kCols];
+  __shared__ float sh_g[kWarps][kTok][kGmax];
+  __shared__ uint8_t sh_eval[kWarps][kMaxExperts];
+  __shared__ int sh_pick[kWarps][kTok][kMaxTopK];
+  __shared__ int sh_list[kWarps][kList];
+  __shared__ __align__(16) float sh_bias[kCols];
+  __shared__ float sh_p[kWarps][kTok][kCols];        // sums of p at the end; route_exact's fp32 values
+  __shared__ int sh_cnt[kCols];
+  static_assert(sizeof(sh_row[0]) == kMaxExperts * sizeof(long long), "route_exact's scratch");
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane & (L - 1), tok = lane / L;
   const int E = a.E, G = a.n_groups, S = E / G;
   const bool stats = a.tile_cnt != nullptr;
-  double* cs = sh_c[warp] + tok * L * kV;
-  float* csf = reinterpret_cast<float*>(cs);
-  double* gv = sh_g[warp] + tok * kGmax;
-  float* gvf = reinterpret_cast<float*>(gv);
-  int* pick = sh_pick[warp] + tok * kMaxTopK;
-  if (stats)
-    for (int i = tid; i < L * kV; i += kThreads) sh_cnt[i] = 0;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  for (int i = tid; i < kCols; i += kThreads) {
+    sh_cnt[i] = 0;
+    sh_bias[i] = a.bias != nullptr && i < E ? a.bias[i] : 0.f;
+  }
   if (blockIdx.x == 0 && tid == 0 && a.ticket != nullptr) *a.ticket = 0u;
   __syncthreads();
-  float b[kV], psum[kV];
+  float* row = sh_row[warp][0][tok];
+  float* cs = sh_row[warp][1][tok];
+  float* gv = sh_g[warp][tok];
+  int* pick = sh_pick[warp][tok];
+  int* cnt = stats ? sh_cnt : nullptr;
+  // which of the lane's experts exist, and their groups (a byte each)
+  uint32_t exist = 0;
+  uint64_t gids = 0;
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    const int e = sub * kV + i;
-    b[i] = a.bias != nullptr && e < E ? a.bias[e] : 0.f;
-    psum[i] = 0.f;
-  }
-  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  uint32_t bits = 0;
-  const int per_pass = gridDim.x * kWarps * kTok;
-  for (int base = (blockIdx.x * kWarps + warp) * kTok; base < a.T; base += per_pass) {
-    const int t = base + tok;
+  for (int i = 0; i < kV; ++i)
+    if (sub * kV + i < E) {
+      exist |= 1u << i;
+      gids |= static_cast<uint64_t>((sub * kV + i) / S) << (8 * i);
+    }
+  // Lanes per group where groups are whole lanes, a power of two of them.
+  const int gl = G > 1 && S % kV == 0 && ((S / kV) & (S / kV - 1)) == 0 ? S / kV : 0;
+  uint64_t psum[kV / 2];
+#pragma unroll
+  for (int i = 0; i < kV / 2; ++i) psum[i] = f32x2(0.f, 0.f);
+  uint32_t status = 0;
+  int n_list = 0;
+  auto flush = [&]() {
+    __syncwarp();
+    for (int q = 0; q < n_list; ++q)
+      route_exact(a, sh_list[warp][q],
+                  ExactScratch{reinterpret_cast<long long*>(sh_row[warp]), sh_p[warp][0], sh_eval[warp],
+                               sh_pick[warp][0]},
+                  cnt);
+    n_list = 0;
+  };
+
+  const int64_t per_pass = static_cast<int64_t>(gridDim.x) * kWarps * kTok;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTok;
+  float next[kV];
+  load_row<L>(a.logits, first + tok < a.T ? first + tok : 0, first + tok < a.T, E, sub, next);
+  for (int64_t base = first; base < a.T; base += per_pass) {
+    const int64_t t = base + tok;
     const bool valid = t < a.T;
-    float l[kV], s[kV];
-    load_row<L>(a.logits, valid ? t : 0, valid, E, sub, l);
-    // scores
-    float m = 0.f;
+    float l[kV], c[kV];
+    uint64_t s[kV / 2];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) l[i] = next[i];
+    // the next token's row is fetched while this one is worked on
+    const int64_t tn = t + per_pass;
+    load_row<L>(a.logits, tn < a.T ? tn : 0, tn < a.T, E, sub, next);
+    const uint32_t mk = find_masked(l, status);
+    float m, smax, iz = 0.f;
+    scores<L>(l, mk, softmax, s, m);
+    if (softmax || stats) {
+      const float z = lanes_sum<L>(pairs_sum(s));
+      iz = z > 0.f ? rcp_approx(z) : 0.f;
+    }
     if (softmax) {
-      m = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) s[i] = f32x2_mul(s[i], f32x2(iz, iz));
+      smax = iz;  // exp(0) / z
+    }
+    if (stats) {
+      const float f = !valid ? 0.f : softmax ? 1.f : iz;
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) psum[i] = f32x2_fma(s[i], f32x2(f, f), psum[i]);
+    }
+    {
+      const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(sh_bias + sub * kV);
+      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(sh_bias + sub * kV + 4);
+      if (!softmax) {
+#pragma unroll
+        for (int i = 0; i < kV / 2; ++i) f32x2_get(s[i], c[2 * i], c[2 * i + 1]);
+        smax = fmaxf(fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3])), fmaxf(fmaxf(c[4], c[5]), fmaxf(c[6], c[7])));
+        smax = lanes_max<L>(smax);
+      }
+      f32x2_get(f32x2_add(s[0], b0.x), c[0], c[1]);
+      f32x2_get(f32x2_add(s[1], b0.y), c[2], c[3]);
+      f32x2_get(f32x2_add(s[2], b1.x), c[4], c[5]);
+      f32x2_get(f32x2_add(s[3], b1.y), c[6], c[7]);
+    }
+    if (mk != 0u) {
 #pragma unroll
       for (int i = 0; i < kV; ++i)
-        if (!masked(l[i])) m = fmaxf(m, l[i]);
-      m = lanes_max<L>(m);
+        if ((mk >> i) & 1u) {
+          c[i] = -CUDART_INF_F;
+          l[i] = -CUDART_INF_F;
+        }
     }
-    float z = 0.f, smax = 0.f;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      if (masked(l[i])) {
-        if (valid && sub * kV + i < E && l[i] != -CUDART_INF_F) bits |= MOE_DEV_NONFINITE;
-        s[i] = 0.f;
-      } else {
-        s[i] = softmax ? __expf(l[i] - m) : __fdividef(1.f, 1.f + __expf(-l[i]));
-      }
-      z += s[i];
-      smax = fmaxf(smax, s[i]);
-    }
-    z = lanes_sum<L>(z);
-    if (softmax) {
-      const float iz = z > 0.f ? 1.f / z : 0.f;
-#pragma unroll
-      for (int i = 0; i < kV; ++i) s[i] *= iz;
-      smax = iz;  // exp(0) / z
-    } else {
-      smax = lanes_max<L>(smax);
-    }
-    // Selection values. A score's error is within 2^-21 of the row's largest
-    // score (2^-17 where all logits are far below zero and the exponent's
-    // rounding counts), the sum adds its own rounding, and the keys drop 3
-    // bits (2^-20): values closer than `near` are decided in fp64.
-    float c[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) c[i] = masked(l[i]) ? -CUDART_INF_F : s[i] + b[i];
+    *reinterpret_cast<float4*>(row + sub * kV) = make_float4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<float4*>(row + sub * kV + 4) = make_float4(l[4], l[5], l[6], l[7]);
+    // A score's error is within 2^-21 of the row's largest score (2^-17 where
+    // all logits are far below zero and the exponent's rounding counts), the
+    // bias adds a rounding, and the keys drop 3 bits (2^-20): values closer
+    // than `near` are decided in fp64.
     const float near_abs = smax * (softmax || smax > 1e-3f ? 0x1p-20f : 0x1p-16f);
     auto near = [&](float x, float y) {
-      return fabsf(x - y) <= near_abs + 0x1p-19f * fmaxf(fabsf(x), fabsf(y));
+      return fabsf(x - y) < fmaf(0x1p-19f, fmaxf(fabsf(x), fabsf(y)), near_abs);
     };
     bool unsure = smax < 1e-30f;
-    uint32_t kept = 0xffffffffu;
+    uint32_t avail = exist;
     if (G > 1) {
+      float v = 0.f;
+      int g0 = 0, step = 0;
+      if (gl > 0) {
+        float v1 = c[0], v2 = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (sub * kV + i < E) csf[sub * kV + i] = c[i];
-      __syncwarp();
-      for (int g = sub; g < G; g += L) {
-        float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
-        for (int q = 0; q < S; ++q) {
-          const float v = csf[g * S + q];
-          v2 = fmaxf(v2, fminf(v, v1));
-          v1 = fmaxf(v1, v);
+        for (int i = 1; i < kV; ++i) {
+          v2 = fmaxf(v2, fminf(c[i], v1));
+          v1 = fmaxf(v1, c[i]);
         }
-        gvf[g] = a.group_top == 2 ? v1 + v2 : v1;
+        for (int o = 1; o < gl; o <<= 1) {
+          const float o1 = __shfl_xor_sync(kFull, v1, o), o2 = __shfl_xor_sync(kFull, v2, o);
+          v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
+          v1 = fmaxf(v1, o1);
+        }
+        v = a.group_top == 2 ? v1 + v2 : v1;
+        if ((sub & (gl - 1)) == 0 && sub / gl < G) gv[sub / gl] = v;
+        g0 = sub / gl;
+        step = G;  // the lane's own group alone
+      } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) cs[sub * kV + i] = c[i];
+        __syncwarp();
+        for (int g = sub; g < G; g += L) {
+          float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
+          for (int q = 0; q < S; ++q) {
+            const float x = cs[g * S + q];
+            v2 = fmaxf(v2, fminf(x, v1));
+            v1 = fmaxf(v1, x);
+          }
+          gv[g] = a.group_top == 2 ? v1 + v2 : v1;
+        }
+        g0 = sub;
+        step = L;
       }
       __syncwarp();
-      kept = 0u;
-      for (int g = sub; g < G; g += L) {
-        const float v = gvf[g];
+      uint32_t kept = 0u;
+      for (int g = g0; g < G; g += step) {
+        const float x = gv[g];
         int ahead = 0, sure = 0, maybe = 0;
         for (int h = 0; h < G; ++h) {
-          const float o = gvf[h];
-          ahead += (o > v || (o == v && h < g)) ? 1 : 0;
-          const bool close = v != -CUDART_INF_F && o != -CUDART_INF_F && near(o, v);
-          sure += (o > v && !close) ? 1 : 0;
-          maybe += (h != g && (o > v || close)) ? 1 : 0;
+          const float o = gv[h];
+          ahead += (o > x || (o == x && h < g)) ? 1 : 0;
+          const bool close = near(o, x);  // false where either is -inf: their difference is not finite
+          sure += (o > x && !close) ? 1 : 0;
+          maybe += (h != g && (o > x || close)) ? 1 : 0;
         }
         if (ahead < a.topk_groups) kept |= 1u << g;
-        unsure |= v != -CUDART_INF_F && sure < a.topk_groups && maybe >= a.topk_groups;
+        unsure |= x != -CUDART_INF_F && sure < a.topk_groups && maybe >= a.topk_groups;
       }
-      kept = lanes_reduce<L>(kept, [](uint32_t x, uint32_t y) { return x | y; });
-      __syncwarp();
-    }
-    uint32_t key[kV];
+      if (gl > 0) {
+        avail = kept != 0u ? exist : 0u;
+      } else {
+        kept = lanes_reduce<L>(kept, [](uint32_t x, uint32_t y) { return x | y; });
+        avail = 0u;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int e = sub * kV + i;
-      const bool in = e < E && ((kept >> (G > 1 ? e / S : 0)) & 1u);
-      key[i] = !in ? static_cast<uint32_t>(7 - i)
-                   : c[i] == -CUDART_INF_F ? key_masked(e)
-                                           : key_of(c[i], i);
+        for (int i = 0; i < kV; ++i)
+          avail |= ((kept >> ((gids >> (8 * i)) & 31u)) & 1u) << i;
+        avail &= exist;
+      }
+    }
+    float key[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) key[i] = key_of(c[i], i);
+    if (avail != 0xffu || mk != 0u) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        key[i] = !((avail >> i) & 1u) ? key_out(i) : ((mk >> i) & 1u) ? key_masked(sub * kV + i) : key[i];
     }
     // the lane's keys, largest first (Batcher's odd-even merge sort of 8)
     auto swap = [&](int x, int y) {
-      const uint32_t hi = max(key[x], key[y]), lo = min(key[x], key[y]);
+      const float hi = fmaxf(key[x], key[y]), lo = fminf(key[x], key[y]);
       key[x] = hi;
       key[y] = lo;
     };
@@ -326,83 +591,41 @@ __global__ void __launch_bounds__(kThreads) route_grouped_kernel(GroupedArgs a) 
     swap(0, 4); swap(1, 5); swap(2, 6); swap(3, 7);
     swap(2, 4); swap(3, 5);
     swap(1, 2); swap(3, 4); swap(5, 6);
-    uint32_t prev = 0;
+    float prev = CUDART_INF_F;
     for (int j = 0; j <= a.k; ++j) {
-      const uint32_t best = lanes_max_u32<L>(key[0]);
-      if (j > 0 && key_regular(prev) && key_regular(best))
-        unsure |= near(key_value(prev), key_value(best));
+      const float best = lanes_max<L>(key[0]);
+      // regular values in descending order (against the first, inf, false)
+      unsure |= best > kRegular && near(prev, best);
       prev = best;
-      const uint32_t owners = __ballot_sync(kFull, key[0] == best);
-      const int first = __ffs(static_cast<int>(L == 32 ? owners : (owners >> (tok * L)) & ((1u << (L & 31)) - 1u))) - 1;
-      if (sub == first && j < a.k) {
-        pick[j] = sub * kV + 7 - static_cast<int>(best & 7u);
+      // the owner takes it out; two owners are a tie
+      const uint32_t owners = (__ballot_sync(kFull, key[0] == best) >> (tok * (L & 31))) & (0xffffffffu >> (32 - L));
+      unsure |= best > kRegular && (owners & (owners - 1u)) != 0u;
+      if (key[0] == best && j < a.k) {
+        pick[j] = sub * kV + 7 - static_cast<int>(__float_as_uint(best) & 7u);
 #pragma unroll
         for (int i = 0; i + 1 < kV; ++i) key[i] = key[i + 1];
-        key[kV - 1] = 0u;
+        key[kV - 1] = -CUDART_INF_F;
       }
     }
     __syncwarp();
-    unsure = unsure && valid;
-    // every lane of the token has to agree; all tokens of the warp follow
-    if (__any_sync(kFull, unsure)) {
-      const uint32_t who = __ballot_sync(kFull, unsure);
-      const bool mine = L == 32 ? who != 0 : ((who >> (tok * L)) & ((1u << (L & 31)) - 1u)) != 0;
-      int keep[kMaxTopK];
-#pragma unroll
-      for (int j = 0; j < kMaxTopK; ++j) keep[j] = j < a.k ? pick[j] : 0;
-      __syncwarp();
-      route_exact<L>(a, l, sub, cs, gv, pick);
-      if (!mine && sub == 0) {
-#pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j)
-          if (j < a.k) pick[j] = keep[j];
-      }
-      __syncwarp();
-    }
-    // weights of the chosen, from the logits again (cached): slot j in lane j
-    // of the token, or two passes and more where L < k
-    float den = 1.f;
-    float top = -CUDART_INF_F;
-    for (int j = sub; j < a.k; j += L) {
-      const float x = valid ? a.logits[static_cast<int64_t>(t) * E + pick[j]] : 0.f;
-      if (!masked(x)) top = fmaxf(top, x);
-    }
-    top = lanes_max<L>(top);
-    // Renormalised weights are ratios: softmax scores are taken relative to
-    // the largest chosen logit, and so are sigmoid scores far below zero
-    // (where 1 + exp(l) is 1), which would underflow.
-    const bool ratio = a.renormalize && (softmax || top < -40.f);
-    auto score_of = [&](float x) {
-      if (masked(x)) return 0.f;
-      if (ratio) return expf(x - top);
-      return softmax ? expf(x - m) / z : 1.f / (1.f + expf(-x));
-    };
-    if (a.renormalize) {
-      float sum = 0.f;
-      for (int j = sub; j < a.k; j += L)
-        sum += score_of(valid ? a.logits[static_cast<int64_t>(t) * E + pick[j]] : 0.f);
-      den = lanes_sum<L>(sum);
-    }
-    for (int j = sub; j < a.k; j += L) {
-      if (valid) {
-        const int e = pick[j];
-        const float w = score_of(a.logits[static_cast<int64_t>(t) * E + e]);
-        a.topk_idx[static_cast<int64_t>(t) * a.k + j] = e;
-        a.topk_w[static_cast<int64_t>(t) * a.k + j] = den > 0.f ? a.scale * w / den : 0.f;
-        if (stats) atomicAdd(&sh_cnt[e], 1);
-      }
-    }
-    if (stats) {
-      const float iz = softmax ? 1.f : (z > 0.f ? 1.f / z : 0.f);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) psum[i] += valid ? s[i] * iz : 0.f;
+    const uint32_t doubt = __ballot_sync(kFull, unsure && valid);
+    const bool mine = ((doubt >> (tok * (L & 31))) & (0xffffffffu >> (32 - L))) != 0u;
+    write_slots<L>(a, t, pick, row, m, iz, sub, valid && !mine, cnt);
+    if (doubt != 0u) {
+      const uint32_t heads = __ballot_sync(kFull, mine && sub == 0);
+      if (mine && sub == 0) sh_list[warp][n_list + __popc(heads & ((1u << lane) - 1u))] =
+          static_cast<int>(t);
+      n_list += __popc(heads);
+      if (n_list > kList - kTok) flush();
     }
     __syncwarp();
   }
-  if (bits) atomicOr(a.dev_status, bits);
+  flush();
+  if (status) atomicOr(a.dev_status, status);
   if (stats) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) sh_p[warp][tok][sub * kV + i] = psum[i];
+    for (int i = 0; i < kV / 2; ++i)
+      f32x2_get(psum[i], sh_p[warp][tok][sub * kV + 2 * i], sh_p[warp][tok][sub * kV + 2 * i + 1]);
     __syncthreads();
     for (int e = tid; e < E; e += kThreads) {
       float p = 0.f;
@@ -425,8 +648,9 @@ __global__ void __launch_bounds__(kThreads) route_grouped_kernel(GroupedArgs a) 
 // h_e = grad_aux E f_e / T, p = s / sum s:
 //   softmax  dl_e += p_e (h_e - sum p h);  sigmoid  dl_e += p_e (1 - s_e) (h_e - sum p h)
 template <int L>
-__global__ void __launch_bounds__(kThreads) route_grouped_bwd_kernel(GroupedBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __grid_constant__ GroupedBwdArgs a) {
   constexpr int kTok = 32 / L;
+  constexpr int kPer = (kMaxTopK + L - 1) / L;  // chosen slots per lane: sub, sub + L, ...
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -434,129 +658,161 @@ __global__ void __launch_bounds__(kThreads) route_grouped_bwd_kernel(GroupedBwdA
   const int E = a.E;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX, aux = a.grad_aux != nullptr;
   const bool need_p = aux || (softmax && !a.renormalize);  // the whole row's scores
-  float h[kV];
-  if (aux) {
-    const float f = *a.grad_aux * (static_cast<float>(E) / (static_cast<float>(a.T) * static_cast<float>(a.T) * static_cast<float>(a.k)));
+  __shared__ __align__(16) float sh_row[kWarps][kTok][L * kV];
+  uint64_t h[kV / 2];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int e = sub * kV + i;
-      h[i] = e < E ? f * static_cast<float>(a.routed[e]) : 0.f;
+  for (int i = 0; i < kV / 2; ++i) h[i] = f32x2(0.f, 0.f);
+  if (aux) {
+    const float T = static_cast<float>(a.T);
+    const float f = *a.grad_aux * (static_cast<float>(E) / T) / (T * static_cast<float>(a.k));
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) {
+      const int e = sub * kV + 2 * i;
+      h[i] = f32x2(e < E ? f * static_cast<float>(a.routed[e]) : 0.f,
+                   e + 1 < E ? f * static_cast<float>(a.routed[e + 1]) : 0.f);
     }
   }
-  const int per_pass = gridDim.x * kWarps * kTok;
-  for (int base = (blockIdx.x * kWarps + warp) * kTok; base < a.T; base += per_pass) {
-    const int t = base + tok;
-    const bool valid = t < a.T;
-    float l[kV], s[kV], grad[kV];
-    load_row<L>(a.logits, valid ? t : 0, valid, E, sub, l);
-    float m = -CUDART_INF_F, z = 0.f;
-    if (softmax) {
+  uint32_t status = 0;  // the forward has reported
+  const int64_t per_pass = static_cast<int64_t>(gridDim.x) * kWarps * kTok;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTok;
+  // The next token's row and chosen logits, and the slots of the one after it,
+  // are fetched while one is worked on. The row itself is not needed where only
+  // chosen experts have a gradient.
+  float next[kV], next_g[kPer], next_x[kPer], after_g[kPer];
+  int next_e[kPer], after_e[kPer];
 #pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (!masked(l[i])) m = fmaxf(m, l[i]);
-      m = lanes_max<L>(m);
-    }
-    if (need_p) {
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        s[i] = masked(l[i]) ? 0.f
-                            : softmax ? __expf(l[i] - m) : __fdividef(1.f, 1.f + __expf(-l[i]));
-        z += s[i];
-      }
-      z = lanes_sum<L>(z);
-    }
-    const float iz = z > 0.f ? 1.f / z : 0.f;
-    // the chosen slots, in lanes sub, sub + L, ...
-    constexpr int kPer = (kMaxTopK + L - 1) / L;
-    int ej[kPer];
-    float sj[kPer], slope[kPer], gj[kPer];
-    float top = -CUDART_INF_F;
-    float x[kPer];
+  for (int i = 0; i < kV; ++i) next[i] = 0.f;
+  auto fetch_slots = [&](int64_t t) {
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int j = sub + q * L;
-      ej[q] = -1;
-      gj[q] = 0.f;
-      x[q] = -CUDART_INF_F;
-      if (valid && j < a.k) {
-        ej[q] = a.topk_idx[static_cast<int64_t>(t) * a.k + j];
-        gj[q] = a.grad_w[static_cast<int64_t>(t) * a.k + j];
-        if (ej[q] < 0 || ej[q] >= E) ej[q] = -1;
-        else x[q] = a.logits[static_cast<int64_t>(t) * E + ej[q]];
-        if (masked(x[q])) ej[q] = -1;
-        else top = fmaxf(top, x[q]);
-      }
+      const bool in = t < a.T && j < a.k;
+      after_e[q] = in ? a.topk_idx[t * a.k + j] : -1;
+      after_g[q] = in ? a.grad_w[t * a.k + j] : 0.f;
     }
-    top = lanes_max<L>(top);
-    const bool ratio = a.renormalize && (softmax || top < -40.f);
-    float sum = 0.f;
+  };
+  auto fetch = [&](int64_t t) {  // the token whose slots were fetched last
+    if (need_p) load_row<L>(a.logits, t < a.T ? t : 0, t < a.T, E, sub, next);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      slope[q] = softmax ? 1.f : 1.f / (1.f + expf(x[q]));  // 1 - s
-      sj[q] = ej[q] < 0 ? 0.f
-                        : ratio ? expf(x[q] - top)
-                                : softmax ? expf(x[q] - m) * iz : 1.f / (1.f + expf(-x[q]));
-      sum += sj[q];
+      next_e[q] = after_e[q];
+      next_g[q] = after_g[q];
+      next_x[q] = -CUDART_INF_F;
+      if (next_e[q] >= 0 && next_e[q] < E) next_x[q] = a.logits[t * E + next_e[q]];
     }
-    float dj[kPer];
-    float dot = 0.f;
+  };
+  fetch_slots(first + tok);
+  fetch(first + tok);
+  fetch_slots(first + tok + per_pass);
+  for (int64_t base = first; base < a.T; base += per_pass) {
+    const int64_t t = base + tok;
+    const bool valid = t < a.T;
+    float l[kV];
+    uint64_t s[kV / 2], grad[kV / 2];
+    int ej[kPer];
+    float gj[kPer], x[kPer];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) l[i] = next[i];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      gj[q] = next_g[q];
+      x[q] = next_x[q];
+      ej[q] = masked(x[q]) ? -1 : next_e[q];
+    }
+    fetch(t + per_pass);
+    fetch_slots(t + 2 * per_pass);
+    float m = 0.f, iz = 0.f;
+    if (need_p) {
+      const uint32_t mk = find_masked(l, status);
+      scores<L>(l, mk, softmax, s, m);
+      const float z = lanes_sum<L>(pairs_sum(s));
+      iz = z > 0.f ? rcp_approx(z) : 0.f;
+    }
+    // the chosen slots: in the first lanes of the token
+    constexpr int kLanes = L < kMaxTopK ? L : kMaxTopK;
+    float top = 0.f;
     if (a.renormalize) {
-      sum = lanes_sum<L>(sum);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      top = -CUDART_INF_F;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q)
+        if (ej[q] >= 0) top = fmaxf(top, x[q]);
+      top = lanes_reduce<kLanes>(top, [](float u, float v) { return fmaxf(u, v); });
+    }
+    const bool ratio = a.renormalize && (softmax || top < -40.f);
+    const float shift = ratio ? top : m;
+    float sj[kPer], dj[kPer];
+    float sum = 0.f, dot = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const float y = exp2_approx((ratio || softmax ? x[q] - shift : -x[q]) * kLog2e);
+      sj[q] = ej[q] < 0 ? 0.f : ratio ? y : softmax ? y * iz : rcp_approx(1.f + y);
+      sum += sj[q];
+      dj[q] = softmax ? 1.f : rcp_approx(1.f + exp2_approx(x[q] * kLog2e));  // 1 - s
+    }
+    if (a.renormalize) {
+      sum = lanes_sum<kLanes>(sum);
+      const float inv = sum > 0.f ? rcp_approx(sum) : 0.f;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         sj[q] *= inv;
         dot += sj[q] * gj[q];
       }
-      dot = lanes_sum<L>(dot);
+      dot = lanes_sum<kLanes>(dot);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) dj[q] = a.scale * sj[q] * slope[q] * (gj[q] - dot);
+      for (int q = 0; q < kPer; ++q) dj[q] *= a.scale * sj[q] * (gj[q] - dot);
       dot = 0.f;
     } else {
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        dj[q] = a.scale * sj[q] * slope[q] * gj[q];
+        dj[q] *= a.scale * sj[q] * gj[q];
         dot += softmax ? dj[q] : 0.f;
       }
       dot = lanes_sum<L>(dot);
     }
-    // the whole row's part
-    float ph = 0.f;
-    if (aux) {
+    // the whole row's part: p_e slope_e (h_e - sum p h - dot)
 #pragma unroll
-      for (int i = 0; i < kV; ++i) ph += s[i] * iz * h[i];
-      ph = lanes_sum<L>(ph);
-    }
+    for (int i = 0; i < kV / 2; ++i) grad[i] = f32x2(0.f, 0.f);
+    if (need_p) {
+      float ph = 0.f;
+      if (aux) {
+        uint64_t acc = f32x2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      grad[i] = 0.f;
-      if (need_p) {
-        const float p = s[i] * iz;
-        if (softmax && !a.renormalize) grad[i] -= p * dot;
-        if (aux) grad[i] += p * (softmax ? 1.f : 1.f - s[i]) * (h[i] - ph);
+        for (int i = 0; i < kV / 2; ++i) acc = f32x2_fma(s[i], h[i], acc);
+        float u, v;
+        f32x2_get(acc, u, v);
+        ph = lanes_sum<L>(u + v) * iz;
+      }
+      if (softmax && !a.renormalize) ph += dot;
+      const float c = -ph * iz;
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) {
+        const uint64_t d = f32x2_fma(h[i], f32x2(iz, iz), f32x2(c, c));
+        const uint64_t p = softmax ? s[i] : f32x2_fma(f32x2_mul(s[i], f32x2(-1.f, -1.f)), s[i], s[i]);
+        grad[i] = f32x2_mul(p, d);
       }
     }
+    // the chosen experts' part is added in shared memory
+    float* row = sh_row[warp][tok];
+    *reinterpret_cast<ulonglong2*>(row + sub * kV) = make_ulonglong2(grad[0], grad[1]);
+    *reinterpret_cast<ulonglong2*>(row + sub * kV + 4) = make_ulonglong2(grad[2], grad[3]);
+    __syncwarp();
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
-      for (int j = 0; j < L && q * L + j < a.k; ++j) {
-        const int e = __shfl_sync(kFull, ej[q], tok * L + j);
-        const float d = __shfl_sync(kFull, dj[q], tok * L + j);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) grad[i] += e == sub * kV + i ? d : 0.f;
-      }
+      if (ej[q] >= 0) row[ej[q]] += dj[q];
+    __syncwarp();
     if (valid) {
-      float* row = a.grad_logits + static_cast<int64_t>(t) * E;
+      float* out = a.grad_logits + t * E;
       const int e0 = sub * kV;
       if ((E & 3) == 0) {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           if (e0 + 4 * q < E)
-            *reinterpret_cast<float4*>(row + e0 + 4 * q) =
-                make_float4(grad[4 * q], grad[4 * q + 1], grad[4 * q + 2], grad[4 * q + 3]);
+            __stcs(reinterpret_cast<float4*>(out + e0 + 4 * q),
+                   *reinterpret_cast<const float4*>(row + e0 + 4 * q));
       } else {
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-          if (e0 + i < E) row[e0 + i] = grad[i];
+          if (e0 + i < E) out[e0 + i] = row[e0 + i];
       }
     }
   }
