@@ -95,7 +95,7 @@ struct CombineArgs {
 
 // Grouped routing (csrc/moe_route_grouped.cu): its blocks' partial counts and
 // probability sums are [E][blocks], as the routing tiles' are.
-constexpr int kGroupedMaxBlocks = 456;  // three to an SM
+constexpr int kGroupedMaxBlocks = 608;  // four to an SM
 struct GroupedArgs {
   int T, E, k;
   int score, n_groups, topk_groups, group_top, renormalize;

@@ -7,13 +7,18 @@
 //   group value = sum of the group's g largest c; the best groups are kept
 //   idx = top-k of c over the kept groups, w_j = scale * s_j / sum_j s_j
 //
-// L lanes share one token and hold 8 consecutive experts each (L * 8 >= E), so
-// a warp routes 32 / L tokens at once and a row is read in 16-byte vectors.
+// Forward: P lanes share one token (32 P >= E), lane p holding the 16-byte pieces
+// p, p + P, ... of its row, 32 experts: a warp routes 32 / P tokens at once, and
+// what is done once per token (merging the lanes' lists, the weights) is shared
+// by many experts. Only values are kept in order, never pairs of value and
+// index: a second look at the row finds the experts whose values made it.
+// Gradient: L lanes share a token and hold 8 consecutive experts each.
 //
 // The choice is that of the formulas in 64 bits. Scores are computed in fp32,
 // and wherever two values that a decision compares are closer than the fp32
-// error allows, the token is decided again in fp64 (fp64 runs at a small
-// fraction of the fp32 rate here, so only those tokens pay for it).
+// error allows, the token is decided again in fp64 (fp64 runs at 1/64 of the
+// fp32 rate here, so only those tokens pay for it). Values that are equal are
+// always decided there, so ties need no care elsewhere.
 #include <math_constants.h>
 
 #include "moe_internal.h"
@@ -23,26 +28,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kV = 8;          // experts per lane
-constexpr int kWarps = 8;
+constexpr int kV = 8;          // experts per lane, gradient
+constexpr int kWarps = 8;      // gradient
 constexpr int kThreads = 32 * kWarps;
+constexpr int kFwdWarps = 4;
+constexpr int kFwdThreads = 32 * kFwdWarps;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLowest = 3.402823466e38f;  // -kLowest: fp32's lowest value
-
-// Keys order selection values as floats: the lowest 3 bits replaced by 7 - slot,
-// so that a lane's keys differ and carry the slot. Keys below kRegular mark
-// experts that come after every other one: masked experts of kept groups, by
-// index (their bits end in 7 - slot too), then experts that are not to be had.
-constexpr float kRegular = -2.9e38f;
-__device__ __forceinline__ float key_of(float c, int slot) {
-  return __uint_as_float((__float_as_uint(c) & ~7u) | static_cast<uint32_t>(7 - slot));
-}
-__device__ __forceinline__ float key_masked(int e) {  // -3.0e38 and a little below
-  return __uint_as_float(0xff61b000u + 8u * static_cast<uint32_t>(e) + static_cast<uint32_t>(7 - (e & 7)));
-}
-__device__ __forceinline__ float key_out(int slot) {  // -3.3e38 and a little below
-  return __uint_as_float(0xff784000u + static_cast<uint32_t>(7 - slot));
-}
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -75,6 +67,12 @@ __device__ __forceinline__ float lanes_max(float v) {
   }
   return lanes_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ bool masked(float l) { return !(fabsf(l) < CUDART_INF_F); }
 
 // ------------------------------------------------------------- fp64 ----
@@ -150,8 +148,34 @@ struct ExactScratch {     // shared memory of one warp
   int* pick;              // [kMaxTopK]
 };
 
+// exp of an fp32 difference in fp64: x = n ln 2 + r, |r| <= ln 2 / 2, and the
+// Taylor series of exp(r) to r^13 / 13! (the next term is below 2^-57). x is at
+// most 0 or held to a range where nothing overflows.
+__device__ __forceinline__ double exp64(double x) {
+  x = fmax(fmin(x, 700.0), -700.0);
+  const double n = rint(x * 1.4426950408889634);
+  // ln 2 in two parts, the first with zeros at its end
+  double r = fma(n, -0x1.62e42fp-1, x);
+  r = fma(n, -(0x1.df473de6af279p-26), r);
+  double y = 1.0 / 6227020800.0;
+  y = fma(y, r, 1.0 / 479001600.0);
+  y = fma(y, r, 1.0 / 39916800.0);
+  y = fma(y, r, 1.0 / 3628800.0);
+  y = fma(y, r, 1.0 / 362880.0);
+  y = fma(y, r, 1.0 / 40320.0);
+  y = fma(y, r, 1.0 / 5040.0);
+  y = fma(y, r, 1.0 / 720.0);
+  y = fma(y, r, 1.0 / 120.0);
+  y = fma(y, r, 1.0 / 24.0);
+  y = fma(y, r, 1.0 / 6.0);
+  y = fma(y, r, 0.5);
+  y = fma(y, r, 1.0);
+  y = fma(y, r, 1.0);
+  return __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
+}
+
 __device__ __noinline__ double score64(float x, float m, bool softmax) {
-  const double y = exp(softmax ? static_cast<double>(x) - static_cast<double>(m) : -static_cast<double>(x));
+  const double y = exp64(softmax ? static_cast<double>(x) - static_cast<double>(m) : -static_cast<double>(x));
   return softmax ? y : 1.0 / (1.0 + y);
 }
 
@@ -161,63 +185,75 @@ __device__ __noinline__ double score64(float x, float m, bool softmax) {
 // error. (A softmax with a bias needs its fp64 sum too, hence all exponentials.)
 // Few tokens come here, on any SM, so the code is kept short: fetching
 // instructions for the first time costs more than running them.
-__device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const ExactScratch& sc,
-                                         int* cnt) {
+// known: the kept groups where they are not in doubt, else 0.
+__device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t known,
+                                         const ExactScratch& sc, int* cnt) {
+  constexpr int kPer = kMaxExperts / 32;  // lane l: experts l, l + 32, ...
   const int lane = threadIdx.x & 31;
   const int E = a.E, S = a.E / a.n_groups;
+  const uint32_t inv = a.n_groups > 1 ? 65536u / static_cast<uint32_t>(S) + 1u : 0u;  // e / S = e inv >> 16, e < 256
   const float* row = a.logits + static_cast<int64_t>(t) * E;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   const bool all = softmax && a.bias != nullptr;
   const long long kInf = order64(-CUDART_INF);
   const long long kNever = -0x7fffffffffffffffll - 1;  // not evaluated: below -inf
   float m = -CUDART_INF_F, smax = 0.f, z = 0.f, big = 0.f;
-#pragma unroll 1
-  for (int e = lane; e < E; e += 32) {
-    const float x = row[e];
-    sc.cf[e] = masked(x) ? -CUDART_INF_F : x;
-    m = fmaxf(m, sc.cf[e]);
+  float x[kPer], c[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = lane + 32 * i < E ? row[lane + 32 * i] : -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (masked(x[i])) x[i] = -CUDART_INF_F;
+    m = fmaxf(m, x[i]);
   }
   m = lanes_max<32>(m);
   if (m == -CUDART_INF_F) m = 0.f;  // nothing unmasked
   double z64 = 0.0;
-#pragma unroll 1
-  for (int e = lane; e < E; e += 32) {  // cf: the scores, -inf where masked
-    const float x = sc.cf[e];
-    sc.cs[e] = x == -CUDART_INF_F ? kInf : kNever;
-    if (x != -CUDART_INF_F) {
-      const float y = softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
-      sc.cf[e] = y;
-      z += y;
-      smax = fmaxf(smax, y);
-      if (all) z64 += score64(x, m, true);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {  // the scores, -inf where masked
+    c[i] = x[i];
+    if (x[i] != -CUDART_INF_F) {
+      const float y = __expf(softmax ? x[i] - m : -x[i]);
+      c[i] = softmax ? y : __fdividef(1.f, 1.f + y);
+      z += c[i];
+      smax = fmaxf(smax, c[i]);
     }
+    if (lane + 32 * i < E) sc.cs[lane + 32 * i] = x[i] == -CUDART_INF_F ? kInf : kNever;
+  }
+  if (all) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32)
+      if (!masked(row[e])) z64 += score64(row[e], m, true);
+    z64 = lanes_reduce<32>(z64, [](double u, double v) { return u + v; });
   }
   z = lanes_sum<32>(z);
   smax = lanes_max<32>(smax);
   const float iz = softmax && z > 0.f ? 1.f / z : 0.f;
-  if (all) z64 = lanes_reduce<32>(z64, [](double x, double y) { return x + y; });
   // softmax scores are compared as exp(l - m) where nothing is added to them
-#pragma unroll 1
-  for (int e = lane; e < E; e += 32)
-    if (a.bias != nullptr && sc.cf[e] != -CUDART_INF_F) {
-      sc.cf[e] = fmaf(sc.cf[e], all ? iz : 1.f, a.bias[e]);
-      big = fmaxf(big, fabsf(sc.cf[e]));
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 32 * i;
+    if (a.bias != nullptr && c[i] != -CUDART_INF_F) {
+      c[i] = fmaf(c[i], all ? iz : 1.f, a.bias[e]);
+      big = fmaxf(big, fabsf(c[i]));
     }
+    if (e < E) sc.cf[e] = c[i];
+  }
   big = fmaxf(lanes_max<32>(big), all ? smax * iz : smax);
   // fp32 errors are within 2^-18 of the largest value (2^-14 where the logits are
   // so low that exp's argument is what errs)
   const float slack = big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
   __syncwarp();
-  uint32_t kept = 0xffffffffu;
+  uint32_t kept = a.n_groups > 1 ? known : 1u;
   int n = 0;
   // phase 0 settles the groups, phase 1 the experts
 #pragma unroll 1
-  for (int phase = a.n_groups > 1 ? 0 : 1; phase < 2; ++phase) {
-    float bound = -CUDART_INF_F;  // lane g: of group g
+  for (int phase = kept == 0u ? 0 : 1; phase < 2; ++phase) {
+    float bound = -CUDART_INF_F;  // phase 0, lane g: of group g
     if (phase == 0) {
       if (lane < a.n_groups) {
         float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
-#pragma unroll 1
+#pragma unroll 4
         for (int q = 0; q < S; ++q) {
           const float v = sc.cf[lane * S + q];
           v2 = fmaxf(v2, fminf(v, v1));
@@ -228,10 +264,11 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const Exac
     } else {
       // the k-th largest of the lanes' own maxima
       float own = -CUDART_INF_F;
-#pragma unroll 1
-      for (int e = lane; e < E; e += 32)
-        if ((kept >> (a.n_groups > 1 ? e / S : 0)) & 1u) own = fmaxf(own, sc.cf[e]);
-#pragma unroll 1
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t g = (static_cast<uint32_t>(lane + 32 * i) * inv) >> 16;
+        if ((kept >> (g & 31u)) & 1u) own = fmaxf(own, c[i]);
+      }
       for (int j = 0; j < a.k; ++j) {
         bound = lanes_max<32>(own);
         const unsigned who = __ballot_sync(kFull, own == bound);
@@ -240,11 +277,12 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const Exac
     }
     // the candidates, in order of their index
     n = 0;
-#pragma unroll 1
-    for (int b = 0; b < E; b += 32) {
-      const int e = b + lane, g = e < E && a.n_groups > 1 ? e / S : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = lane + 32 * i;
+      const uint32_t g = (static_cast<uint32_t>(e) * inv) >> 16;
       const float lim = phase == 0 ? __shfl_sync(kFull, bound, g) : bound;
-      const bool in = e < E && sc.cf[e] >= lim - slack && (phase == 0 || ((kept >> g) & 1u));
+      const bool in = e < E && c[i] >= lim - slack && (phase == 0 || ((kept >> (g & 31u)) & 1u));
       const unsigned who = __ballot_sync(kFull, in);
       if (in) sc.list[n + __popc(who & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
       n += __popc(who);
@@ -264,7 +302,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const Exac
     if (phase == 0) {
       long long v1 = kInf, v2 = kInf;
       if (lane < a.n_groups) {
-#pragma unroll 1
+#pragma unroll 4
         for (int q = 0; q < S; ++q) {
           const long long v = sc.cs[lane * S + q];
           v2 = max(v2, min(v, v1));
@@ -275,7 +313,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const Exac
                        __longlong_as_double(order64(__longlong_as_double(v2))));
       }
       int ahead = 0;
-#pragma unroll 1
+#pragma unroll 4
       for (int h = 0; h < a.n_groups; ++h) {
         const long long o = __shfl_sync(kFull, v1, h);
         ahead += (o > v1 || (o == v1 && h < lane)) ? 1 : 0;
@@ -289,7 +327,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, const Exac
     const int e = sc.list[q];
     const long long v = sc.cs[e];
     int rank = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int r = 0; r < n; ++r) {
       const long long o = sc.cs[sc.list[r]];
       rank += (o > v || (o == v && r < q)) ? 1 : 0;
@@ -385,236 +423,364 @@ __device__ __forceinline__ float pairs_sum(const uint64_t (&s)[kV / 2]) {
   return a + b;
 }
 
-template <int L>
-__global__ void __launch_bounds__(kThreads, 3) route_grouped_kernel(const __grid_constant__ GroupedArgs a) {
-  constexpr int kTok = 32 / L;                       // tokens per warp
-  constexpr int kCols = L * kV;
-  constexpr int kGmax = kCols < 32 ? kCols : 32;     // groups per token at most
-  constexpr int kList = 32;                          // tokens a warp puts off
-  // per warp: logits and selection values of its tokens; route_exact's values
-  __shared__ __align__(16) float sh_row[kWarps][2][kTok][kCols];
-  __shared__ float sh_g[kWarps][kTok][kGmax];
-  __shared__ uint8_t sh_eval[kWarps][kMaxExperts];
-  __shared__ int sh_pick[kWarps][kTok][kMaxTopK];
-  __shared__ int sh_list[kWarps][kList];
-  __shared__ __align__(16) float sh_bias[kCols];
-  __shared__ float sh_p[kWarps][kTok][kCols];        // sums of p at the end; route_exact's fp32 values
+// Descending order of the values of an array of registers.
+__device__ __forceinline__ void order_pair(float& x, float& y) {
+  const float hi = fmaxf(x, y);
+  y = fminf(x, y);
+  x = hi;
+}
+__device__ __forceinline__ void sort8(float (&k)[8]) {  // Batcher's odd-even merge sort
+  auto o = [&](int x, int y) { order_pair(k[x], k[y]); };
+  o(0, 1); o(2, 3); o(4, 5); o(6, 7);
+  o(0, 2); o(1, 3); o(4, 6); o(5, 7);
+  o(1, 2); o(5, 6);
+  o(0, 4); o(1, 5); o(2, 6); o(3, 7);
+  o(2, 4); o(3, 5);
+  o(1, 2); o(3, 4); o(5, 6);
+}
+
+// The KD largest values seen (descending) and the largest of the others.
+template <int KD>
+struct TopList {
+  float v[KD];
+  float rest;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < KD; ++i) v[i] = -CUDART_INF_F;
+    rest = -CUDART_INF_F;
+  }
+  // With the descending list u: the larger of v[i] and u[KD-1-i] are the KD
+  // largest of both, as a bitonic sequence.
+  __device__ __forceinline__ void merge(const float (&u)[KD]) {
+    float out = rest;
+#pragma unroll
+    for (int i = 0; i < KD; ++i) {
+      const float x = v[i], y = u[KD - 1 - i];
+      v[i] = fmaxf(x, y);
+      out = fmaxf(out, fminf(x, y));
+    }
+    rest = out;
+#pragma unroll
+    for (int d = KD / 2; d > 0; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < KD; ++i)
+        if ((i & d) == 0) order_pair(v[i], v[i + d]);
+  }
+  // Eight values (unordered).
+  __device__ __forceinline__ void add8(float (&x)[8]) {
+    if constexpr (KD == 8) {
+      sort8(x);
+      merge(x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float c = x[e];
+#pragma unroll
+        for (int i = 0; i < KD; ++i) {
+          const float hi = fmaxf(c, v[i]);
+          c = fminf(c, v[i]);
+          v[i] = hi;
+        }
+        rest = fmaxf(rest, c);
+      }
+    }
+  }
+};
+
+// KD: at least k, of 2, 4 and 8. kFull: E = 32 P, no piece is cut short.
+template <int P, int KD, bool kFull32>
+__global__ void __launch_bounds__(kFwdThreads, 4)
+    route_grouped_kernel(const __grid_constant__ GroupedArgs a) {
+  constexpr int kTok = 32 / P;                  // tokens per warp
+  constexpr int kCols = 32 * P;
+  constexpr int kPitch = kCols + 4;             // 16-byte pieces of neighbour tokens in other banks
+  constexpr int kGmax = kCols < 32 ? kCols : 32;
+  constexpr int kList = 64;                     // tokens a warp puts off
+  __shared__ __align__(16) float sh_row[kFwdWarps][kTok * kPitch];  // selection values
+  __shared__ float sh_g[kFwdWarps][kTok][kGmax + 1];
+  __shared__ int sh_pick[kFwdWarps][kTok][kMaxTopK];
+  __shared__ int2 sh_list[kFwdWarps][kList];    // token, and its kept groups if certain
+  __shared__ __align__(16) float sh_bias[kCols];  // -inf past E
   __shared__ int sh_cnt[kCols];
-  static_assert(sizeof(sh_row[0]) == kMaxExperts * sizeof(long long), "route_exact's scratch");
+  static_assert(sizeof(sh_row[0]) >= kMaxExperts * (sizeof(long long) + sizeof(float) + 1),
+                "route_exact's scratch");
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int sub = lane & (L - 1), tok = lane / L;
+  const int sub = lane & (P - 1), tok = lane / P;
   const int E = a.E, G = a.n_groups, S = E / G;
   const bool stats = a.tile_cnt != nullptr;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  for (int i = tid; i < kCols; i += kThreads) {
+  const bool vec = kFull32 || (E & 3) == 0;
+  for (int i = tid; i < kCols; i += kFwdThreads) {
     sh_cnt[i] = 0;
-    sh_bias[i] = a.bias != nullptr && i < E ? a.bias[i] : 0.f;
+    sh_bias[i] = i >= E ? -CUDART_INF_F : a.bias != nullptr ? a.bias[i] : 0.f;
   }
+  // slots that nothing fills still name an expert
+  for (int i = lane; i < kTok * kMaxTopK; i += 32) sh_pick[warp][i / kMaxTopK][i % kMaxTopK] = 0;
   if (blockIdx.x == 0 && tid == 0 && a.ticket != nullptr) *a.ticket = 0u;
   __syncthreads();
-  float* row = sh_row[warp][0][tok];
-  float* cs = sh_row[warp][1][tok];
+  float* row = sh_row[warp] + tok * kPitch;
   float* gv = sh_g[warp][tok];
   int* pick = sh_pick[warp][tok];
   int* cnt = stats ? sh_cnt : nullptr;
-  // which of the lane's experts exist, and their groups (a byte each)
-  uint32_t exist = 0;
-  uint64_t gids = 0;
+  uint64_t psum[16];
 #pragma unroll
-  for (int i = 0; i < kV; ++i)
-    if (sub * kV + i < E) {
-      exist |= 1u << i;
-      gids |= static_cast<uint64_t>((sub * kV + i) / S) << (8 * i);
-    }
-  // Lanes per group where groups are whole lanes, a power of two of them.
-  const int gl = G > 1 && S % kV == 0 && ((S / kV) & (S / kV - 1)) == 0 ? S / kV : 0;
-  uint64_t psum[kV / 2];
-#pragma unroll
-  for (int i = 0; i < kV / 2; ++i) psum[i] = f32x2(0.f, 0.f);
+  for (int i = 0; i < 16; ++i) psum[i] = f32x2(0.f, 0.f);
   uint32_t status = 0;
   int n_list = 0;
   auto flush = [&]() {
     __syncwarp();
-    for (int q = 0; q < n_list; ++q)
-      route_exact(a, sh_list[warp][q],
-                  ExactScratch{reinterpret_cast<long long*>(sh_row[warp]), sh_p[warp][0], sh_eval[warp],
-                               sh_pick[warp][0]},
-                  cnt);
+    long long* scratch = reinterpret_cast<long long*>(sh_row[warp]);
+    float* cf = reinterpret_cast<float*>(scratch + kMaxExperts);
+    const ExactScratch sc{scratch, cf, reinterpret_cast<uint8_t*>(cf + kMaxExperts), sh_pick[warp][0]};
+    for (int q = 0; q < n_list; ++q) {
+      const int2 w = sh_list[warp][q];
+      route_exact(a, w.x, static_cast<uint32_t>(w.y), sc, cnt);
+    }
     n_list = 0;
   };
+  // piece i of the lane: experts 4 (sub + P i) .. + 3; the warp's pieces at i
+  // start at 4 P i, so those from E on are skipped by all lanes
+#define MOE_PIECES(i) _Pragma("unroll") for (int i = 0; i < 8; ++i) if (kFull32 || 4 * P * i < E)
 
-  const int64_t per_pass = static_cast<int64_t>(gridDim.x) * kWarps * kTok;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTok;
-  float next[kV];
-  load_row<L>(a.logits, first + tok < a.T ? first + tok : 0, first + tok < a.T, E, sub, next);
+  const int64_t per_pass = static_cast<int64_t>(gridDim.x) * kFwdWarps * kTok;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kFwdWarps + warp) * kTok;
   for (int64_t base = first; base < a.T; base += per_pass) {
     const int64_t t = base + tok;
     const bool valid = t < a.T;
-    float l[kV], c[kV];
-    uint64_t s[kV / 2];
+    const float* src = a.logits + (valid ? t : 0) * E;
+    float x[32];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) l[i] = next[i];
-    // the next token's row is fetched while this one is worked on
-    const int64_t tn = t + per_pass;
-    load_row<L>(a.logits, tn < a.T ? tn : 0, tn < a.T, E, sub, next);
-    const uint32_t mk = find_masked(l, status);
-    float m, smax, iz = 0.f;
-    scores<L>(l, mk, softmax, s, m);
+    for (int i = 0; i < 32; ++i) x[i] = -kLowest;
+    if (vec) {
+      MOE_PIECES(i) {
+        const int e = 4 * (sub + P * i);
+        if (kFull32 || e < E) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(src + e));
+          x[4 * i] = v.x;
+          x[4 * i + 1] = v.y;
+          x[4 * i + 2] = v.z;
+          x[4 * i + 3] = v.w;
+        }
+      }
+    } else {
+      MOE_PIECES(i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 4 * (sub + P * i) + q;
+          if (e < E) x[4 * i + q] = __ldg(src + e);
+        }
+      }
+    }
+    // a logit that is not finite makes the sum NaN
+    uint64_t chk = f32x2(0.f, 0.f);
+    float m = -CUDART_INF_F;
+    MOE_PIECES(i) {
+      chk = f32x2_fma(f32x2(x[4 * i], x[4 * i + 1]), f32x2(0.f, 0.f), chk);
+      chk = f32x2_fma(f32x2(x[4 * i + 2], x[4 * i + 3]), f32x2(0.f, 0.f), chk);
+      m = max3(max3(m, x[4 * i], x[4 * i + 1]), x[4 * i + 2], x[4 * i + 3]);
+    }
+    float c0, c1;
+    f32x2_get(chk, c0, c1);
+    const bool has_mask = __any_sync(kFull, !(c0 + c1 == 0.f));
+    uint32_t mk = 0u;
+    if (has_mask) {
+      m = -kLowest;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (masked(x[i])) {
+          mk |= 1u << i;
+          if (valid && x[i] != -CUDART_INF_F) status |= MOE_DEV_NONFINITE;
+          x[i] = -kLowest;
+        }
+        m = fmaxf(m, x[i]);
+      }
+    }
+    m = lanes_max<P>(m);
+    // scores: softmax not yet divided by their sum. Past E they are those of the
+    // lowest value: 0 unless the whole row is that low, which is left to fp64.
+    if (softmax) {
+      MOE_PIECES(i) {
+#pragma unroll
+        for (int q = 4 * i; q < 4 * i + 4; q += 2) {
+          float u, v;
+          f32x2_get(f32x2_mul(f32x2_add(f32x2(x[q], x[q + 1]), f32x2(-m, -m)), f32x2(kLog2e, kLog2e)), u, v);
+          x[q] = exp2_approx(u);
+          x[q + 1] = exp2_approx(v);
+        }
+      }
+    } else {
+      MOE_PIECES(i) {
+#pragma unroll
+        for (int q = 4 * i; q < 4 * i + 4; q += 2) {
+          float u, v;
+          f32x2_get(f32x2_mul(f32x2(x[q], x[q + 1]), f32x2(-kLog2e, -kLog2e)), u, v);
+          f32x2_get(f32x2_add(f32x2(exp2_approx(u), exp2_approx(v)), f32x2(1.f, 1.f)), u, v);
+          x[q] = rcp_approx(u);
+          x[q + 1] = rcp_approx(v);
+        }
+      }
+    }
+    if (has_mask) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if ((mk >> i) & 1u) x[i] = 0.f;
+    }
+    uint64_t zz = f32x2(0.f, 0.f);
     if (softmax || stats) {
-      const float z = lanes_sum<L>(pairs_sum(s));
+      MOE_PIECES(i) {
+        zz = f32x2_add(zz, f32x2(x[4 * i], x[4 * i + 1]));
+        zz = f32x2_add(zz, f32x2(x[4 * i + 2], x[4 * i + 3]));
+      }
+    }
+    float iz = 0.f;
+    if (softmax || stats) {
+      f32x2_get(zz, c0, c1);
+      const float z = lanes_sum<P>(c0 + c1);
       iz = z > 0.f ? rcp_approx(z) : 0.f;
     }
-    if (softmax) {
-#pragma unroll
-      for (int i = 0; i < kV / 2; ++i) s[i] = f32x2_mul(s[i], f32x2(iz, iz));
-      smax = iz;  // exp(0) / z
-    }
+    const bool low = m < -1e38f;  // nothing there, or nothing above the lowest values
+    const float smax = low ? 0.f : softmax ? iz : rcp_approx(1.f + exp2_approx(-m * kLog2e));
     if (stats) {
-      const float f = !valid ? 0.f : softmax ? 1.f : iz;
-#pragma unroll
-      for (int i = 0; i < kV / 2; ++i) psum[i] = f32x2_fma(s[i], f32x2(f, f), psum[i]);
-    }
-    {
-      const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(sh_bias + sub * kV);
-      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(sh_bias + sub * kV + 4);
-      if (!softmax) {
-#pragma unroll
-        for (int i = 0; i < kV / 2; ++i) f32x2_get(s[i], c[2 * i], c[2 * i + 1]);
-        smax = fmaxf(fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3])), fmaxf(fmaxf(c[4], c[5]), fmaxf(c[6], c[7])));
-        smax = lanes_max<L>(smax);
+      const float f = valid ? iz : 0.f;
+      MOE_PIECES(i) {
+        psum[2 * i] = f32x2_fma(f32x2(x[4 * i], x[4 * i + 1]), f32x2(f, f), psum[2 * i]);
+        psum[2 * i + 1] = f32x2_fma(f32x2(x[4 * i + 2], x[4 * i + 3]), f32x2(f, f), psum[2 * i + 1]);
       }
-      f32x2_get(f32x2_add(s[0], b0.x), c[0], c[1]);
-      f32x2_get(f32x2_add(s[1], b0.y), c[2], c[3]);
-      f32x2_get(f32x2_add(s[2], b1.x), c[4], c[5]);
-      f32x2_get(f32x2_add(s[3], b1.y), c[6], c[7]);
     }
-    if (mk != 0u) {
+    // selection values, -inf where masked or past E
+    const float f = softmax ? iz : 1.f;
+    MOE_PIECES(i) {
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sh_bias + 4 * (sub + P * i));
+      f32x2_get(f32x2_fma(f32x2(x[4 * i], x[4 * i + 1]), f32x2(f, f), b.x), x[4 * i], x[4 * i + 1]);
+      f32x2_get(f32x2_fma(f32x2(x[4 * i + 2], x[4 * i + 3]), f32x2(f, f), b.y), x[4 * i + 2], x[4 * i + 3]);
+    }
+    if (has_mask) {
 #pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if ((mk >> i) & 1u) {
-          c[i] = -CUDART_INF_F;
-          l[i] = -CUDART_INF_F;
-        }
+      for (int i = 0; i < 32; ++i)
+        if ((mk >> i) & 1u) x[i] = -CUDART_INF_F;
     }
-    *reinterpret_cast<float4*>(row + sub * kV) = make_float4(l[0], l[1], l[2], l[3]);
-    *reinterpret_cast<float4*>(row + sub * kV + 4) = make_float4(l[4], l[5], l[6], l[7]);
-    // A score's error is within 2^-21 of the row's largest score (2^-17 where
-    // all logits are far below zero and the exponent's rounding counts), the
-    // bias adds a rounding, and the keys drop 3 bits (2^-20): values closer
-    // than `near` are decided in fp64.
+    MOE_PIECES(i) {
+      *reinterpret_cast<float4*>(row + 4 * (sub + P * i)) =
+          make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    }
+    __syncwarp();
+    // A score's error is within 2^-21 of the row's largest score (2^-17 where all
+    // logits are far below zero and the exponent's rounding counts), and the bias
+    // adds a rounding: values closer than `near` are decided in fp64.
     const float near_abs = smax * (softmax || smax > 1e-3f ? 0x1p-20f : 0x1p-16f);
-    auto near = [&](float x, float y) {
-      return fabsf(x - y) < fmaf(0x1p-19f, fmaxf(fabsf(x), fabsf(y)), near_abs);
+    auto near = [&](float u, float v) {  // false where either is not finite
+      return fabsf(u - v) < fmaf(0x1p-22f, fmaxf(fabsf(u), fabsf(v)), near_abs);
     };
     bool unsure = smax < 1e-30f;
-    uint32_t avail = exist;
+    uint32_t certain = 1u;  // the kept groups, or 0 where they are in doubt
     if (G > 1) {
-      float v = 0.f;
-      int g0 = 0, step = 0;
-      if (gl > 0) {
-        float v1 = c[0], v2 = -CUDART_INF_F;
-#pragma unroll
-        for (int i = 1; i < kV; ++i) {
-          v2 = fmaxf(v2, fminf(c[i], v1));
-          v1 = fmaxf(v1, c[i]);
-        }
-        for (int o = 1; o < gl; o <<= 1) {
-          const float o1 = __shfl_xor_sync(kFull, v1, o), o2 = __shfl_xor_sync(kFull, v2, o);
-          v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
-          v1 = fmaxf(v1, o1);
-        }
-        v = a.group_top == 2 ? v1 + v2 : v1;
-        if ((sub & (gl - 1)) == 0 && sub / gl < G) gv[sub / gl] = v;
-        g0 = sub / gl;
-        step = G;  // the lane's own group alone
-      } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) cs[sub * kV + i] = c[i];
-        __syncwarp();
-        for (int g = sub; g < G; g += L) {
-          float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
-          for (int q = 0; q < S; ++q) {
-            const float x = cs[g * S + q];
-            v2 = fmaxf(v2, fminf(x, v1));
-            v1 = fmaxf(v1, x);
+      for (int g = sub; g < G; g += P) {
+        float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
+        auto see = [&](float u) {
+          v2 = fmaxf(v2, fminf(u, v1));
+          v1 = fmaxf(v1, u);
+        };
+        if ((S & 3) == 0) {
+          for (int q = 0; q < S; q += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(row + g * S + q);
+            see(u.x);
+            see(u.y);
+            see(u.z);
+            see(u.w);
           }
-          gv[g] = a.group_top == 2 ? v1 + v2 : v1;
+        } else {
+          for (int q = 0; q < S; ++q) see(row[g * S + q]);
         }
-        g0 = sub;
-        step = L;
+        gv[g] = a.group_top == 2 ? v1 + v2 : v1;
       }
       __syncwarp();
       uint32_t kept = 0u;
-      for (int g = g0; g < G; g += step) {
-        const float x = gv[g];
+      for (int g = sub; g < G; g += P) {
+        const float u = gv[g];
         int ahead = 0, sure = 0, maybe = 0;
         for (int h = 0; h < G; ++h) {
           const float o = gv[h];
-          ahead += (o > x || (o == x && h < g)) ? 1 : 0;
-          const bool close = near(o, x);  // false where either is -inf: their difference is not finite
-          sure += (o > x && !close) ? 1 : 0;
-          maybe += (h != g && (o > x || close)) ? 1 : 0;
+          const bool close = near(o, u);
+          ahead += (o > u || (o == u && h < g)) ? 1 : 0;
+          sure += (o > u && !close) ? 1 : 0;
+          maybe += (h != g && (o > u || close)) ? 1 : 0;
         }
         if (ahead < a.topk_groups) kept |= 1u << g;
-        unsure |= x != -CUDART_INF_F && sure < a.topk_groups && maybe >= a.topk_groups;
+        unsure |= u != -CUDART_INF_F && sure < a.topk_groups && maybe >= a.topk_groups;
       }
-      if (gl > 0) {
-        avail = kept != 0u ? exist : 0u;
-      } else {
-        kept = lanes_reduce<L>(kept, [](uint32_t x, uint32_t y) { return x | y; });
-        avail = 0u;
+      kept = lanes_reduce<P>(kept, [](uint32_t u, uint32_t v) { return u | v; });
+      const uint32_t vague = __ballot_sync(kFull, unsure);
+      certain = ((vague >> (tok * P)) & (0xffffffffu >> (32 - P))) != 0u ? 0u : kept;
+      MOE_PIECES(i) {
+        const int e = 4 * (sub + P * i);
+        int g = e / S, left = S - (e - g * S);  // experts left in the group, this one included
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-          avail |= ((kept >> ((gids >> (8 * i)) & 31u)) & 1u) << i;
-        avail &= exist;
+        for (int q = 0; q < 4; ++q) {
+          if (!((kept >> (g & 31)) & 1u)) x[4 * i + q] = -CUDART_INF_F;
+          if (--left == 0) {
+            ++g;
+            left = S;
+          }
+        }
       }
     }
-    float key[kV];
+    TopList<KD> top;
+    top.clear();
 #pragma unroll
-    for (int i = 0; i < kV; ++i) key[i] = key_of(c[i], i);
-    if (avail != 0xffu || mk != 0u) {
+    for (int i = 0; i < 8; i += 2)
+      if (kFull32 || 4 * P * i < E) {
+        float u[8];
 #pragma unroll
-      for (int i = 0; i < kV; ++i)
-        key[i] = !((avail >> i) & 1u) ? key_out(i) : ((mk >> i) & 1u) ? key_masked(sub * kV + i) : key[i];
-    }
-    // the lane's keys, largest first (Batcher's odd-even merge sort of 8)
-    auto swap = [&](int x, int y) {
-      const float hi = fmaxf(key[x], key[y]), lo = fminf(key[x], key[y]);
-      key[x] = hi;
-      key[y] = lo;
-    };
-    swap(0, 1); swap(2, 3); swap(4, 5); swap(6, 7);
-    swap(0, 2); swap(1, 3); swap(4, 6); swap(5, 7);
-    swap(1, 2); swap(5, 6);
-    swap(0, 4); swap(1, 5); swap(2, 6); swap(3, 7);
-    swap(2, 4); swap(3, 5);
-    swap(1, 2); swap(3, 4); swap(5, 6);
-    float prev = CUDART_INF_F;
-    for (int j = 0; j <= a.k; ++j) {
-      const float best = lanes_max<L>(key[0]);
-      // regular values in descending order (against the first, inf, false)
-      unsure |= best > kRegular && near(prev, best);
-      prev = best;
-      // the owner takes it out; two owners are a tie
-      const uint32_t owners = (__ballot_sync(kFull, key[0] == best) >> (tok * (L & 31))) & (0xffffffffu >> (32 - L));
-      unsure |= best > kRegular && (owners & (owners - 1u)) != 0u;
-      if (key[0] == best && j < a.k) {
-        pick[j] = sub * kV + 7 - static_cast<int>(__float_as_uint(best) & 7u);
-#pragma unroll
-        for (int i = 0; i + 1 < kV; ++i) key[i] = key[i + 1];
-        key[kV - 1] = -CUDART_INF_F;
+        for (int q = 0; q < 8; ++q)
+          u[q] = kFull32 || 4 * P * (i + q / 4) < E ? x[4 * i + q] : -CUDART_INF_F;
+        top.add8(u);
       }
+#pragma unroll
+    for (int o = 1; o < P; o <<= 1) {
+      float u[KD];
+#pragma unroll
+      for (int i = 0; i < KD; ++i) u[i] = __shfl_xor_sync(kFull, top.v[i], o);
+      const float r = __shfl_xor_sync(kFull, top.rest, o);
+      top.merge(u);
+      top.rest = fmaxf(top.rest, r);
+    }
+    float last = top.v[0];  // the k-th
+#pragma unroll
+    for (int i = 0; i < KD; ++i)
+      if (i < a.k) {
+        unsure |= near(top.v[i], i + 1 < KD ? top.v[i + 1] : top.rest);
+        last = top.v[i];
+      }
+    unsure |= last == -CUDART_INF_F;  // fewer than k left
+    // the experts at or above the k-th, k of them unless the token is in doubt
+    uint32_t found = 0u;
+    MOE_PIECES(i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (x[4 * i + q] >= last) found |= 1u << (4 * i + q);
+    }
+    if (unsure) found = 0u;
+    while (found != 0u) {
+      const int b = __ffs(static_cast<int>(found)) - 1;
+      found &= found - 1u;
+      const int e = 4 * (sub + P * (b >> 2)) + (b & 3);
+      const float u = row[e];
+      int rank = 0;
+#pragma unroll
+      for (int i = 0; i < KD; ++i) rank += top.v[i] > u ? 1 : 0;
+      if (rank < a.k) pick[rank] = e;
     }
     __syncwarp();
     const uint32_t doubt = __ballot_sync(kFull, unsure && valid);
-    const bool mine = ((doubt >> (tok * (L & 31))) & (0xffffffffu >> (32 - L))) != 0u;
-    write_slots<L>(a, t, pick, row, m, iz, sub, valid && !mine, cnt);
+    const bool mine = ((doubt >> (tok * P)) & (0xffffffffu >> (32 - P))) != 0u;
+    write_slots<P>(a, t, pick, src, m, iz, sub, valid && !mine, cnt);
     if (doubt != 0u) {
       const uint32_t heads = __ballot_sync(kFull, mine && sub == 0);
-      if (mine && sub == 0) sh_list[warp][n_list + __popc(heads & ((1u << lane) - 1u))] =
-          static_cast<int>(t);
+      if (mine && sub == 0)
+        sh_list[warp][n_list + __popc(heads & ((1u << lane) - 1u))] =
+            make_int2(static_cast<int>(t), static_cast<int>(certain));
       n_list += __popc(heads);
       if (n_list > kList - kTok) flush();
     }
@@ -623,19 +789,24 @@ __global__ void __launch_bounds__(kThreads, 3) route_grouped_kernel(const __grid
   flush();
   if (status) atomicOr(a.dev_status, status);
   if (stats) {
-#pragma unroll
-    for (int i = 0; i < kV / 2; ++i)
-      f32x2_get(psum[i], sh_p[warp][tok][sub * kV + 2 * i], sh_p[warp][tok][sub * kV + 2 * i + 1]);
+    // per warp into its own rows' space, then over the block's warps and tokens
     __syncthreads();
-    for (int e = tid; e < E; e += kThreads) {
+    MOE_PIECES(i) {
+      const int e = 4 * (sub + P * i);
+      f32x2_get(psum[2 * i], row[e], row[e + 1]);
+      f32x2_get(psum[2 * i + 1], row[e + 2], row[e + 3]);
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += kFwdThreads) {
       float p = 0.f;
-      for (int w = 0; w < kWarps; ++w)
+      for (int w = 0; w < kFwdWarps; ++w)
 #pragma unroll
-        for (int q = 0; q < kTok; ++q) p += sh_p[w][q][e];
+        for (int q = 0; q < kTok; ++q) p += sh_row[w][q * kPitch + e];
       a.ppart[static_cast<size_t>(e) * gridDim.x + blockIdx.x] = p;
       a.tile_cnt[static_cast<size_t>(e) * gridDim.x + blockIdx.x] = sh_cnt[e];
     }
   }
+#undef MOE_PIECES
 }
 
 // ----------------------------------------------------------- gradient ----
@@ -818,34 +989,60 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
   }
 }
 
-int lanes_of(int E) {
+int lanes_of(int E) {  // gradient: lanes per token
   int L = 2;
   while (L * kV < E) L <<= 1;
   return L;
+}
+// Forward: lanes per token. 32 experts to a lane do the least work per token;
+// where the tokens are too few to fill the GPU, 8 to a lane have the answer
+// sooner (one token of 64 experts: 6 against 10 us; 131072 of 128: 64 against 48).
+constexpr int kFewTokens = 4096;
+int parts_of(int T, int E) {
+  const int each = T <= kFewTokens ? 8 : 32;
+  int P = 1;
+  while (each * P < E) P <<= 1;
+  return P;
+}
+
+template <int P, int KD>
+cudaError_t launch_forward_kd(const GroupedArgs& a, cudaStream_t st) {
+  const dim3 grid(route_grouped_blocks(a.T, a.E)), block(kFwdThreads);
+  if constexpr (P <= kMaxExperts / 32)
+    if (a.E == 32 * P) return launch_pdl(route_grouped_kernel<P, KD, true>, grid, block, 0, st, a);
+  return launch_pdl(route_grouped_kernel<P, KD, false>, grid, block, 0, st, a);
+}
+template <int P>
+cudaError_t launch_forward(const GroupedArgs& a, cudaStream_t st) {
+  if (a.k <= 2) return launch_forward_kd<P, 2>(a, st);
+  if (a.k <= 4) return launch_forward_kd<P, 4>(a, st);
+  return launch_forward_kd<P, 8>(a, st);
 }
 
 }  // namespace
 
 int route_grouped_blocks(int T, int E) {
-  const int per_block = kWarps * (32 / lanes_of(E));
-  const int n = (T + per_block - 1) / per_block;
-  return n < kGroupedMaxBlocks ? n : kGroupedMaxBlocks;
+  const int per_block = kFwdWarps * (32 / parts_of(T, E));
+  const int64_t n = (static_cast<int64_t>(T) + per_block - 1) / per_block;
+  return static_cast<int>(n < kGroupedMaxBlocks ? n : kGroupedMaxBlocks);
 }
 
 cudaError_t launch_route_grouped(const GroupedArgs& a, cudaStream_t st) {
-  const dim3 grid(route_grouped_blocks(a.T, a.E)), block(kThreads);
-  switch (lanes_of(a.E)) {
-    case 2: return launch_pdl(route_grouped_kernel<2>, grid, block, 0, st, a);
-    case 4: return launch_pdl(route_grouped_kernel<4>, grid, block, 0, st, a);
-    case 8: return launch_pdl(route_grouped_kernel<8>, grid, block, 0, st, a);
-    case 16: return launch_pdl(route_grouped_kernel<16>, grid, block, 0, st, a);
-    default: return launch_pdl(route_grouped_kernel<32>, grid, block, 0, st, a);
+  switch (parts_of(a.T, a.E)) {
+    case 1: return launch_forward<1>(a, st);
+    case 2: return launch_forward<2>(a, st);
+    case 4: return launch_forward<4>(a, st);
+    case 8: return launch_forward<8>(a, st);
+    case 16: return launch_forward<16>(a, st);
+    default: return launch_forward<32>(a, st);
   }
 }
 
 cudaError_t launch_route_grouped_bwd(const GroupedBwdArgs& a, cudaStream_t st) {
-  const dim3 grid(route_grouped_blocks(a.T, a.E)), block(kThreads);
-  switch (lanes_of(a.E)) {
+  const int L = lanes_of(a.E);
+  const int64_t blocks = (static_cast<int64_t>(a.T) + kWarps * (32 / L) - 1) / (kWarps * (32 / L));
+  const dim3 grid(static_cast<unsigned>(blocks < kGroupedMaxBlocks ? blocks : kGroupedMaxBlocks)), block(kThreads);
+  switch (L) {
     case 2: return launch_pdl(route_grouped_bwd_kernel<2>, grid, block, 0, st, a);
     case 4: return launch_pdl(route_grouped_bwd_kernel<4>, grid, block, 0, st, a);
     case 8: return launch_pdl(route_grouped_bwd_kernel<8>, grid, block, 0, st, a);
