@@ -487,23 +487,25 @@ struct TopList {
   }
 };
 
-// KD: at least k, of 2, 4 and 8. kFull: E = 32 P, no piece is cut short.
-template <int P, int KD, bool kFull32>
+// KD: at least k, of 2, 4 and 8. N: 16-byte pieces per lane (8, or 2 for few
+// tokens, which also keeps that code short). kWhole: E = 4 N P, no piece missing.
+template <int P, int KD, int N, bool kWhole>
 __global__ void __launch_bounds__(kFwdThreads, 4)
     route_grouped_kernel(const __grid_constant__ GroupedArgs a) {
   constexpr int kTok = 32 / P;                  // tokens per warp
-  constexpr int kCols = 32 * P;
+  constexpr int kX = 4 * N;                     // experts per lane
+  constexpr int kCols = kX * P;
   constexpr int kPitch = kCols + 4;             // 16-byte pieces of neighbour tokens in other banks
   constexpr int kGmax = kCols < 32 ? kCols : 32;
   constexpr int kList = 64;                     // tokens a warp puts off
-  __shared__ __align__(16) float sh_row[kFwdWarps][kTok * kPitch];  // selection values
+  // selection values; room for route_exact's scratch
+  constexpr int kExact = kMaxExperts * (sizeof(long long) + sizeof(float) + 1) / sizeof(float);
+  __shared__ __align__(16) float sh_row[kFwdWarps][kTok * kPitch > kExact ? kTok * kPitch : kExact];
   __shared__ float sh_g[kFwdWarps][kTok][kGmax + 1];
   __shared__ int sh_pick[kFwdWarps][kTok][kMaxTopK];
   __shared__ int2 sh_list[kFwdWarps][kList];    // token, and its kept groups if certain
   __shared__ __align__(16) float sh_bias[kCols];  // -inf past E
   __shared__ int sh_cnt[kCols];
-  static_assert(sizeof(sh_row[0]) >= kMaxExperts * (sizeof(long long) + sizeof(float) + 1),
-                "route_exact's scratch");
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   const int E = a.E, G = a.n_groups, S = E / G;
   const bool stats = a.tile_cnt != nullptr;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  const bool vec = kFull32 || (E & 3) == 0;
+  const bool vec = kWhole || (E & 3) == 0;
   for (int i = tid; i < kCols; i += kFwdThreads) {
     sh_cnt[i] = 0;
     sh_bias[i] = i >= E ? -CUDART_INF_F : a.bias != nullptr ? a.bias[i] : 0.f;
@@ -524,9 +526,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   float* gv = sh_g[warp][tok];
   int* pick = sh_pick[warp][tok];
   int* cnt = stats ? sh_cnt : nullptr;
-  uint64_t psum[16];
+  uint64_t psum[kX / 2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) psum[i] = f32x2(0.f, 0.f);
+  for (int i = 0; i < kX / 2; ++i) psum[i] = f32x2(0.f, 0.f);
   uint32_t status = 0;
   int n_list = 0;
   auto flush = [&]() {
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   };
   // piece i of the lane: experts 4 (sub + P i) .. + 3; the warp's pieces at i
   // start at 4 P i, so those from E on are skipped by all lanes
-#define MOE_PIECES(i) _Pragma("unroll") for (int i = 0; i < 8; ++i) if (kFull32 || 4 * P * i < E)
+#define MOE_PIECES(i) _Pragma("unroll") for (int i = 0; i < N; ++i) if (kWhole || 4 * P * i < E)
 
   const int64_t per_pass = static_cast<int64_t>(gridDim.x) * kFwdWarps * kTok;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kFwdWarps + warp) * kTok;
@@ -550,13 +552,13 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     const int64_t t = base + tok;
     const bool valid = t < a.T;
     const float* src = a.logits + (valid ? t : 0) * E;
-    float x[32];
+    float x[kX];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = -kLowest;
+    for (int i = 0; i < kX; ++i) x[i] = -kLowest;
     if (vec) {
       MOE_PIECES(i) {
         const int e = 4 * (sub + P * i);
-        if (kFull32 || e < E) {
+        if (kWhole || e < E) {
           const float4 v = __ldcs(reinterpret_cast<const float4*>(src + e));
           x[4 * i] = v.x;
           x[4 * i + 1] = v.y;
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     if (has_mask) {
       m = -kLowest;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kX; ++i) {
         if (masked(x[i])) {
           mk |= 1u << i;
           if (valid && x[i] != -CUDART_INF_F) status |= MOE_DEV_NONFINITE;
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     if (has_mask) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < kX; ++i)
         if ((mk >> i) & 1u) x[i] = 0.f;
     }
     uint64_t zz = f32x2(0.f, 0.f);
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     if (has_mask) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < kX; ++i)
         if ((mk >> i) & 1u) x[i] = -CUDART_INF_F;
     }
     MOE_PIECES(i) {
@@ -729,12 +731,12 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     TopList<KD> top;
     top.clear();
 #pragma unroll
-    for (int i = 0; i < 8; i += 2)
-      if (kFull32 || 4 * P * i < E) {
+    for (int i = 0; i < N; i += 2)
+      if (kWhole || 4 * P * i < E) {
         float u[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          u[q] = kFull32 || 4 * P * (i + q / 4) < E ? x[4 * i + q] : -CUDART_INF_F;
+          u[q] = kWhole || 4 * P * (i + q / 4) < E ? x[4 * i + q] : -CUDART_INF_F;
         top.add8(u);
       }
 #pragma unroll
@@ -1006,17 +1008,21 @@ int parts_of(int T, int E) {
 }
 
 template <int P, int KD>
-cudaError_t launch_forward_kd(const GroupedArgs& a, cudaStream_t st) {
-  const dim3 grid(route_grouped_blocks(a.T, a.E)), block(kFwdThreads);
-  if constexpr (P <= kMaxExperts / 32)
-    if (a.E == 32 * P) return launch_pdl(route_grouped_kernel<P, KD, true>, grid, block, 0, st, a);
-  return launch_pdl(route_grouped_kernel<P, KD, false>, grid, block, 0, st, a);
+cudaError_t launch_many(const GroupedArgs& a, dim3 grid, cudaStream_t st) {
+  const dim3 block(kFwdThreads);
+  if (a.E == 32 * P) return launch_pdl(route_grouped_kernel<P, KD, 8, true>, grid, block, 0, st, a);
+  return launch_pdl(route_grouped_kernel<P, KD, 8, false>, grid, block, 0, st, a);
 }
 template <int P>
 cudaError_t launch_forward(const GroupedArgs& a, cudaStream_t st) {
-  if (a.k <= 2) return launch_forward_kd<P, 2>(a, st);
-  if (a.k <= 4) return launch_forward_kd<P, 4>(a, st);
-  return launch_forward_kd<P, 8>(a, st);
+  const dim3 grid(route_grouped_blocks(a.T, a.E));
+  if constexpr (P <= kMaxExperts / 32)
+    if (a.T > kFewTokens) {
+      if (a.k <= 2) return launch_many<P, 2>(a, grid, st);
+      if (a.k <= 4) return launch_many<P, 4>(a, grid, st);
+      return launch_many<P, 8>(a, grid, st);
+    }
+  return launch_pdl(route_grouped_kernel<P, 8, 2, false>, grid, dim3(kFwdThreads), 0, st, a);
 }
 
 }  // namespace
