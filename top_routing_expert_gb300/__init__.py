@@ -232,8 +232,8 @@ class _Args:
     def __call__(self, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
         if t is None:
             return None
-        if not t.is_cuda or t.get_device() != self.dev or not t.is_contiguous() \
-                or t.dtype != dtype or t.numel() < self.need[name]:
+        # get_device() is -1 for host tensors
+        if t.get_device() != self.dev or not t.is_contiguous() or t.dtype != dtype or t.numel() < self.need[name]:
             return _ptr(t, dtype, name, self.need[name])   # raises with the reason
         return t.data_ptr()
 
@@ -702,12 +702,27 @@ def moe_route_grouped_bwd(shape, cfg: RouteConfig, logits, topk_idx, grad_topk_w
 
 # ------------------------------------------------- microscaled 4-bit ----
 
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The current device, on which t has to be."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _address(t: torch.Tensor, dtype, name: str, dev: int) -> int:
+    """As _ptr, for a tensor whose shape has been checked."""
+    if t.get_device() != dev or t.dtype != dtype or not t.is_contiguous():
+        return _ptr(t, dtype, name)   # raises with the reason
+    return t.data_ptr()
+
+
 def _mx4_rows(x_q, x_scale):
     """rows and K of MX4 rows: x_q [rows, K/2], x_scale [ceil(K/128), rows, 4]."""
     if x_q.dim() != 2:
         raise ValueError("x_q must be [rows, K/2]")
-    rows, K = x_q.shape[0], 2 * x_q.shape[1]
-    if tuple(x_scale.shape) != ((K + 127) // 128, rows, 4):
+    rows, half = x_q.shape
+    K = 2 * half
+    if x_scale.shape != ((K + 127) // 128, rows, 4):
         raise ValueError(f"x_scale must be [ceil(K/128), rows, 4] = "
                          f"[{(K + 127) // 128}, {rows}, 4], got {list(x_scale.shape)}")
     return rows, K
@@ -720,7 +735,7 @@ def _mx4_weights(Wq, w_scale):
         raise ValueError("Wq must be [E, N, K/2]")
     E, N, K = Wq.shape[0], Wq.shape[1], 2 * Wq.shape[2]
     want = (E, (N + 127) // 128, (K + 127) // 128, 32, 4, 4)
-    if tuple(w_scale.shape) != want:
+    if w_scale.shape != want:
         raise ValueError(f"w_scale must be {list(want)}, got {list(w_scale.shape)}")
     return E, K, N
 
@@ -730,28 +745,32 @@ def moe_quantize_rows_mx4(x, x_q, x_scale, n_rows=None, stream=None):
     (uint8). n_rows (int32, one element on the device): rows at or past it
     are left out."""
     rows, K = _mx4_rows(x_q, x_scale)
-    if tuple(x.shape) != (rows, K):
+    if x.shape != (rows, K):
         raise ValueError(f"x must be [rows, K] = [{rows}, {K}], got {list(x.shape)}")
+    dev = _device_of(x, "x")
     _check("moe_quantize_rows_mx4", load_library().moe_quantize_rows_mx4(
-        rows, K, _ptr(x, torch.bfloat16, "x"), _ptr(n_rows, torch.int32, "n_rows", 1),
-        _ptr(x_q, torch.uint8, "x_q"), _ptr(x_scale, torch.uint8, "x_scale"), _stream(stream)))
+        rows, K, _address(x, torch.bfloat16, "x", dev), _ptr(n_rows, torch.int32, "n_rows", 1),
+        _address(x_q, torch.uint8, "x_q", dev), _address(x_scale, torch.uint8, "x_scale", dev),
+        _stream(stream)))
 
 
 def moe_dequantize_rows_mx4(x_q, x_scale, x, stream=None):
     """MX4 rows -> x [rows, K] bf16, the values they stand for."""
     rows, K = _mx4_rows(x_q, x_scale)
-    if tuple(x.shape) != (rows, K):
+    if x.shape != (rows, K):
         raise ValueError(f"x must be [rows, K] = [{rows}, {K}], got {list(x.shape)}")
+    dev = _device_of(x_q, "x_q")
     _check("moe_dequantize_rows_mx4", load_library().moe_dequantize_rows_mx4(
-        rows, K, _ptr(x_q, torch.uint8, "x_q"), _ptr(x_scale, torch.uint8, "x_scale"),
-        _ptr(x, torch.bfloat16, "x"), _stream(stream)))
+        rows, K, _address(x_q, torch.uint8, "x_q", dev),
+        _address(x_scale, torch.uint8, "x_scale", dev), _address(x, torch.bfloat16, "x", dev),
+        _stream(stream)))
 
 
 def moe_quantize_weights_mx4(W, Wq, w_scale, stream=None):
     """W [E, K, N] bf16 -> Wq [E, N, K/2] and w_scale [E, ceil(N/128),
     ceil(K/128), 32, 4, 4] (uint8)."""
     E, K, N = _mx4_weights(Wq, w_scale)
-    if tuple(W.shape) != (E, K, N):
+    if W.shape != (E, K, N):
         raise ValueError(f"W must be [E, K, N] = [{E}, {K}, {N}], got {list(W.shape)}")
     _check("moe_quantize_weights_mx4", load_library().moe_quantize_weights_mx4(
         E, K, N, _ptr(W, torch.bfloat16, "W"), _ptr(Wq, torch.uint8, "Wq"),
@@ -784,13 +803,15 @@ def moe_expert_gemm_mx4(x_q, x_scale, offsets, Wq, w_scale, out, gelu=False, dev
     E, Kw, N = _mx4_weights(Wq, w_scale)
     if K != Kw:
         raise ValueError(f"x_q has K = {K}, Wq has K = {Kw}")
-    if tuple(out.shape) != (rows, N):
+    if out.shape != (rows, N):
         raise ValueError(f"out must be [rows, N] = [{rows}, {N}], got {list(out.shape)}")
+    dev = _device_of(x_q, "x_q")
     _check("moe_expert_gemm_mx4", load_library().moe_expert_gemm_mx4(
-        E, rows, K, N, _ptr(x_q, torch.uint8, "x_q"), _ptr(x_scale, torch.uint8, "x_scale"),
-        _ptr(offsets, torch.int32, "offsets", E + 1), _ptr(Wq, torch.uint8, "Wq"),
-        _ptr(w_scale, torch.uint8, "w_scale"), 1 if gelu else 0,
-        _ptr(out, torch.bfloat16, "out"), _ptr(dev_status, torch.int32, "dev_status", 1),
+        E, rows, K, N, _address(x_q, torch.uint8, "x_q", dev),
+        _address(x_scale, torch.uint8, "x_scale", dev),
+        _ptr(offsets, torch.int32, "offsets", E + 1), _address(Wq, torch.uint8, "Wq", dev),
+        _address(w_scale, torch.uint8, "w_scale", dev), 1 if gelu else 0,
+        _address(out, torch.bfloat16, "out", dev), _ptr(dev_status, torch.int32, "dev_status", 1),
         _stream(stream)))
 
 

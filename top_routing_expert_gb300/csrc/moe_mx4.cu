@@ -58,8 +58,20 @@ __device__ __forceinline__ uint32_t codes8(const uint4& v, float inv, bool bad) 
   return r;
 }
 
-// One warp per row, 256 values at a time: a lane holds 8 consecutive values,
-// four lanes a block.
+// A warp takes 4 rows x 256 values: all its loads go out before the first is
+// used, and the scale words of the four rows, which are neighbours in memory,
+// leave together. A lane holds 8 consecutive values of each row, four lanes a
+// block of 32.
+constexpr int kRows = 4;
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {  // read once
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __restrict__ x,
                                                             uint8_t* __restrict__ q,
                                                             uint8_t* __restrict__ scale,
@@ -73,27 +85,45 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* __re
     const int64_t v = *n_rows;
     n = v < 0 ? 0 : (v < rows ? v : rows);
   }
-  const int nvec = K >> 3;
+  const int chunks = (K + 255) >> 8;
+  const int64_t tasks = (n + kRows - 1) / kRows * chunks;
   const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
-       r += warps) {
-    const uint4* src = reinterpret_cast<const uint4*>(x + r * K);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(q + r * (K >> 1));
-    for (int b = 0; b < nvec; b += 32) {
-      const int i = b + lane;
-      const uint4 v = i < nvec ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-      uint32_t m = abs_max2(abs_max2(abs_max2(abs_max2(0u, v.x), v.y), v.z), v.w);
-      m = max(m, __shfl_xor_sync(kFull, m, 1));
-      m = max(m, __shfl_xor_sync(kFull, m, 2));
-      const uint32_t byte = scale_byte(m);
-      if (i < nvec) dst[i] = codes8(v, scale_inverse(byte), byte == 255u);
+  for (int64_t task = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; task < tasks;
+       task += warps) {
+    const int64_t r0 = task / chunks * kRows;
+    const int i = static_cast<int>(task % chunks) * 32 + lane;  // 8 values of the row
+    const bool in = 8 * i < K;
+    const int m = static_cast<int>(n - r0 < kRows ? n - r0 : kRows);
+    uint4 v[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      v[j] = in && j < m ? ld_stream(reinterpret_cast<const uint4*>(x + (r0 + j) * K) + i)
+                         : make_uint4(0, 0, 0, 0);
+    uint32_t word[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      uint32_t a = abs_max2(abs_max2(abs_max2(abs_max2(0u, v[j].x), v[j].y), v[j].z), v[j].w);
+      a = max(a, __shfl_xor_sync(kFull, a, 1));
+      a = max(a, __shfl_xor_sync(kFull, a, 2));
+      const uint32_t byte = scale_byte(a);
+      if (in && j < m)
+        *reinterpret_cast<uint32_t*>(q + (r0 + j) * (K >> 1) + 4 * static_cast<int64_t>(i)) =
+            codes8(v[j], scale_inverse(byte), byte == 255u);
       // the word of 128 values: four blocks' bytes, from lanes 0, 4, 8, 12 of 16
       uint32_t w = byte << (8 * ((lane >> 2) & 3));
       w |= __shfl_xor_sync(kFull, w, 4);
       w |= __shfl_xor_sync(kFull, w, 8);
-      const int kb = i >> 4;
-      if ((lane & 15) == 0 && i < nvec)
-        reinterpret_cast<uint32_t*>(scale)[static_cast<int64_t>(kb) * rows + r] = w;
+      word[j] = w;
+    }
+    if ((lane & 15) == 0 && in) {
+      uint32_t* s = reinterpret_cast<uint32_t*>(scale) + static_cast<int64_t>(i >> 4) * rows + r0;
+      if (m == kRows && (rows & 3) == 0) {
+        *reinterpret_cast<uint4*>(s) = make_uint4(word[0], word[1], word[2], word[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (j < m) s[j] = word[j];
+      }
     }
   }
 }
@@ -117,20 +147,46 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const uint8_t* __r
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int nvec = K >> 3;
+  const int chunks = (K + 255) >> 8;
+  const int64_t tasks = (rows + kRows - 1) / kRows * chunks;
   const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < rows;
-       r += warps) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(q + r * (K >> 1));
-    uint4* dst = reinterpret_cast<uint4*>(x + r * K);
-    for (int i = lane; i < nvec; i += 32) {
-      const uint32_t c = __ldg(src + i);
-      const uint32_t byte = scale[(static_cast<int64_t>(i >> 4) * rows + r) * 4 + ((i >> 2) & 3)];
-      const float s = scale_value(byte);
-      dst[i] = make_uint4(dequant2(c & 255u, s), dequant2((c >> 8) & 255u, s),
-                          dequant2((c >> 16) & 255u, s), dequant2(c >> 24, s));
+  for (int64_t task = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; task < tasks;
+       task += warps) {
+    const int64_t r0 = task / chunks * kRows;
+    const int i = static_cast<int>(task % chunks) * 32 + lane;
+    if (8 * i >= K) continue;
+    const int m = static_cast<int>(rows - r0 < kRows ? rows - r0 : kRows);
+    uint32_t c[kRows], w[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      c[j] = j < m ? __ldcs(reinterpret_cast<const uint32_t*>(q + (r0 + j) * (K >> 1)) + i) : 0u;
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(scale) + static_cast<int64_t>(i >> 4) * rows + r0;
+    if (m == kRows && (rows & 3) == 0) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(s));
+      w[0] = u.x;
+      w[1] = u.y;
+      w[2] = u.z;
+      w[3] = u.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) w[j] = j < m ? __ldg(s + j) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const float f = scale_value((w[j] >> (8 * ((lane >> 2) & 3))) & 255u);
+      if (j < m)
+        st_global_cs_v4(reinterpret_cast<uint4*>(x + (r0 + j) * K) + i,
+                        make_uint4(dequant2(c[j] & 255u, f), dequant2((c[j] >> 8) & 255u, f),
+                                   dequant2((c[j] >> 16) & 255u, f), dequant2(c[j] >> 24, f)));
     }
   }
+}
+
+// Enough warps for every task, or 64 to an SM.
+unsigned rows_grid(int64_t rows, int K, int num_sms) {
+  const int64_t tasks = (rows + kRows - 1) / kRows * ((K + 255) / 256);
+  const int64_t blocks = (tasks + 7) / 8;
+  return static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8);
 }
 
 // Weights W [E, K, N] -> Wq [E, N, K/2]: a block takes 64 columns x 128 k
@@ -185,18 +241,14 @@ cudaError_t launch_quantize_rows_mx4(const uint16_t* x, uint8_t* q, uint8_t* sca
                                      const int32_t* n_rows, int64_t rows, int K, int num_sms,
                                      cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  int64_t grid = (rows + 7) / 8;
-  if (grid > num_sms * 8) grid = num_sms * 8;
-  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, x, q,
+  return launch_pdl(quantize_rows_kernel, dim3(rows_grid(rows, K, num_sms)), dim3(256), 0, st, x, q,
                     scale, n_rows, rows, K);
 }
 
 cudaError_t launch_dequantize_rows_mx4(const uint8_t* q, const uint8_t* scale, uint16_t* x,
                                        int64_t rows, int K, int num_sms, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  int64_t grid = (rows + 7) / 8;
-  if (grid > num_sms * 8) grid = num_sms * 8;
-  return launch_pdl(dequantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, q,
+  return launch_pdl(dequantize_rows_kernel, dim3(rows_grid(rows, K, num_sms)), dim3(256), 0, st, q,
                     scale, x, rows, K);
 }
 
