@@ -140,7 +140,7 @@ __device__ __forceinline__ void store_rows(uint32_t stage, uint16_t* d, int pitc
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 struct Tile {
-  int e, row0, row_end, n0;
+  int e, row0, row_end, n0;  // at most tile_tokens rows, at least one
 };
 
 // Tile order: groups of 8 token tiles, all column tiles of a group before the
@@ -159,10 +159,13 @@ __device__ __forceinline__ Tile decode(int L, const int* prefix, const int* offs
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= tt) lo = mid; else hi = mid - 1;
   }
+  // the expert's rows go evenly over its tiles, in 16s: no tile is a remnant
+  const int rows = offs[lo + 1] - offs[lo], tiles = prefix[lo + 1] - prefix[lo];
+  const int each = ((rows + tiles - 1) / tiles + 15) & ~15;
   Tile t;
   t.e = lo;
-  t.row0 = offs[lo] + (tt - prefix[lo]) * nt;
-  t.row_end = offs[lo + 1];
+  t.row0 = offs[lo] + (tt - prefix[lo]) * each;
+  t.row_end = min(t.row0 + each, offs[lo + 1]);
   t.n0 = (r / gsz) * bm;
   return t;
 }
@@ -191,32 +194,36 @@ struct Tiles {
 };
 
 // Segment offsets, held to the buffer and non-decreasing, and the prefix of the
-// experts' token tiles. All threads; followed by a barrier of the caller's.
+// experts' token tiles, by one warp; followed by a barrier of the caller's. (One
+// thread going through 64 offsets in shared memory took 2 us.)
 __device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, int* prefix, int nt) {
-  const int tid = threadIdx.x, lane = tid & 31, E = p.E;
-  for (int i = tid; i <= E; i += kThreads) {
-    const int v = p.offsets[i];
-    offs[i] = v < 0 ? 0 : (v > p.rows ? p.rows : v);  // rows outside the buffer are never touched
-  }
-  __syncthreads();
-  if (tid == 0)
-    for (int i = 1; i <= E; ++i) offs[i] = offs[i] < offs[i - 1] ? offs[i - 1] : offs[i];
-  __syncthreads();
-  if (tid < 32) {
-    int carry = 0;
-    for (int b = 0; b < E; b += 32) {
-      const int e = b + lane;
-      const int n = e < E ? (offs[e + 1] - offs[e] + nt - 1) / nt : 0;
-      int incl = n;
+  const int lane = threadIdx.x & 31, E = p.E;
+  int last = 0, tiles = 0;  // offs[b - 1] and the tiles of the experts before it
+  for (int b = 0; b <= E; b += 32) {
+    const int i = b + lane;
+    int v = i <= E ? p.offsets[i] : 0;
+    v = v < 0 ? 0 : (v > p.rows ? p.rows : v);  // rows outside the buffer are never touched
+    v = max(v, last);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (e < E) prefix[e] = carry + incl - n;
-      carry += __shfl_sync(0xffffffffu, incl, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, u);
     }
-    if (lane == 0) prefix[E] = carry;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = b == 0 ? v : last;
+    // the tiles of expert i - 1, and through it
+    int n = i <= E ? (v - before + nt - 1) / nt : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += u;
+    }
+    if (i <= E) {
+      offs[i] = v;
+      prefix[i] = tiles + n;
+    }
+    last = __shfl_sync(0xffffffffu, v, 31);
+    tiles += __shfl_sync(0xffffffffu, n, 31);
   }
 }
 
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  load_offsets(p, offs, prefix, NT);
+  if (warp == 0) load_offsets(p, offs, prefix, NT);
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // barriers initialised before any remote use
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bytes = kSubs * (kWBytes + kWScaleBytes) + xbytes;  // per CTA and stage
     const int s_none = E * ((p.N + kBM - 1) / kBM) * nkb;  // past the end: reads as zeros
     while (!aborted && tiles.next(c)) {
-      const int half = ((min(NT, c.row_end - c.row0) + 15) & ~15) >> 1;
+      const int half = ((c.row_end - c.row0 + 15) & ~15) >> 1;
       const int n0 = c.n0 + static_cast<int>(rank) * kBM;
       const int x_row = c.row0 + (kPair ? static_cast<int>(rank) * half : 0);
       // scale blocks of this CTA's 128 columns (past N or K: others', unused)
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       };
       while (!aborted && tiles.next(c)) {
-        const int n_tok = min(NT, c.row_end - c.row0);
+        const int n_tok = c.row_end - c.row0;
         idesc = idesc_mxf4_e8m0(kSubN, static_cast<uint32_t>((n_tok + 15) & ~15));
         const bool b = kPair && c.n0 + kSubN < p.N;
         if (!acquire(acc)) break;
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch = [&](uint32_t(&v)[kTokenWords]) {
       if (fkb == 0 && f_more) {
         f_more = tiles.next(c);
-        f_tok = min(NT, c.row_end - c.row0);
+        f_tok = c.row_end - c.row0;
         f_src = xs + static_cast<size_t>(h) * p.rows + c.row0;
       }
       if (!f_more) return;
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
     bool aborted = false;
     while (!aborted && tiles.next(c)) {
-      const int n_tok = min(NT, c.row_end - c.row0);
+      const int n_tok = c.row_end - c.row0;
       for (int sub = 0; sub < kSubs; ++sub) {
         if (sub > 0 && c.n0 + kSubN >= p.N) break;
         const int a = kPair ? sub : acc;
