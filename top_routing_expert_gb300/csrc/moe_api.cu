@@ -1537,8 +1537,8 @@ moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N, co
   // the 512-byte blocks of the weights' scales, two at a time
   if (!tmap_u32_rows(&tm_ws, w_scale, 128, static_cast<uint64_t>(E) * ((N + 127) / 128) * ((K + 127) / 128), 2))
     return MOE_ERR_CUDA;
-  // stores of 32 rows x 64 columns
-  if (!tmap_bf16_2d(&tm_d, D, N, rows, 64, 32)) return MOE_ERR_CUDA;
+  // stores of 16 rows x 32 columns
+  if (!tmap_bf16_2d(&tm_d, D, N, rows, 32, 16, CU_TENSOR_MAP_SWIZZLE_64B)) return MOE_ERR_CUDA;
   MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, tm_ws, tm_d, a, pair, num_sms(),
                                   static_cast<cudaStream_t>(stream)));
   return MOE_OK;

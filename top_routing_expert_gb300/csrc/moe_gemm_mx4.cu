@@ -39,7 +39,7 @@ constexpr int kScaleWarps = 2;
 constexpr int kTokenWords = (kMaxTokens + 31) / 32;  // scale words per lane, block and tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp (two share theirs)
+constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp, two buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSfX = 480;  // scales of a K block: the tokens', 2 x 8 columns,
 constexpr uint32_t kTmemSfW = 496;  // and the weights', 2 x 4 columns per sub-tile
@@ -110,26 +110,24 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, int gelu, uint32_t (&
   }
 }
 
-// To shared memory, transposed: [32 tokens][64 columns] of two warps (this one's
-// columns first or second by `hq`), 128-byte rows in TMA's 128-byte swizzle,
-// which also keeps the 16-byte pieces of eight tokens in different banks.
-__device__ __forceinline__ void stage_chunk(const uint32_t (&m)[16], uint32_t stage, int hq,
-                                            int lane) {
+// Half a chunk (h) to shared memory, transposed: [16 tokens][32 columns], 64-byte
+// rows in TMA's 64-byte swizzle, which also keeps the 16-byte pieces of eight
+// tokens in different banks.
+__device__ __forceinline__ void stage_half(const uint32_t (&m)[16], int h, uint32_t buf, int lane) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const uint32_t t = lane & 7, c = 4u * hq + (static_cast<uint32_t>(lane) >> 3);
-    stmatrix_x4_trans(stage + 1024u * g + 128u * t + 16u * (c ^ t), m[4 * g], m[4 * g + 1],
-                      m[4 * g + 2], m[4 * g + 3]);
+  for (int g = 0; g < 2; ++g) {
+    const uint32_t t = 8u * g + (lane & 7), c = static_cast<uint32_t>(lane) >> 3;
+    const int f = 4 * (2 * h + g);
+    stmatrix_x4_trans(buf + 64u * t + 16u * (c ^ ((t >> 1) & 3u)), m[f], m[f + 1], m[f + 2], m[f + 3]);
   }
 }
 
-// The first n (under 32) tokens of a staged chunk to D, each warp half of them.
-__device__ __forceinline__ void store_rows(uint32_t stage, uint16_t* d, int pitch, int n, int hq,
-                                           int lane) {
+// The first n (under 16) tokens of a staged half to D.
+__device__ __forceinline__ void store_rows(uint32_t buf, uint16_t* d, int pitch, int n, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t t = 16u * hq + 4u * i + (static_cast<uint32_t>(lane) >> 3), c = lane & 7;
-    const uint4 v = ld_shared_v4(stage + 128u * t + 16u * (c ^ (t & 7u)));
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = 8u * i + (static_cast<uint32_t>(lane) >> 2), c = lane & 3;
+    const uint4 v = ld_shared_v4(buf + 64u * t + 16u * (c ^ ((t >> 1) & 3u)));
     if (static_cast<int>(t) < n) st_global_cs_v4(d + static_cast<size_t>(t) * pitch + 8 * c, v);
   }
 }
@@ -680,14 +678,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ epilogue ----
-    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns; two
-    // neighbours stage 32 tokens x 64 columns together, and one of their threads
-    // stores them by TMA (64-byte rows from each warp's own lanes made the large
-    // product 6 % slower)
-    const int q = warp & 3, half = (warp - 4) >> 2, hq = q & 1;
-    const int bar_id = 1 + ((warp - 4) >> 1);
-    const bool issuer = hq == 0 && lane == 0;
-    const uint32_t stage_addr = smem_u32(staging + ((warp - 4) >> 1) * 2 * kChunkBytes);
+    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns, and
+    // stages 16 tokens of them at a time, in two buffers by turns, for TMA to store
+    // (stores of 16 bytes a lane made the large product 14 % slower; 64 columns of
+    // two warps at a time cost more in their barriers than longer rows gained)
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t stage_addr = smem_u32(staging + (warp - 4) * kChunkBytes);
+    uint32_t turn = 0;
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
@@ -697,8 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int sub = 0; sub < kSubs; ++sub) {
         if (sub > 0 && c.n0 + kSubN >= p.N) break;
         const int a = kPair ? sub : acc;
-        // both warps of a pair go on, or neither
-        if (!pair_barrier_and(bar_id, wait(&tfull[a], (acc_phase >> a) & 1u))) {
+        if (!__all_sync(0xffffffffu, wait(&tfull[a], (acc_phase >> a) & 1u))) {
           aborted = true;
           break;
         }
@@ -722,26 +718,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kPair) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(a));
         else mbar_arrive(&tempty[a]);
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int j = 64 * i + 32 * half;
-          if (any && j < n_tok) {  // the same for both warps: N is a multiple of 64
-            if (issuer) tma_store_wait_read();
-            pair_barrier(bar_id);
-            stage_chunk(m[i], stage_addr, hq, lane);
+        for (int i = 0; i < 2 * kChunks; ++i) {
+          const int j = 64 * (i >> 1) + 32 * half + 16 * (i & 1);
+          if (any && j < n_tok) {
+            const uint32_t buf = stage_addr + turn * (kChunkBytes / 2);
+            turn ^= 1u;
+            if (lane == 0) tma_store_wait_read<1>();  // of this buffer's last store
+            __syncwarp();
+            stage_half(m[i >> 1], i & 1, buf, lane);
             fence_proxy_async();
-            pair_barrier(bar_id);
-            if (n_tok - j >= 32) {
-              if (issuer) tma_store_2d(&tm_d, stage_addr, n, c.row0 + j);
+            __syncwarp();
+            if (n_tok - j >= 16) {
+              if (lane == 0) tma_store_2d(&tm_d, buf, n, c.row0 + j);
             } else {  // rows past the segment belong to the next expert
-              store_rows(stage_addr, p.D + static_cast<size_t>(c.row0 + j) * p.N + n - 32 * hq, p.N,
-                         n_tok - j, hq, lane);
+              store_rows(buf, p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N, n_tok - j, lane);
+              if (lane == 0) tma_store_commit();  // an empty group, this buffer's turn
             }
           }
         }
       }
       if constexpr (!kPair) acc ^= 1;
     }
-    if (issuer) tma_store_wait();
+    if (lane == 0) tma_store_wait();
   }
   __syncwarp();
   tc_fence_before();

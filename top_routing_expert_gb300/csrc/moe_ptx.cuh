@@ -613,9 +613,12 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
   return v;
 }
 
-// 2-D tiled TMA store from shared memory, a bulk group of the issuing thread;
-// `wait_read` returns when its groups no longer read shared memory, `wait` when
-// they are complete.
+// 2-D tiled TMA store from shared memory, a bulk group of the issuing thread.
+// `wait_read` returns when all but its last kPending groups no longer read
+// shared memory, `wait` when all are complete.
+__device__ __forceinline__ void tma_store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t saddr, int32_t c0,
                                              int32_t c1) {
   asm volatile(
@@ -623,31 +626,14 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sa
           reinterpret_cast<uint64_t>(map)),
       "r"(saddr), "r"(c0), "r"(c1)
       : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  tma_store_commit();
 }
+template <int kPending>
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
 }
 __device__ __forceinline__ void tma_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-// Barrier `id` among 64 threads (two warps); with a predicate, whether it holds
-// in all of them.
-__device__ __forceinline__ void pair_barrier(int id) {
-  asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ bool pair_barrier_and(int id, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.red.and.pred q, %1, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(pred ? 1u : 0u)
-      : "memory");
-  return r != 0;
 }
 
 // Two fp32 values in one 64-bit register: one instruction for both.
