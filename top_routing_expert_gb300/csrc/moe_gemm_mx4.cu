@@ -16,8 +16,8 @@
 // multiple of anything), so two warps fetch them into registers, coalesced and
 // stages ahead, and store them word by word in their places.
 //
-// Roles (384 threads): warp 0 = TMA producer, warp 1 = UMMA issuer and TMEM
-// allocation, warps 2-3 = token scales, warps 4-11 = epilogue (two to a TMEM
+// Roles (640 threads): warp 0 = TMA producer, warp 1 = UMMA issuer and TMEM
+// allocation, warps 2-3 = token scales, warps 4-19 = epilogue (four to a TMEM
 // lane quadrant, taking chunks of 32 tokens in turn).
 //
 // Few rows per expert run on single CTAs (M = 128), more on CTA pairs
@@ -37,9 +37,9 @@ constexpr uint32_t kWScaleBytes = 1024;  // 2 x 512
 constexpr int kMaxStages = 10;
 constexpr int kScaleWarps = 2;
 constexpr int kTokenWords = (kMaxTokens + 31) / 32;  // scale words per lane, block and tile
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;                        // four to a TMEM lane quadrant
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr uint32_t kChunkBytes = 2048;   // epilogue staging per warp, two buffers
+constexpr uint32_t kChunkBytes = 1024;   // epilogue staging per warp: 16 tokens x 32 columns
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSfX = 480;  // scales of a K block: the tokens', 2 x 8 columns,
 constexpr uint32_t kTmemSfW = 496;  // and the weights', 2 x 4 columns per sub-tile
@@ -678,13 +678,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ epilogue ----
-    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns, and
-    // stages 16 tokens of them at a time, in two buffers by turns, for TMA to store
+    // warp w reads TMEM lanes 32 (w % 4) .. + 31, i.e. 32 output columns, and every
+    // fourth chunk of 32 tokens, which it stages 16 at a time for TMA to store
     // (stores of 16 bytes a lane made the large product 14 % slower; 64 columns of
-    // two warps at a time cost more in their barriers than longer rows gained)
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t stage_addr = smem_u32(staging + (warp - 4) * kChunkBytes);
-    uint32_t turn = 0;
+    // two warps at a time cost more in their barriers than longer rows gained).
+    // With 8 warps instead of 16 the GELU of the ragged product took 35 us, not 31.
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t buf = smem_u32(staging + (warp - 4) * kChunkBytes);
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;  // bit a: parity of accumulator a's next use
@@ -706,12 +706,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 static_cast<uint32_t>(a * kMaxTokens);
         // Everything is read out of TMEM and the accumulator handed back before
         // anything is stored: its next use waits for the reads alone.
-        constexpr int kChunks = (kMaxTokens + 63) / 64;
+        constexpr int kChunks = (kMaxTokens + 127) / 128;
         uint32_t m[kChunks][16];
         const bool any = n < p.N;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-          const int j = 64 * i + 32 * half;
+          const int j = 128 * i + 32 * part;
           if (any && j < n_tok) load_chunk(t_base + static_cast<uint32_t>(j), p.gelu, m[i]);
         }
         tc_fence_before();
@@ -719,11 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive(&tempty[a]);
 #pragma unroll
         for (int i = 0; i < 2 * kChunks; ++i) {
-          const int j = 64 * (i >> 1) + 32 * half + 16 * (i & 1);
+          const int j = 128 * (i >> 1) + 32 * part + 16 * (i & 1);
           if (any && j < n_tok) {
-            const uint32_t buf = stage_addr + turn * (kChunkBytes / 2);
-            turn ^= 1u;
-            if (lane == 0) tma_store_wait_read<1>();  // of this buffer's last store
+            if (lane == 0) tma_store_wait_read();
             __syncwarp();
             stage_half(m[i >> 1], i & 1, buf, lane);
             fence_proxy_async();
@@ -732,7 +730,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) tma_store_2d(&tm_d, buf, n, c.row0 + j);
             } else {  // rows past the segment belong to the next expert
               store_rows(buf, p.D + static_cast<size_t>(c.row0 + j) * p.N + n, p.N, n_tok - j, lane);
-              if (lane == 0) tma_store_commit();  // an empty group, this buffer's turn
             }
           }
         }

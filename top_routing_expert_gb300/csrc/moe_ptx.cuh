@@ -614,11 +614,8 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
 }
 
 // 2-D tiled TMA store from shared memory, a bulk group of the issuing thread.
-// `wait_read` returns when all but its last kPending groups no longer read
-// shared memory, `wait` when all are complete.
-__device__ __forceinline__ void tma_store_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
+// `wait_read` returns when its groups no longer read shared memory, `wait` when
+// they are complete.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t saddr, int32_t c0,
                                              int32_t c1) {
   asm volatile(
@@ -626,11 +623,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sa
           reinterpret_cast<uint64_t>(map)),
       "r"(saddr), "r"(c0), "r"(c1)
       : "memory");
-  tma_store_commit();
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-template <int kPending>
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
