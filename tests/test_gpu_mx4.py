@@ -205,3 +205,72 @@ def test_product_repeats_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(a, out) and status.item() == 0
+
+
+# ------------------------------------------------------------------ layer ----
+
+@pytest.mark.parametrize("T,H,E,k,h,cf,score", [(257, 192, 16, 3, 320, 1.0, "sigmoid"),
+                                                (1, 128, 8, 2, 128, 1.25, "softmax"),
+                                                (700, 256, 32, 4, 128, 2.0, "sigmoid")])
+def test_layer_step_by_step(T, H, E, k, h, cf, score):
+    """Each step of the layer against the oracle on that step's own inputs
+    (rounding to 4 bits in between would let a last-bit difference grow)."""
+    from top_routing_expert_gb300.mx4 import Mx4Layer
+    g = torch.Generator().manual_seed(T)
+    draw = lambda *n, std=1.0: (std * torch.randn(n, generator=g)).to(torch.bfloat16).to(DEV)
+    x, gate = draw(T, H), draw(H, E, std=H ** -0.5)
+    W1, W2 = draw(E, H, h, std=H ** -0.5), draw(E, h, H, std=h ** -0.5)
+    cfg = dict(score=score, n_groups=4, topk_groups=2, group_top=2, scale=1.5)
+    bias = (0.05 * torch.randn(E, generator=g)).to(DEV)
+    layer = Mx4Layer(moe.MoeShape.make(T, H, E, k, h, cf), moe.RouteConfig.make(**cfg), W1, W2)
+    for t in (layer.act, layer.x_perm, layer.y_perm):
+        t.fill_(7.0)
+    y = torch.empty_like(x)
+    layer.forward(x, gate, y, select_bias=bias)
+    torch.cuda.synchronize()
+    assert layer.dev_status.item() == 0
+    idx, w, _ = O.route_grouped(layer.logits.cpu().numpy().astype(np.float64),
+                                bias.cpu().numpy().astype(np.float64), k, **cfg)
+    np.testing.assert_array_equal(layer.topk_idx.cpu().numpy(), idx)
+    d = O.dispatch_plan(idx, E, O.capacity(T, E, k, cf))
+    np.testing.assert_array_equal(layer.dest_row.cpu().numpy(), d.dest_row)
+    n = int(d.offsets[-1])
+    counts = np.diff(d.offsets).tolist()
+    _check(layer.act, layer.x_perm[:n], W1.cpu(), counts, gelu=True)
+    _check(layer.y_perm, layer.act[:n], W2.cpu(), counts)
+    # combine: an fp32 sum of k products and one rounding to bf16 (the sum itself,
+    # not the oracle's combine, which is rounded to bf16 already)
+    rows = np.where(d.dest_row >= 0, d.dest_row, 0)
+    terms = (_f64(layer.y_perm)[rows] * (d.dest_row >= 0)[:, :, None]
+             * layer.topk_w.cpu().numpy().astype(np.float64)[:, :, None])
+    ref, mag = terms.sum(axis=1), np.abs(terms).sum(axis=1)
+    assert (np.abs(_f64(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 16 * 2.0 ** -24 * mag + 1e-30).all()
+    # the router's gradient for the weights' gradient of a sum of y times v
+    grad = layer.router_grad(torch.ones_like(layer.topk_w), torch.empty_like(layer.logits))
+    l = layer.logits.cpu().numpy().astype(np.float64)
+    want = O.route_grouped_grad(l, idx, np.ones((T, k)), score, True, 1.5)
+    assert np.abs(grad.cpu().numpy() - want).max() <= 2 * (48 + 8 * np.abs(l).max()) * 2.0 ** -24 * 1.5
+
+
+def test_layer_in_a_graph_and_with_no_tokens():
+    from top_routing_expert_gb300.mx4 import Mx4Layer
+    T, H, E, k, h = 300, 128, 8, 2, 192
+    g = torch.Generator().manual_seed(0)
+    draw = lambda *n: (0.1 * torch.randn(n, generator=g)).to(torch.bfloat16).to(DEV)
+    x, gate, W1, W2 = draw(T, H), draw(H, E), draw(E, H, h), draw(E, h, H)
+    layer = Mx4Layer(moe.MoeShape.make(T, H, E, k, h, 1.0), moe.RouteConfig.make(), W1, W2)
+    y, want = torch.empty_like(x), torch.empty_like(x)
+    layer.forward(x, gate, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward(x, gate, y)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and layer.dev_status.item() == 0
+    none = Mx4Layer(moe.MoeShape.make(0, H, E, k, h, 1.0), moe.RouteConfig.make(), W1, W2)
+    none.forward(x[:0], gate, y[:0])
+    torch.cuda.synchronize()
+    assert none.aux.item() == 0 and none.routed_counts.sum().item() == 0
+    with pytest.raises(ValueError):
+        Mx4Layer(moe.MoeShape.make(T, H, E, k, h, 1.0), moe.RouteConfig.make(), W2, W1)
