@@ -68,8 +68,7 @@ struct Ws {
   int32_t* kept;
   int32_t* offsets;
   int32_t* cap;  // expert parallelism: this rank's capacity per expert
-  int32_t* grouped_cnt;   // grouped routing: [E][blocks] counts, their prefix, sums of p
-  int32_t* grouped_base;
+  int32_t* grouped_cnt;   // grouped routing: [E][blocks] counts and sums of p
   float* grouped_p;
   uint32_t* status;
   uint32_t* ticket;
@@ -142,7 +141,6 @@ size_t layout(const Dims& d, uint8_t* base, Ws* w, bool fp8 = false) {
   v.y_perm = static_cast<uint16_t*>(take(A * d.H * 2));
   const size_t EB = static_cast<size_t>(d.E) * route_grouped_blocks(d.T, d.E);
   v.grouped_cnt = static_cast<int32_t*>(take(EB * 4));
-  v.grouped_base = static_cast<int32_t*>(take(EB * 4));
   v.grouped_p = static_cast<float*>(take(EB * 4));
   v.x_scale = nullptr;
   v.act_q = nullptr;
@@ -1404,22 +1402,18 @@ moe_status moe_route_grouped(const moe_shape* s, const moe_route_config* cfg, co
   a.dev_status = dev_status ? dev_status : w.status;
   MOE_CUDA(launch_route_grouped(a, st));
   if (!stats) return MOE_OK;
-  ScanArgs sc;
-  sc.T = d.T;
-  sc.E = d.E;
-  sc.k = d.k;
-  sc.n_tiles = route_grouped_blocks(d.T, d.E);
-  sc.C = d.C;
-  sc.tile_cnt = w.grouped_cnt;
-  sc.tile_base = w.grouped_base;
-  sc.ppart = w.grouped_p;
-  sc.routed = routed_counts ? routed_counts : w.routed;
-  sc.P = P ? P : w.P;
-  sc.aux = aux;
-  sc.kept = nullptr;
-  sc.offsets = nullptr;
-  sc.ticket = w.ticket;
-  MOE_CUDA(launch_scan(sc, st));
+  GroupedStatsArgs g;
+  g.T = d.T;
+  g.E = d.E;
+  g.k = d.k;
+  g.blocks = route_grouped_blocks(d.T, d.E);
+  g.cnt = w.grouped_cnt;
+  g.ppart = w.grouped_p;
+  g.routed = routed_counts ? routed_counts : w.routed;
+  g.P = P ? P : w.P;
+  g.aux = aux;
+  g.ticket = w.ticket;
+  MOE_CUDA(launch_grouped_stats(g, st));
   return MOE_OK;
 }
 

@@ -194,9 +194,47 @@ struct Tiles {
 // Segment offsets, held to the buffer and non-decreasing, and the prefix of the
 // experts' token tiles, by one warp; followed by a barrier of the caller's. (One
 // thread going through 64 offsets in shared memory took 2 us.)
-__device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, int* prefix, int nt) {
+__device__ __forceinline__ void prefix_tiles(const int* offs, int* prefix, int E, int nt) {
+  const int lane = threadIdx.x & 31;
+  int tiles = 0;
+  for (int b = 0; b <= E; b += 32) {
+    const int i = b + lane;  // the tiles of expert i - 1, and through it
+    int n = i > 0 && i <= E ? (offs[i] - offs[i - 1] + nt - 1) / nt : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += u;
+    }
+    if (i <= E) prefix[i] = tiles + n;
+    tiles += __shfl_sync(0xffffffffu, n, 31);
+  }
+  __syncwarp();
+}
+
+// Tile size where the tiles are so few that the last round of them over the
+// units counts: lane c tries 16 c tokens less than the widest, at the cost of its
+// rounds times its size (and about 48 tokens' worth a round for what every tile
+// costs). 8191 skewed rows of 16 experts: 31 us with the widest tiles.
+__device__ __forceinline__ int choose_tile(const int* offs, int E, int nt, int n_tiles_n, int units) {
+  const int lane = threadIdx.x & 31;
+  const int cand = nt - 16 * (lane & 15);
+  int tiles = 0;
+  if (cand >= 64) {
+    const float inv = 1.0f / static_cast<float>(cand);
+    for (int e = 0; e < E; ++e)  // a ceiling to within a rounding: an estimate
+      tiles += static_cast<int>(ceilf(static_cast<float>(offs[e + 1] - offs[e]) * inv));
+  }
+  const int rounds = (tiles * n_tiles_n + units - 1) / units;
+  uint32_t key = cand >= 64 ? (static_cast<uint32_t>(rounds) * static_cast<uint32_t>(cand + 48)) << 4 | (lane & 15u)
+                            : 0xffffffffu;
+  key = __reduce_min_sync(0xffffffffu, key);
+  return nt - 16 * static_cast<int>(key & 15u);
+}
+
+__device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, int* prefix, int nt,
+                                             int n_tiles_n, int units) {
   const int lane = threadIdx.x & 31, E = p.E;
-  int last = 0, tiles = 0;  // offs[b - 1] and the tiles of the experts before it
+  int last = 0;  // offs[b - 1]
   for (int b = 0; b <= E; b += 32) {
     const int i = b + lane;
     int v = i <= E ? p.offsets[i] : 0;
@@ -207,21 +245,14 @@ __device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, in
       const int u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v = max(v, u);
     }
-    int before = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) before = b == 0 ? v : last;
-    // the tiles of expert i - 1, and through it
-    int n = i <= E ? (v - before + nt - 1) / nt : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += u;
-    }
-    if (i <= E) {
-      offs[i] = v;
-      prefix[i] = tiles + n;
-    }
+    if (i <= E) offs[i] = v;
     last = __shfl_sync(0xffffffffu, v, 31);
-    tiles += __shfl_sync(0xffffffffu, n, 31);
+  }
+  __syncwarp();
+  prefix_tiles(offs, prefix, E, nt);
+  if (nt > 64 && E <= 64 && prefix[E] * n_tiles_n <= 8 * units) {
+    const int fit = choose_tile(offs, E, nt, n_tiles_n, units);
+    if (fit != nt) prefix_tiles(offs, prefix, E, fit);
   }
 }
 
@@ -388,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (warp == 0) load_offsets(p, offs, prefix, NT);
+  const int n_tiles_n = (p.N + kTileN - 1) / kTileN;
+  if (warp == 0) load_offsets(p, offs, prefix, NT, n_tiles_n, units);
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // barriers initialised before any remote use
@@ -396,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
   const int total_t = uniform(prefix[E]);
-  const int n_tiles_n = (p.N + kTileN - 1) / kTileN;
   const int total = total_t * n_tiles_n;
   const int nk = (p.K + kStageK - 1) / kStageK;   // stages per tile
   const int nkb = (p.K + 127) / 128;              // 128-deep scale blocks

@@ -106,8 +106,17 @@ struct GroupedArgs {
   float* topk_w;         // [T,k]
   int32_t* tile_cnt;     // [E][blocks] or nullptr (no statistics)
   float* ppart;          // [E][blocks]
-  uint32_t* ticket;      // reset to 0 (used by the scan)
+  uint32_t* ticket;      // reset to 0 (used by the statistics)
   uint32_t* dev_status;
+};
+struct GroupedStatsArgs {
+  int T, E, k, blocks;
+  const int32_t* cnt;    // [E][blocks]
+  const float* ppart;    // [E][blocks]
+  int32_t* routed;       // [E]
+  float* P;              // [E]
+  float* aux;            // [1] or nullptr
+  uint32_t* ticket;      // 0
 };
 struct GroupedBwdArgs {
   int T, E, k;
@@ -221,6 +230,7 @@ cudaError_t launch_route_gemm(const CUtensorMap& tm_x, const CUtensorMap& tm_gat
 cudaError_t launch_route_logits(const RouteArgs& a, cudaStream_t st);
 int route_grouped_blocks(int T, int E);
 cudaError_t launch_route_grouped(const GroupedArgs& a, cudaStream_t st);
+cudaError_t launch_grouped_stats(const GroupedStatsArgs& a, cudaStream_t st);
 cudaError_t launch_route_grouped_bwd(const GroupedBwdArgs& a, cudaStream_t st);
 cudaError_t launch_quantize_rows_mx4(const uint16_t* x, uint8_t* q, uint8_t* scale,
                                      const int32_t* n_rows, int64_t rows, int K, int num_sms,

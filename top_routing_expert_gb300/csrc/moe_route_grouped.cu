@@ -811,6 +811,52 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
 #undef MOE_PIECES
 }
 
+// The blocks' counts and probability sums to routed, P and aux: a warp per
+// expert, then the last block to finish. (The dispatch's scan, which could do
+// this too, also forms prefixes: 7.2 us instead of 4 for 608 blocks.)
+__global__ void __launch_bounds__(kThreads) grouped_stats_kernel(GroupedStatsArgs a) {
+  __shared__ int last;
+  __shared__ float sh[kWarps];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * kWarps + warp;
+  if (e < a.E) {
+    const int32_t* cnt = a.cnt + static_cast<size_t>(e) * a.blocks;
+    const float* pp = a.ppart + static_cast<size_t>(e) * a.blocks;
+    int n = 0;
+    float p = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < a.blocks; i += 32) {
+      n += cnt[i];
+      p += pp[i];
+    }
+    n = lanes_reduce<32>(n, [](int u, int v) { return u + v; });
+    p = lanes_sum<32>(p);
+    if (lane == 0) {
+      a.routed[e] = n;
+      a.P[e] = p / static_cast<float>(a.T);
+    }
+  }
+  if (a.aux == nullptr) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x - 1 ? 1 : 0;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const int i = threadIdx.x;
+  float v = i < a.E ? static_cast<float>(__ldcg(a.routed + i)) * __ldcg(a.P + i) : 0.f;
+  v = lanes_sum<32>(v);
+  if (lane == 0) sh[warp] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float sum = 0.f;
+    for (int w = 0; w < kWarps; ++w) sum += sh[w];
+    *a.aux = static_cast<float>(a.E) * sum / (static_cast<float>(a.T) * static_cast<float>(a.k));
+  }
+}
+
 // ----------------------------------------------------------- gradient ----
 // With q_j = s_j / sum of the chosen s and gradient g_j of weight j:
 //   softmax, renormalised  dl_j = scale q_j (g_j - sum q g)
@@ -1042,6 +1088,10 @@ cudaError_t launch_route_grouped(const GroupedArgs& a, cudaStream_t st) {
     case 16: return launch_forward<16>(a, st);
     default: return launch_forward<32>(a, st);
   }
+}
+
+cudaError_t launch_grouped_stats(const GroupedStatsArgs& a, cudaStream_t st) {
+  return launch_pdl(grouped_stats_kernel, dim3((a.E + kWarps - 1) / kWarps), dim3(kThreads), 0, st, a);
 }
 
 cudaError_t launch_route_grouped_bwd(const GroupedBwdArgs& a, cudaStream_t st) {
