@@ -352,8 +352,7 @@ __device__ __noinline__ void issue_tail(const Block& b, int steps, bool wide, ui
 // an SM takes in from L2 (one 256-column sub-tile alone: 34 KB for 480, 71).
 // Each CTA loads half of the tokens' codes and all of their scales, and the
 // leader (rank 0) issues the UMMAs, so stage barriers of both CTAs' copies live
-// there. At a tile's ends the UMMAs of A run ahead of those of B by a stage, so
-// that one accumulator is drained while the other is computed.
+// there.
 // Otherwise a tile is 128 columns of one CTA, its accumulators used in turn.
 template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -598,10 +597,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();  // the scale warps' stores, before tcgen05.cp reads them
           tc_fence_after();
-          // B follows A at once, but A goes first through the tile's first two blocks
-          // and its last two
-          const bool hold = b && ((kb == 0 && nk > 1) || kb == nk - 2);
-          if (kPair && b && !hold && b_kb == kb && kb != 0 && kb != nk - 1) {
+          // B goes with A, block by block. While B's accumulator is still being drained
+          // A goes on alone, as far as the ring holds the blocks that B has to come
+          // back to. (Letting A run ahead at a tile's end too cost more in issue than
+          // it hid: 145 against 139 us on 98304 x 1408 x 2048.)
+          bool hold = false;
+          if (b && b_kb == 0 && kb < nk - 1 && kb + 2 <= nst)
+            hold = !__all_sync(0xffffffffu, mbar_try_wait(&tempty[1], ((acc_phase >> 1) & 1u) ^ 1u));
+          if (kPair && b && !hold && b_kb == kb && kb != nk - 1) {
+            if (kb == 0 && !acquire(1)) {
+              aborted = true;
+              break;
+            }
             const Block k = block(stage, kb, 0u, 0);
             if (wide) issue_block_ab<true>(k, k.d + kMaxTokens, &empty[stage]);
             else issue_block_ab<false>(k, k.d + kMaxTokens, &empty[stage]);
