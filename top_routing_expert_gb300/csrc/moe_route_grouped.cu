@@ -12,13 +12,13 @@
 // what is done once per token (merging the lanes' lists, the weights) is shared
 // by many experts. Only values are kept in order, never pairs of value and
 // index: a second look at the row finds the experts whose values made it.
-// Gradient: L lanes share a token and hold 8 consecutive experts each.
+// Gradient: L lanes share a token and hold 16 experts each, in the same way.
 //
-// The choice is that of the formulas in 64 bits. Scores are computed in fp32,
-// and wherever two values that a decision compares are closer than the fp32
-// error allows, the token is decided again in fp64 (fp64 runs at 1/64 of the
-// fp32 rate here, so only those tokens pay for it). Values that are equal are
-// always decided there, so ties need no care elsewhere.
+// The choice is that of the formulas in 64 bits, exponentials to 2^-44. Scores
+// are computed in fp32, and wherever two values that a decision compares are
+// closer than the fp32 error allows, the token is decided again with more bits,
+// which only those tokens pay for. Values that are equal are always decided
+// there, so ties need no care elsewhere.
 #include <math_constants.h>
 
 #include "moe_internal.h"
@@ -28,9 +28,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kV = 8;          // experts per lane, gradient
-constexpr int kWarps = 8;      // gradient
+constexpr int kV = 16;         // experts per lane, gradient
+constexpr int kWarps = 4;      // gradient
 constexpr int kThreads = 32 * kWarps;
+constexpr int kStatsWarps = 8;
+constexpr int kStatsThreads = 32 * kStatsWarps;
+static_assert(kStatsThreads >= kMaxExperts, "a thread per expert sums the balance loss");
 constexpr int kFwdWarps = 4;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 constexpr unsigned kFull = 0xffffffffu;
@@ -75,10 +78,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ __forceinline__ bool masked(float l) { return !(fabsf(l) < CUDART_INF_F); }
 
-// ------------------------------------------------------------- fp64 ----
-// The choice of one token in fp64, by a whole warp (lane l: experts l, l + 32,
-// ...), then its weights. fp64 instructions run at 1/64 of the fp32 rate, so
-// comparisons are made on the values' bits as ordered integers.
+// -------------------------------------------------- close decisions ----
+// Order of fp64 values as integers (fp64 instructions take a warp 64 clocks each
+// here). Its own inverse.
 __device__ __forceinline__ long long order64(double v) {
   const long long b = __double_as_longlong(v);
   return b ^ ((b >> 63) & 0x7fffffffffffffffll);
@@ -148,46 +150,102 @@ struct ExactScratch {     // shared memory of one warp
   int* pick;              // [kMaxTopK]
 };
 
-// exp of an fp32 difference in fp64: x = n ln 2 + r, |r| <= ln 2 / 2, and the
-// Taylor series of exp(r) to r^13 / 13! (the next term is below 2^-57). x is at
-// most 0 or held to a range where nothing overflows.
-__device__ __forceinline__ double exp64(double x) {
-  x = fmax(fmin(x, 700.0), -700.0);
-  const double n = rint(x * 1.4426950408889634);
-  // ln 2 in two parts, the first with zeros at its end
-  double r = fma(n, -0x1.62e42fp-1, x);
-  r = fma(n, -(0x1.df473de6af279p-26), r);
-  double y = 1.0 / 6227020800.0;
-  y = fma(y, r, 1.0 / 479001600.0);
-  y = fma(y, r, 1.0 / 39916800.0);
-  y = fma(y, r, 1.0 / 3628800.0);
-  y = fma(y, r, 1.0 / 362880.0);
-  y = fma(y, r, 1.0 / 40320.0);
-  y = fma(y, r, 1.0 / 5040.0);
-  y = fma(y, r, 1.0 / 720.0);
-  y = fma(y, r, 1.0 / 120.0);
-  y = fma(y, r, 1.0 / 24.0);
-  y = fma(y, r, 1.0 / 6.0);
-  y = fma(y, r, 0.5);
-  y = fma(y, r, 1.0);
-  y = fma(y, r, 1.0);
-  return __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
+// Values as an unevaluated sum of two fp32 (Dekker, Knuth): 48 bits of fp32
+// instructions, each of which takes a sixteenth of an fp64 one's time.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // exact
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Two ordered_sum(float a, float b) {  // exact for |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return ordered_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+// a / b: a quotient of fp32 and one more for what it leaves.
+__device__ __forceinline__ Two divide(Two a, Two b) {
+  const float y = rcp_approx(b.hi), q = __fmul_rn(a.hi, y), p = __fmul_rn(q, b.hi);
+  const float left = __fsub_rn(a.hi, p) - __fmaf_rn(q, b.hi, -p) + __fmaf_rn(-q, b.lo, a.lo);
+  return ordered_sum(q, __fmul_rn(left, y));
+}
+__device__ __forceinline__ Two lanes_sum(Two v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, Two{__shfl_xor_sync(kFull, v.hi, o), __shfl_xor_sync(kFull, v.lo, o)});
+  return v;
+}
+// 2^n of n in -126 .. 127
+__device__ __forceinline__ float power2(int n) { return __int_as_float((n + 127) << 23); }
+
+// exp(x) 2^-n to 45 bits: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor
+// series of exp(r) to r^13 / 13! (the next term is below 2^-57), its terms from
+// r^7 on (below 2^-22) in plain fp32. x is held to where fp64's exp has a value.
+__device__ __forceinline__ Two exp_parts(Two x, int& n) {
+  if (!(fabsf(x.hi) < 700.f)) x = {copysignf(700.f, x.hi), 0.f};
+  const float nf = rintf(x.hi * kLog2e);
+  n = static_cast<int>(nf);
+  // ln 2 in three parts; products of the first, of 12 bits, with n are exact
+  Two r = two_sum(x.hi, __fmul_rn(nf, -0x1.62ep-1f));
+  float tail = r.lo;
+  r = two_sum(r.hi, x.lo);
+  tail += r.lo;
+  constexpr float kLn2b = 0x1.0bfbe8p-15f, kLn2c = 0x1.cf79acp-40f;
+  const float p = __fmul_rn(nf, -kLn2b);
+  tail += __fmaf_rn(nf, -kLn2c, __fmaf_rn(nf, -kLn2b, -p));
+  r = two_sum(r.hi, p);
+  r = ordered_sum(r.hi, tail + r.lo);
+  float y = 1.f / 6227020800.f;
+  y = fmaf(y, r.hi, 1.f / 479001600.f);
+  y = fmaf(y, r.hi, 1.f / 39916800.f);
+  y = fmaf(y, r.hi, 1.f / 3628800.f);
+  y = fmaf(y, r.hi, 1.f / 362880.f);
+  y = fmaf(y, r.hi, 1.f / 40320.f);
+  y = fmaf(y, r.hi, 1.f / 5040.f);
+  Two v{y, 0.f};
+  auto step = [&](double c) {  // v = v r + c, c above |v r|
+    const float ch = static_cast<float>(c), cl = static_cast<float>(c - static_cast<double>(ch));
+    const float q = __fmul_rn(v.hi, r.hi);
+    float e = __fmaf_rn(v.hi, r.hi, -q);
+    e = __fmaf_rn(v.lo, r.hi, __fmaf_rn(v.hi, r.lo, e)) + cl;
+    const Two s = ordered_sum(ch, q);
+    v = ordered_sum(s.hi, s.lo + e);
+  };
+  step(1.0 / 720.0);
+  step(1.0 / 120.0);
+  step(1.0 / 24.0);
+  step(1.0 / 6.0);
+  step(0.5);
+  step(1.0);
+  step(1.0);
+  return v;
 }
 
-__device__ __noinline__ double score64(float x, float m, bool softmax) {
-  const double y = exp64(softmax ? static_cast<double>(x) - static_cast<double>(m) : -static_cast<double>(x));
+// The score as fp64: exp(x - m) / z, or the sigmoid of x. The latter's last two
+// steps are fp64's own: scores next to 1 are equal, or not, as they round there.
+__device__ __noinline__ double score64(float x, float m, bool softmax, Two z) {
+  int n;
+  Two v = exp_parts(softmax ? two_sum(x, -m) : Two{-x, 0.f}, n);
+  if (softmax) v = divide(v, z);
+  double y = static_cast<double>(v.hi) + static_cast<double>(v.lo);
+  y = __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
   return softmax ? y : 1.0 / (1.0 + y);
 }
 
-// Only experts that may matter are evaluated in fp64: those whose fp32 value is
+// Only experts that may matter are evaluated so: those whose fp32 value is
 // within `slack` of the group_top-th of their group, then those within it of a
 // lower bound of the kept groups' k-th. All others rank below them whatever the
-// error. (A softmax with a bias needs its fp64 sum too, hence all exponentials.)
-// Few tokens come here, on any SM, so the code is kept short: fetching
-// instructions for the first time costs more than running them.
-// known: the kept groups where they are not in doubt, else 0.
-__device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t known,
-                                         const ExactScratch& sc, int* cnt) {
+// error. (A softmax with a bias needs its sum so too, hence all exponentials.)
+// Few tokens come here, on any SM, and the last of them holds up the launch, so
+// loads are made at once and loops kept short.
+// known: the kept groups where they are not in doubt, else 0; kth: with them
+// known, the k-th largest value found in fp32. bias: in shared memory.
+__device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t known, float kth,
+                                         const float* bias, const ExactScratch& sc, int* cnt) {
   constexpr int kPer = kMaxExperts / 32;  // lane l: experts l, l + 32, ...
   const int lane = threadIdx.x & 31;
   const int E = a.E, S = a.E / a.n_groups;
@@ -208,38 +266,45 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   }
   m = lanes_max<32>(m);
   if (m == -CUDART_INF_F) m = 0.f;  // nothing unmasked
-  double z64 = 0.0;
+  Two zz{0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {  // the scores, -inf where masked
-    c[i] = x[i];
-    if (x[i] != -CUDART_INF_F) {
-      const float y = __expf(softmax ? x[i] - m : -x[i]);
-      c[i] = softmax ? y : __fdividef(1.f, 1.f + y);
+  for (int i = 0; i < kPer; ++i)
+    if (32 * i < E) {  // the scores, 0 where masked
+      const float y = exp2_approx((softmax ? x[i] - m : -x[i]) * kLog2e);
+      c[i] = softmax ? y : rcp_approx(1.f + y);
       z += c[i];
       smax = fmaxf(smax, c[i]);
     }
-    if (lane + 32 * i < E) sc.cs[lane + 32 * i] = x[i] == -CUDART_INF_F ? kInf : kNever;
-  }
   if (all) {
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32)
-      if (!masked(row[e])) z64 += score64(row[e], m, true);
-    z64 = lanes_reduce<32>(z64, [](double u, double v) { return u + v; });
+#pragma unroll 2
+    for (int e = lane; e < E; e += 32) {
+      const float l = row[e];
+      int n;
+      const Two v = exp_parts(two_sum(l, -m), n);
+      const float f = masked(l) ? 0.f : power2(max(n, -120));
+      zz = add(zz, Two{v.hi * f, v.lo * f});
+    }
+    zz = lanes_sum(zz);
+  } else {
+    zz.hi = 1.f;  // softmax scores are compared as exp(l - m) where nothing is added to them
   }
   z = lanes_sum<32>(z);
   smax = lanes_max<32>(smax);
-  const float iz = softmax && z > 0.f ? 1.f / z : 0.f;
-  // softmax scores are compared as exp(l - m) where nothing is added to them
+  const float iz = softmax && z > 0.f ? rcp_approx(z) : 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    if (a.bias != nullptr && c[i] != -CUDART_INF_F) {
-      c[i] = fmaf(c[i], all ? iz : 1.f, a.bias[e]);
-      big = fmaxf(big, fabsf(c[i]));
+  for (int i = 0; i < kPer; ++i)
+    if (32 * i < E) {
+      const int e = lane + 32 * i;
+      const float b = e < E ? bias[e] : 0.f;
+      c[i] = x[i] == -CUDART_INF_F ? x[i] : fmaf(c[i], softmax ? iz : 1.f, b);
+      if (x[i] != -CUDART_INF_F) big = fmaxf(big, fabsf(c[i]));
+      if (e < E) {
+        sc.cf[e] = c[i];
+        sc.cs[e] = x[i] == -CUDART_INF_F ? kInf : kNever;
+      }
     }
-    if (e < E) sc.cf[e] = c[i];
-  }
-  big = fmaxf(lanes_max<32>(big), all ? smax * iz : smax);
+  smax = softmax ? smax * iz : smax;
+  big = fmaxf(lanes_max<32>(big), smax);
   // fp32 errors are within 2^-18 of the largest value (2^-14 where the logits are
   // so low that exp's argument is what errs)
   const float slack = big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
@@ -261,13 +326,15 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
         }
         bound = a.group_top == 2 ? v2 : v1;
       }
+    } else if (known != 0u) {
+      bound = kth;
     } else {
       // the k-th largest of the lanes' own maxima
       float own = -CUDART_INF_F;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const uint32_t g = (static_cast<uint32_t>(lane + 32 * i) * inv) >> 16;
-        if ((kept >> (g & 31u)) & 1u) own = fmaxf(own, c[i]);
+        if (32 * i < E && ((kept >> (g & 31u)) & 1u)) own = fmaxf(own, c[i]);
       }
       for (int j = 0; j < a.k; ++j) {
         bound = lanes_max<32>(own);
@@ -279,6 +346,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
     n = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+      if (32 * i >= E) break;
       const int e = lane + 32 * i;
       const uint32_t g = (static_cast<uint32_t>(e) * inv) >> 16;
       const float lim = phase == 0 ? __shfl_sync(kFull, bound, g) : bound;
@@ -292,9 +360,8 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
     for (int q = lane; q < n; q += 32) {
       const int e = sc.list[q];
       if (sc.cs[e] == kNever) {
-        double v = score64(row[e], m, softmax);
-        if (all) v /= z64;
-        if (a.bias != nullptr) v += static_cast<double>(a.bias[e]);
+        double v = score64(row[e], m, softmax, zz);
+        if (a.bias != nullptr) v += static_cast<double>(bias[e]);
         sc.cs[e] = order64(v);
       }
     }
@@ -341,17 +408,18 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
 
 // ------------------------------------------------------------- kernel ----
 
-// The lane's 8 logits of row t, the type's lowest value past E or T.
+// The lane's kV logits of row t, pieces of four: sub, sub + L, ...; the type's
+// lowest value past E or T.
 template <int L>
 __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64_t t, bool valid,
                                          int E, int sub, float (&l)[kV]) {
   const float* row = logits + t * E;
-  const int e0 = sub * kV;
   if ((E & 3) == 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kV / 4; ++h) {
+      const int e = 4 * (sub + L * h);
       float4 v = make_float4(-kLowest, -kLowest, -kLowest, -kLowest);
-      if (valid && e0 + 4 * h < E) v = __ldg(reinterpret_cast<const float4*>(row + e0 + 4 * h));
+      if (valid && e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
       l[4 * h] = v.x;
       l[4 * h + 1] = v.y;
       l[4 * h + 2] = v.z;
@@ -359,7 +427,10 @@ __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) l[i] = valid && e0 + i < E ? __ldg(row + e0 + i) : -kLowest;
+    for (int i = 0; i < kV; ++i) {
+      const int e = 4 * (sub + L * (i / 4)) + i % 4;
+      l[i] = valid && e < E ? __ldg(row + e) : -kLowest;
+    }
   }
 }
 
@@ -391,7 +462,10 @@ __device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool s
   m = 0.f;
   float x[kV];
   if (softmax) {
-    m = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i + 1 < kV; i += 2) m = max3(m, l[i], l[i + 1]);
+    m = fmaxf(m, l[kV - 1]);
     m = lanes_max<L>(m);
 #pragma unroll
     for (int i = 0; i < kV; i += 2)
@@ -419,7 +493,10 @@ __device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool s
 }
 __device__ __forceinline__ float pairs_sum(const uint64_t (&s)[kV / 2]) {
   float a, b;
-  f32x2_get(f32x2_add(f32x2_add(s[0], s[1]), f32x2_add(s[2], s[3])), a, b);
+  uint64_t sum = s[0];
+#pragma unroll
+  for (int i = 1; i < kV / 2; ++i) sum = f32x2_add(sum, s[i]);
+  f32x2_get(sum, a, b);
   return a + b;
 }
 
@@ -503,7 +580,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   __shared__ __align__(16) float sh_row[kFwdWarps][kTok * kPitch > kExact ? kTok * kPitch : kExact];
   __shared__ float sh_g[kFwdWarps][kTok][kGmax + 1];
   __shared__ int sh_pick[kFwdWarps][kTok][kMaxTopK];
-  __shared__ int2 sh_list[kFwdWarps][kList];    // token, and its kept groups if certain
+  // token, its kept groups if certain, its k-th value
+  __shared__ int sh_list[kFwdWarps][3][kList];
   __shared__ __align__(16) float sh_bias[kCols];  // -inf past E
   __shared__ int sh_cnt[kCols];
   grid_dependency_wait();
@@ -537,8 +615,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     float* cf = reinterpret_cast<float*>(scratch + kMaxExperts);
     const ExactScratch sc{scratch, cf, reinterpret_cast<uint8_t*>(cf + kMaxExperts), sh_pick[warp][0]};
     for (int q = 0; q < n_list; ++q) {
-      const int2 w = sh_list[warp][q];
-      route_exact(a, w.x, static_cast<uint32_t>(w.y), sc, cnt);
+      const auto& w = sh_list[warp];
+      route_exact(a, w[0][q], static_cast<uint32_t>(w[1][q]), __int_as_float(w[2][q]), sh_bias, sc, cnt);
     }
     n_list = 0;
   };
@@ -601,7 +679,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     m = lanes_max<P>(m);
     // scores: softmax not yet divided by their sum. Past E they are those of the
-    // lowest value: 0 unless the whole row is that low, which is left to fp64.
+    // lowest value: 0 unless the whole row is that low, which is decided again.
     if (softmax) {
       MOE_PIECES(i) {
 #pragma unroll
@@ -670,7 +748,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     __syncwarp();
     // A score's error is within 2^-21 of the row's largest score (2^-17 where all
     // logits are far below zero and the exponent's rounding counts), and the bias
-    // adds a rounding: values closer than `near` are decided in fp64.
+    // adds a rounding: values closer than `near` are decided again.
     const float near_abs = smax * (softmax || smax > 1e-3f ? 0x1p-20f : 0x1p-16f);
     auto near = [&](float u, float v) {  // false where either is not finite
       return fabsf(u - v) < fmaf(0x1p-22f, fmaxf(fabsf(u), fabsf(v)), near_abs);
@@ -780,9 +858,12 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     write_slots<P>(a, t, pick, src, m, iz, sub, valid && !mine, cnt);
     if (doubt != 0u) {
       const uint32_t heads = __ballot_sync(kFull, mine && sub == 0);
-      if (mine && sub == 0)
-        sh_list[warp][n_list + __popc(heads & ((1u << lane) - 1u))] =
-            make_int2(static_cast<int>(t), static_cast<int>(certain));
+      if (mine && sub == 0) {
+        const int q = n_list + __popc(heads & ((1u << lane) - 1u));
+        sh_list[warp][0][q] = static_cast<int>(t);
+        sh_list[warp][1][q] = static_cast<int>(certain);
+        sh_list[warp][2][q] = __float_as_int(last);
+      }
       n_list += __popc(heads);
       if (n_list > kList - kTok) flush();
     }
@@ -814,13 +895,13 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
 // The blocks' counts and probability sums to routed, P and aux: a warp per
 // expert, then the last block to finish. (The dispatch's scan, which could do
 // this too, also forms prefixes: 7.2 us instead of 4 for 608 blocks.)
-__global__ void __launch_bounds__(kThreads) grouped_stats_kernel(GroupedStatsArgs a) {
+__global__ void __launch_bounds__(kStatsThreads) grouped_stats_kernel(GroupedStatsArgs a) {
   __shared__ int last;
-  __shared__ float sh[kWarps];
+  __shared__ float sh[kStatsWarps];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = blockIdx.x * kWarps + warp;
+  const int e = blockIdx.x * kStatsWarps + warp;
   if (e < a.E) {
     const int32_t* cnt = a.cnt + static_cast<size_t>(e) * a.blocks;
     const float* pp = a.ppart + static_cast<size_t>(e) * a.blocks;
@@ -852,7 +933,7 @@ __global__ void __launch_bounds__(kThreads) grouped_stats_kernel(GroupedStatsArg
   __syncthreads();
   if (threadIdx.x == 0) {
     float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) sum += sh[w];
+    for (int w = 0; w < kStatsWarps; ++w) sum += sh[w];
     *a.aux = static_cast<float>(a.E) * sum / (static_cast<float>(a.T) * static_cast<float>(a.k));
   }
 }
@@ -886,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     const float f = *a.grad_aux * (static_cast<float>(E) / T) / (T * static_cast<float>(a.k));
 #pragma unroll
     for (int i = 0; i < kV / 2; ++i) {
-      const int e = sub * kV + 2 * i;
+      const int e = 4 * (sub + L * (i / 2)) + 2 * (i % 2);
       h[i] = f32x2(e < E ? f * static_cast<float>(a.routed[e]) : 0.f,
                    e + 1 < E ? f * static_cast<float>(a.routed[e + 1]) : 0.f);
     }
@@ -1012,8 +1093,9 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     }
     // the chosen experts' part is added in shared memory
     float* row = sh_row[warp][tok];
-    *reinterpret_cast<ulonglong2*>(row + sub * kV) = make_ulonglong2(grad[0], grad[1]);
-    *reinterpret_cast<ulonglong2*>(row + sub * kV + 4) = make_ulonglong2(grad[2], grad[3]);
+#pragma unroll
+    for (int q = 0; q < kV / 4; ++q)
+      *reinterpret_cast<ulonglong2*>(row + 4 * (sub + L * q)) = make_ulonglong2(grad[2 * q], grad[2 * q + 1]);
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
@@ -1021,23 +1103,21 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     __syncwarp();
     if (valid) {
       float* out = a.grad_logits + t * E;
-      const int e0 = sub * kV;
       if ((E & 3) == 0) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (e0 + 4 * q < E)
-            __stcs(reinterpret_cast<float4*>(out + e0 + 4 * q),
-                   *reinterpret_cast<const float4*>(row + e0 + 4 * q));
+        for (int q = 0; q < kV / 4; ++q) {
+          const int e = 4 * (sub + L * q);
+          if (e < E) __stcs(reinterpret_cast<float4*>(out + e), *reinterpret_cast<const float4*>(row + e));
+        }
       } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-          if (e0 + i < E) out[e0 + i] = row[e0 + i];
+        for (int e = sub; e < E; e += L) out[e] = row[e];
       }
     }
   }
 }
 
-int lanes_of(int E) {  // gradient: lanes per token
+// Gradient: lanes per token.
+int lanes_of(int E) {
   int L = 2;
   while (L * kV < E) L <<= 1;
   return L;
@@ -1091,7 +1171,7 @@ cudaError_t launch_route_grouped(const GroupedArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_grouped_stats(const GroupedStatsArgs& a, cudaStream_t st) {
-  return launch_pdl(grouped_stats_kernel, dim3((a.E + kWarps - 1) / kWarps), dim3(kThreads), 0, st, a);
+  return launch_pdl(grouped_stats_kernel, dim3((a.E + kStatsWarps - 1) / kStatsWarps), dim3(kStatsThreads), 0, st, a);
 }
 
 cudaError_t launch_route_grouped_bwd(const GroupedBwdArgs& a, cudaStream_t st) {
@@ -1102,8 +1182,7 @@ cudaError_t launch_route_grouped_bwd(const GroupedBwdArgs& a, cudaStream_t st) {
     case 2: return launch_pdl(route_grouped_bwd_kernel<2>, grid, block, 0, st, a);
     case 4: return launch_pdl(route_grouped_bwd_kernel<4>, grid, block, 0, st, a);
     case 8: return launch_pdl(route_grouped_bwd_kernel<8>, grid, block, 0, st, a);
-    case 16: return launch_pdl(route_grouped_bwd_kernel<16>, grid, block, 0, st, a);
-    default: return launch_pdl(route_grouped_bwd_kernel<32>, grid, block, 0, st, a);
+    default: return launch_pdl(route_grouped_bwd_kernel<16>, grid, block, 0, st, a);
   }
 }
 
