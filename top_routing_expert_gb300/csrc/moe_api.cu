@@ -1523,7 +1523,7 @@ moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N, co
   a.stages = 0;
   a.dev_status = dev_status;
   a.timeout_ns = wait_timeout_ns();
-  const bool pair = mx4_use_pair(rows, a.E);
+  const bool pair = mx4_use_pair(rows, a.E, N, num_sms());
   CUtensorMap tm_w, tm_x, tm_ws, tm_d;
   if (!tmap_u8_2d(&tm_w, Wq, K / 2, static_cast<uint64_t>(E) * N)) return MOE_ERR_CUDA;
   if (!tmap_u8_2d(&tm_x, x_q, K / 2, rows, pair ? a.tile_tokens / 2 : a.tile_tokens))

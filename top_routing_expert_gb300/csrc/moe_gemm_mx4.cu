@@ -213,8 +213,11 @@ __device__ __forceinline__ void prefix_tiles(const int* offs, int* prefix, int E
 
 // Tile size where the tiles are so few that the last round of them over the
 // units counts: lane c tries 16 c tokens less than the widest, at the cost of its
-// rounds times its size (and about 48 tokens' worth a round for what every tile
-// costs). 8191 skewed rows of 16 experts: 31 us with the widest tiles.
+// rounds times its size and 300 tokens' worth, which a round of tiles of any size
+// costs about. With this and without, in us: 2048 rows of 8 experts (4096 x 1024)
+// 13.6, 15.2; 8191 skewed rows of 16 (1024 x 2816, GELU) 25.9, 27.4; 4096 rows of
+// 4 (2048 x 2048, GELU) 17.0, 19.7; but 8191 rows of 8 16.7, 16.3. Shorter
+// segments lose by it (2048 rows of 64 experts 27.1, 25.1) and keep the widest.
 __device__ __forceinline__ int choose_tile(const int* offs, int E, int nt, int n_tiles_n, int units) {
   const int lane = threadIdx.x & 31;
   const int cand = nt - 16 * (lane & 15);
@@ -225,7 +228,7 @@ __device__ __forceinline__ int choose_tile(const int* offs, int E, int nt, int n
       tiles += static_cast<int>(ceilf(static_cast<float>(offs[e + 1] - offs[e]) * inv));
   }
   const int rounds = (tiles * n_tiles_n + units - 1) / units;
-  uint32_t key = cand >= 64 ? (static_cast<uint32_t>(rounds) * static_cast<uint32_t>(cand + 48)) << 4 | (lane & 15u)
+  uint32_t key = cand >= 64 ? (static_cast<uint32_t>(rounds) * static_cast<uint32_t>(cand + 300)) << 4 | (lane & 15u)
                             : 0xffffffffu;
   key = __reduce_min_sync(0xffffffffu, key);
   return nt - 16 * static_cast<int>(key & 15u);
@@ -250,7 +253,7 @@ __device__ __forceinline__ void load_offsets(const Mx4GemmArgs& p, int* offs, in
   }
   __syncwarp();
   prefix_tiles(offs, prefix, E, nt);
-  if (nt > 64 && E <= 64 && prefix[E] * n_tiles_n <= 8 * units) {
+  if (p.rows >= 256 * E && E <= 64 && prefix[E] * n_tiles_n <= 8 * units) {
     const int fit = choose_tile(offs, E, nt, n_tiles_n, units);
     if (fit != nt) prefix_tiles(offs, prefix, E, fit);
   }
@@ -801,7 +804,14 @@ int mx4_tile_tokens(int64_t rows, int E) {
   return want < kMaxTokens ? static_cast<int>(want) : kMaxTokens;
 }
 
-bool mx4_use_pair(int64_t rows, int E) { return rows >= 64 * static_cast<int64_t>(E); }
+// A pair of CTAs reads each tile's tokens once for 512 columns and has the better
+// rate, unless its tiles are so few that most pairs get one or two of them. In us,
+// pairs against single CTAs: 64 experts of 2048 x 1408 (192 tiles) 15.8, 18.0 at
+// 96 rows and 22.5, 24.8 at 1024; 16 of 4096 x 4096 (128 tiles) 28.4, 31.7 at 128
+// rows; 16 of 1024 x 2816 (96 tiles) 10.4, 9.4 at 128 rows and 11.8, 10.8 at 1024.
+bool mx4_use_pair(int64_t rows, int E, int64_t N, int num_sms) {
+  return rows >= 64 * static_cast<int64_t>(E) || 2 * E * ((N + 511) / 512) >= 3 * (num_sms / 2);
+}
 
 template <bool kPair>
 static cudaError_t launch_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,

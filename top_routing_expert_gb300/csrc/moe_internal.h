@@ -242,7 +242,7 @@ cudaError_t launch_quantize_weights_mx4(const uint16_t* W, uint8_t* Wq, uint8_t*
 // Token tile of the 4-bit grouped product: a multiple of 16, at most 240.
 int mx4_tile_tokens(int64_t rows, int E);
 // Whether it runs as the CTA-pair kernel (token boxes of half a tile).
-bool mx4_use_pair(int64_t rows, int E);
+bool mx4_use_pair(int64_t rows, int E, int64_t N, int num_sms);
 cudaError_t launch_expert_gemm_mx4(const CUtensorMap& tm_w, const CUtensorMap& tm_x,
                                    const CUtensorMap& tm_ws, const CUtensorMap& tm_d,
                                    const Mx4GemmArgs& a, bool pair, int num_sms, cudaStream_t st);

@@ -144,8 +144,9 @@ __device__ __forceinline__ void write_slots(const GroupedArgs& a, int64_t t, con
 }
 
 struct ExactScratch {     // shared memory of one warp
-  long long* cs;          // [kMaxExperts]: ordered fp64 values
-  float* cf;              // [kMaxExperts]: fp32 values
+  long long* val;         // [kMaxExperts]: ordered fp64 values of the listed experts
+  float* x;               // [kMaxExperts]: logits, -inf where masked
+  float* c;               // [kMaxExperts]: selection values in fp32
   uint8_t* list;          // [kMaxExperts]: experts to evaluate
   int* pick;              // [kMaxTopK]
 };
@@ -254,7 +255,6 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   const bool all = softmax && a.bias != nullptr;
   const long long kInf = order64(-CUDART_INF);
-  const long long kNever = -0x7fffffffffffffffll - 1;  // not evaluated: below -inf
   float m = -CUDART_INF_F, smax = 0.f, z = 0.f, big = 0.f;
   float x[kPer], c[kPer];
 #pragma unroll
@@ -263,6 +263,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   for (int i = 0; i < kPer; ++i) {
     if (masked(x[i])) x[i] = -CUDART_INF_F;
     m = fmaxf(m, x[i]);
+    sc.x[lane + 32 * i] = x[i];
   }
   m = lanes_max<32>(m);
   if (m == -CUDART_INF_F) m = 0.f;  // nothing unmasked
@@ -276,12 +277,12 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
       smax = fmaxf(smax, c[i]);
     }
   if (all) {
-#pragma unroll 2
+#pragma unroll 1
     for (int e = lane; e < E; e += 32) {
-      const float l = row[e];
+      const float l = sc.x[e];
       int n;
       const Two v = exp_parts(two_sum(l, -m), n);
-      const float f = masked(l) ? 0.f : power2(max(n, -120));
+      const float f = l == -CUDART_INF_F ? 0.f : power2(max(n, -120));
       zz = add(zz, Two{v.hi * f, v.lo * f});
     }
     zz = lanes_sum(zz);
@@ -298,10 +299,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
       const float b = e < E ? bias[e] : 0.f;
       c[i] = x[i] == -CUDART_INF_F ? x[i] : fmaf(c[i], softmax ? iz : 1.f, b);
       if (x[i] != -CUDART_INF_F) big = fmaxf(big, fabsf(c[i]));
-      if (e < E) {
-        sc.cf[e] = c[i];
-        sc.cs[e] = x[i] == -CUDART_INF_F ? kInf : kNever;
-      }
+      if (known == 0u) sc.c[e] = c[i];
     }
   smax = softmax ? smax * iz : smax;
   big = fmaxf(lanes_max<32>(big), smax);
@@ -320,7 +318,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
         float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
 #pragma unroll 4
         for (int q = 0; q < S; ++q) {
-          const float v = sc.cf[lane * S + q];
+          const float v = sc.c[lane * S + q];
           v2 = fmaxf(v2, fminf(v, v1));
           v1 = fmaxf(v1, v);
         }
@@ -342,43 +340,48 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
         if (lane == __ffs(static_cast<int>(who)) - 1) own = -CUDART_INF_F;
       }
     }
-    // the candidates, in order of their index
-    n = 0;
+    // the candidates
+    uint32_t mine = 0u;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (32 * i >= E) break;
-      const int e = lane + 32 * i;
-      const uint32_t g = (static_cast<uint32_t>(e) * inv) >> 16;
-      const float lim = phase == 0 ? __shfl_sync(kFull, bound, g) : bound;
-      const bool in = e < E && c[i] >= lim - slack && (phase == 0 || ((kept >> (g & 31u)) & 1u));
-      const unsigned who = __ballot_sync(kFull, in);
-      if (in) sc.list[n + __popc(who & ((1u << lane) - 1u))] = static_cast<uint8_t>(e);
-      n += __popc(who);
+    for (int i = 0; i < kPer; ++i)
+      if (32 * i < E) {
+        const int e = lane + 32 * i;
+        const uint32_t g = (static_cast<uint32_t>(e) * inv) >> 16;
+        const float lim = phase == 0 ? __shfl_sync(kFull, bound, g) : bound;
+        if (e < E && c[i] >= lim - slack && (phase == 0 || ((kept >> (g & 31u)) & 1u))) mine |= 1u << i;
+      }
+    n = 0;
+    for (unsigned who; (who = __ballot_sync(kFull, mine != 0u)) != 0u; n += __popc(who)) {
+      if (mine != 0u)
+        sc.list[n + __popc(who & ((1u << lane) - 1u))] =
+            static_cast<uint8_t>(lane + 32 * (__ffs(static_cast<int>(mine)) - 1));
+      mine &= mine - 1u;
     }
     __syncwarp();
 #pragma unroll 1
     for (int q = lane; q < n; q += 32) {
       const int e = sc.list[q];
-      if (sc.cs[e] == kNever) {
-        double v = score64(row[e], m, softmax, zz);
+      const float l = sc.x[e];
+      double v = -CUDART_INF;
+      if (l != -CUDART_INF_F) {
+        v = score64(l, m, softmax, zz);
         if (a.bias != nullptr) v += static_cast<double>(bias[e]);
-        sc.cs[e] = order64(v);
       }
+      sc.val[q] = order64(v);
     }
     __syncwarp();
     if (phase == 0) {
       long long v1 = kInf, v2 = kInf;
-      if (lane < a.n_groups) {
 #pragma unroll 4
-        for (int q = 0; q < S; ++q) {
-          const long long v = sc.cs[lane * S + q];
+      for (int q = 0; q < n; ++q)
+        if (static_cast<int>((sc.list[q] * inv) >> 16) == lane) {
+          const long long v = sc.val[q];
           v2 = max(v2, min(v, v1));
           v1 = max(v1, v);
         }
-        if (a.group_top == 2)  // order64 is its own inverse
-          v1 = order64(__longlong_as_double(order64(__longlong_as_double(v1))) +
-                       __longlong_as_double(order64(__longlong_as_double(v2))));
-      }
+      if (lane < a.n_groups && a.group_top == 2)  // order64 is its own inverse
+        v1 = order64(__longlong_as_double(order64(__longlong_as_double(v1))) +
+                     __longlong_as_double(order64(__longlong_as_double(v2))));
       int ahead = 0;
 #pragma unroll 4
       for (int h = 0; h < a.n_groups; ++h) {
@@ -386,23 +389,25 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
         ahead += (o > v1 || (o == v1 && h < lane)) ? 1 : 0;
       }
       kept = __ballot_sync(kFull, lane < a.n_groups && ahead < a.topk_groups);
+      __syncwarp();
     }
   }
-  // the candidates' ranks: ties go to the lower index, which comes first here
+  // the candidates' ranks, ties to the lower index
 #pragma unroll 1
   for (int q = lane; q < n; q += 32) {
     const int e = sc.list[q];
-    const long long v = sc.cs[e];
+    const long long v = sc.val[q];
     int rank = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int r = 0; r < n; ++r) {
-      const long long o = sc.cs[sc.list[r]];
-      rank += (o > v || (o == v && r < q)) ? 1 : 0;
+      const long long o = sc.val[r];
+      const int f = sc.list[r];
+      rank += static_cast<int>(o > v) | (static_cast<int>(o == v) & static_cast<int>(f < e));
     }
     if (rank < a.k) sc.pick[rank] = e;
   }
   __syncwarp();
-  write_slots<32>(a, t, sc.pick, row, m, iz, lane, true, cnt);
+  write_slots<32>(a, t, sc.pick, sc.x, m, iz, lane, true, cnt);
   __syncwarp();
 }
 
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   constexpr int kGmax = kCols < 32 ? kCols : 32;
   constexpr int kList = 64;                     // tokens a warp puts off
   // selection values; room for route_exact's scratch
-  constexpr int kExact = kMaxExperts * (sizeof(long long) + sizeof(float) + 1) / sizeof(float);
+  constexpr int kExact = kMaxExperts * (sizeof(long long) + 2 * sizeof(float) + 1) / sizeof(float);
   __shared__ __align__(16) float sh_row[kFwdWarps][kTok * kPitch > kExact ? kTok * kPitch : kExact];
   __shared__ float sh_g[kFwdWarps][kTok][kGmax + 1];
   __shared__ int sh_pick[kFwdWarps][kTok][kMaxTopK];
@@ -611,9 +616,9 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   int n_list = 0;
   auto flush = [&]() {
     __syncwarp();
-    long long* scratch = reinterpret_cast<long long*>(sh_row[warp]);
-    float* cf = reinterpret_cast<float*>(scratch + kMaxExperts);
-    const ExactScratch sc{scratch, cf, reinterpret_cast<uint8_t*>(cf + kMaxExperts), sh_pick[warp][0]};
+    long long* val = reinterpret_cast<long long*>(sh_row[warp]);
+    float* f = reinterpret_cast<float*>(val + kMaxExperts);
+    const ExactScratch sc{val, f, f + kMaxExperts, reinterpret_cast<uint8_t*>(f + 2 * kMaxExperts), sh_pick[warp][0]};
     for (int q = 0; q < n_list; ++q) {
       const auto& w = sh_list[warp];
       route_exact(a, w[0][q], static_cast<uint32_t>(w[1][q]), __int_as_float(w[2][q]), sh_bias, sc, cnt);
@@ -1122,17 +1127,22 @@ int lanes_of(int E) {
   while (L * kV < E) L <<= 1;
   return L;
 }
-// Forward: lanes per token. 32 experts to a lane do the least work per token;
-// where the tokens are too few to fill the GPU, 8 to a lane have the answer
-// sooner (one token of 64 experts: 6 against 10 us; 131072 of 128: 64 against 48).
-constexpr int kFewTokens = 4096;
+// Forward: experts per lane. 32 do the least work per token; where there are too
+// few logits to fill the GPU so, 8 have the answer sooner. In us, 8 against 32:
+// 1 token of 64 experts 2.5, 3.1; 1024 of 256 4.2, 4.9; 2048 of 256 8.6, 8.7;
+// 4096 of 256 11.7, 9.8; 8192 of 64 7.0, 7.3; 16384 of 64 9.2, 7.9; 131072 of 64
+// 36.7, 20.6.
+bool few_logits(int64_t T, int E) { return T * E <= 512 * 1024; }
 int parts_of(int T, int E) {
-  const int each = T <= kFewTokens ? 8 : 32;
+  const int each = few_logits(T, E) ? 8 : 32;
   int P = 1;
   while (each * P < E) P <<= 1;
   return P;
 }
 
+// 131072 tokens: a list of 2 for k = 2 takes 39 us at 256 experts, 21.6 at 128,
+// with one of 8 56 and 28; of 4 for k = 4 49 and 28.4, with 8 58 and 30.5. Without
+// kWhole the lists of 2 take 48 and 25, those of 8 72 instead of 64 at 256 experts.
 template <int P, int KD>
 cudaError_t launch_many(const GroupedArgs& a, dim3 grid, cudaStream_t st) {
   const dim3 block(kFwdThreads);
@@ -1143,7 +1153,7 @@ template <int P>
 cudaError_t launch_forward(const GroupedArgs& a, cudaStream_t st) {
   const dim3 grid(route_grouped_blocks(a.T, a.E));
   if constexpr (P <= kMaxExperts / 32)
-    if (a.T > kFewTokens) {
+    if (!few_logits(a.T, a.E)) {
       if (a.k <= 2) return launch_many<P, 2>(a, grid, st);
       if (a.k <= 4) return launch_many<P, 4>(a, grid, st);
       return launch_many<P, 8>(a, grid, st);
