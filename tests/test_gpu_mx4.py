@@ -163,6 +163,13 @@ def test_product_many_experts_and_a_long_reduction():
     _check(_product(q, s, off, w.W1q, w.w1_scale), x, W, [9, 4])
 
 
+def test_product_of_short_segments_with_many_columns():
+    """Few rows to each of many experts: tiles of 512 columns, mostly 16 tokens wide."""
+    counts = [(3 * i) % 5 if i % 7 else 17 * (i % 3) for i in range(100)]
+    x, W, q, s, w, off = _problem(counts, 192, 640, 8, spare=2)
+    _check(_product(q, s, off, w.W1q, w.w1_scale), x, W, counts)
+
+
 def test_product_of_nan_blocks():
     """A block that stands for NaN makes its row NaN, and no other."""
     x, W, q, s, w, off = _problem([20, 12], 256, 128, 4)

@@ -805,12 +805,13 @@ int mx4_tile_tokens(int64_t rows, int E) {
 }
 
 // A pair of CTAs reads each tile's tokens once for 512 columns and has the better
-// rate, unless its tiles are so few that most pairs get one or two of them. In us,
-// pairs against single CTAs: 64 experts of 2048 x 1408 (192 tiles) 15.8, 18.0 at
-// 96 rows and 22.5, 24.8 at 1024; 16 of 4096 x 4096 (128 tiles) 28.4, 31.7 at 128
-// rows; 16 of 1024 x 2816 (96 tiles) 10.4, 9.4 at 128 rows and 11.8, 10.8 at 1024.
+// rate, unless there are so few columns that the pairs get less than 1.5 tiles
+// each. In us, pairs against single CTAs: 64 experts of 2048 x 1408 (2.3 tiles)
+// 15.8, 18.0 at 96 rows and 22.5, 24.8 at 1024; 16 of 4096 x 4096 (1.7 tiles) 28.4,
+// 31.7 at 128 rows; 16 of 1024 x 2816 (1.2) 10.4, 9.4 at 128 rows and 11.8, 10.8
+// at 1024. Long segments are what the pair is made for.
 bool mx4_use_pair(int64_t rows, int E, int64_t N, int num_sms) {
-  return rows >= 64 * static_cast<int64_t>(E) || 2 * E * ((N + 511) / 512) >= 3 * (num_sms / 2);
+  return rows >= 64 * static_cast<int64_t>(E) || 2 * E * N >= 3 * 512 * (num_sms / 2);
 }
 
 template <bool kPair>
