@@ -20,8 +20,16 @@
 // allocation, warps 2-3 = token scales, warps 4-19 = epilogue (four to a TMEM
 // lane quadrant, taking chunks of 32 tokens in turn).
 //
-// Few rows per expert run on single CTAs (M = 128), more on CTA pairs
-// (cta_group::2, M = 256).
+// CTA pairs (cta_group::2, M = 256) do the work, or single CTAs (M = 128) where
+// there are too few columns for the pairs.
+//
+// Measured, with what bounds it: 65536 rows x 4096 x 14336 over 8 experts 1.07 ms,
+// 7.2 PFLOP/s, the power limit (2.0 GHz at 1370 W) and the 51 bytes a clock that
+// each SM takes in; 98304 x 1408 x 2048 over 64 experts 134 us, requests to L2,
+// whose rows of codes are 704 bytes; 16 rows over 8 experts of 4096 x 14336 35 us,
+// 6.3 TB/s of weights; 96 over 64 of 2048 x 1408 with GELU 15.7 us, 4.9 TB/s;
+// 8191 over 16 of 1024 x 2816 with GELU 26 us, a start and an end of 7 us around
+// four rounds of tiles whose GELU takes longer than their products.
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -603,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // B goes with A, block by block. While B's accumulator is still being drained
           // A goes on alone, as far as the ring holds the blocks that B has to come
           // back to. (Letting A run ahead at a tile's end too cost more in issue than
-          // it hid: 145 against 139 us on 98304 x 1408 x 2048.)
+          // it hid: 6 us more on 98304 x 1408 x 2048.)
           bool hold = false;
           if (b && b_kb == 0 && kb < nk - 1 && kb + 2 <= nst)
             hold = !__all_sync(0xffffffffu, mbar_try_wait(&tempty[1], ((acc_phase >> 1) & 1u) ^ 1u));
@@ -723,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // fourth chunk of 32 tokens, which it stages 16 at a time for TMA to store
     // (stores of 16 bytes a lane made the large product 14 % slower; 64 columns of
     // two warps at a time cost more in their barriers than longer rows gained).
-    // With 8 warps instead of 16 the GELU of the ragged product took 35 us, not 31.
+    // With 8 warps instead of 16 the ragged product with GELU took 4 us more.
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t buf = smem_u32(staging + (warp - 4) * kChunkBytes);
     const uint32_t tempty0 = kPair ? mapa_shared(smem_u32(tempty), 0) : 0u;

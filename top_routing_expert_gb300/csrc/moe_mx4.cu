@@ -61,7 +61,8 @@ __device__ __forceinline__ uint32_t codes8(const uint4& v, float inv, bool bad) 
 // A warp takes 4 rows x 256 values: all its loads go out before the first is
 // used, and the scale words of the four rows, which are neighbours in memory,
 // leave together. A lane holds 8 consecutive values of each row, four lanes a
-// block of 32.
+// block of 32. HBM bounds both directions: 65536 x 4096 there and back, 1.36 GB,
+// take 238 us, 5.7 TB/s.
 constexpr int kRows = 4;
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {  // read once
