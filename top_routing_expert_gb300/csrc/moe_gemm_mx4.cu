@@ -23,13 +23,15 @@
 // CTA pairs (cta_group::2, M = 256) do the work, or single CTAs (M = 128) where
 // there are too few columns for the pairs.
 //
-// Measured, with what bounds it: 65536 rows x 4096 x 14336 over 8 experts 1.07 ms,
-// 7.2 PFLOP/s, the power limit (2.0 GHz at 1370 W) and the 51 bytes a clock that
-// each SM takes in; 98304 x 1408 x 2048 over 64 experts 134 us, requests to L2,
-// whose rows of codes are 704 bytes; 16 rows over 8 experts of 4096 x 14336 35 us,
-// 6.3 TB/s of weights; 96 over 64 of 2048 x 1408 with GELU 15.7 us, 4.9 TB/s;
-// 8191 over 16 of 1024 x 2816 with GELU 26 us, a start and an end of 7 us around
-// four rounds of tiles whose GELU takes longer than their products.
+// Measured with a cold L2, and what bounds it: 65536 rows x 4096 x 14336 over 8
+// experts 1.20 ms, 6.4 PFLOP/s (1.07 and 7.2 in short runs): the power limit
+// (2.0 GHz at 1370 W) and the 51 bytes a clock that each SM takes in; 98304 x 1408
+// x 2048 over 64 experts 139 us: requests to L2, whose rows of codes are 704
+// bytes; 16 rows over 8 experts of 4096 x 14336 44 us, 5.0 TB/s of weights; 96
+// over 64 of 2048 x 1408 with GELU 23 us, 3.4 TB/s, and 8191 over 16 of 1024 x
+// 2816 with GELU 29 us: a start and an end of some 7 us around two to four rounds
+// of tiles. Replayed from a graph, with weights left in L2, these three take 35,
+// 16 and 26 us; the comparisons below are such replays.
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
