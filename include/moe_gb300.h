@@ -385,8 +385,9 @@ MOE_API moe_status moe_layer_fwd_host_fp8(const moe_shape* s, int64_t n_micro,
  *   idx = the k experts of largest c in the kept groups, largest first
  *   w_j = scale * s_idx[j] / (sum over the chosen s if renormalize, else 1)
  * Equal values go to the lower index. The bias takes no part in the weights.
- * Which experts are chosen is what these formulas give in binary64 (fp32
- * arithmetic decides only where its error cannot matter). A logit of -inf
+ * Which experts are chosen is what these formulas give in binary64, with
+ * exponentials to a relative 2^-44 (fp32 arithmetic decides only where its
+ * error cannot matter). A logit of -inf
  * masks its expert: its score is 0 and it comes after every other expert (a
  * group with fewer than group_top unmasked experts has value -inf); a token
  * with fewer than k experts left gets masked ones, by index, at weight 0. A

@@ -127,6 +127,26 @@ def test_extreme_logits(score):
         assert (np.abs(got["w"][:5] - w) <= 800 * U * w + 1e-37).all()
 
 
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_a_last_place_apart(score, groups, keep):
+    """Scores that fp32 cannot order: all logits of a token are within a few units
+    in the last place of one value, so each decision needs the exact formulas.
+    Scores differ by 2^-34 of themselves or more there, far above 2^-44. (Sums of
+    two such scores need not: groups go by their best expert.)"""
+    T, E, k = 96, 128, 6
+    g = torch.Generator(device=DEV).manual_seed(11)
+    base = torch.linspace(-9.0, 9.0, T, device=DEV).unsqueeze(1)
+    steps = torch.randint(0, 40, (T, E), generator=g, device=DEV, dtype=torch.int32)
+    logits = (base.contiguous().view(torch.int32) + steps).view(torch.float32)
+    bias = 0.25 * torch.randint(0, 2, (E,), generator=g, device=DEV).float()
+    for b in (None, bias):
+        cfg = dict(score=score, n_groups=groups, topk_groups=keep)
+        got = _run(logits, b, k, **cfg)
+        assert got["status"][0] == 0
+        _check(logits, b, k, got, **cfg)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masked_experts_and_empty_rows(score):
     T, E, k = 130, 24, 4
