@@ -570,7 +570,7 @@ struct TopList {
 };
 
 // KD: at least k, of 2, 4 and 8. N: 16-byte pieces per lane (8, or 2 for few
-// tokens, which also keeps that code short). kWhole: E = 4 N P, no piece missing.
+// logits, which also keeps that code short). kWhole: E = 4 N P, no piece missing.
 // 131072 tokens of 128 experts, top-2 with bias and statistics: 31 us, where the
 // bytes take 10. 16 warps to an SM (128 registers a thread) issue in 45 % of the
 // clocks, half of it comparisons of the lists; waits are for the row and for
