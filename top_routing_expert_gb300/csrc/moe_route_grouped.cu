@@ -1127,6 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
         for (int e = sub; e < E; e += L) out[e] = row[e];
       }
     }
+    __syncwarp();  // the next token's stores to the row come after other lanes' reads of it
   }
 }
 
