@@ -562,12 +562,13 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// Arrive on an mbarrier of the cluster by its shared::cluster address, ordering
-// this CTA's earlier accesses (release at CTA scope). At cluster scope the
-// release waits for every load the thread has in flight.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+// Arrive on an mbarrier of the cluster by its shared::cluster address, releasing
+// at cluster scope the writes to this CTA's shared memory that this thread has
+// made or acquired. Restricted to shared memory, the fence does not wait for the
+// thread's loads from global memory, as a full release would.
+__device__ __forceinline__ void mbar_arrive_release_shared(uint32_t cluster_addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_cluster(cluster_addr);
 }
 
 // 16 TMEM lanes x 32 columns in the fragment layout of 8x8 matrices: for each
