@@ -75,11 +75,20 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN where one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 // GELU-tanh of two values: 0.5 u (1 + tanh z) = u / (1 + 2^(-2 log2(e) z)), z =
 // sqrt(2/pi) (u + 0.044715 u^3). The two quotients share one reciprocal, so a
 // value takes 1.5 special-function operations (4 a clock and SM sub-partition),
 // which bound this epilogue. The exponent is held at 60, so that the product of
-// the denominators stays finite: the result there is below 2^-56, not smaller.
+// the denominators stays finite, and the numerator at -7.5, from where on it is:
+// the result there is -7.5 x 2^-60 for values between that and -0, -inf's too.
+// (Choosing 0 instead: 30.1 us for the ragged product with GELU, this 28.7.) A NaN
+// stays one, and its neighbour a value.
 __device__ __forceinline__ void gelu_tanh_x2(uint32_t& x, uint32_t& y) {
   const float u = __uint_as_float(x), v = __uint_as_float(y);
   const uint64_t uv = f32x2(u, v);
@@ -92,7 +101,7 @@ __device__ __forceinline__ void gelu_tanh_x2(uint32_t& x, uint32_t& y) {
                                 f32x2(1.0f, 1.0f));
   f32x2_get(ab, a, b);
   const float r = rcp_approx(a * b);
-  f32x2_get(f32x2_mul(uv, f32x2_mul(f32x2(r, r), f32x2(b, a))), a, b);
+  f32x2_get(f32x2_mul(f32x2(max_nan(u, -7.5f), max_nan(v, -7.5f)), f32x2_mul(f32x2(r, r), f32x2(b, a))), a, b);
   x = __float_as_uint(a);
   y = __float_as_uint(b);
 }
