@@ -756,16 +756,26 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
           make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     }
     __syncwarp();
-    // A score's error is within 2^-21 of the row's largest score (2^-17 where all
-    // logits are far below zero and the exponent's rounding counts), and the bias
-    // adds a rounding: values closer than `near` are decided again.
-    const float near_abs = smax * (softmax || smax > 1e-3f ? 0x1p-20f : 0x1p-16f);
-    auto near = [&](float u, float v) {  // false where either is not finite
-      return fabsf(u - v) < fmaf(0x1p-22f, fmaxf(fabsf(u), fabsf(v)), near_abs);
+    // Values closer than `near` are decided again. With u = 2^-24, a rounding's share,
+    // 4 u of itself for ex2 and 2 u for rcp, a score is off by at most:
+    //  sigmoid: s (1 - s) (1.23 |l| + 4) u + 3 s u (the argument -l log2e and its
+    //    constant, ex2; the sum and rcp), over all l <= m below (5 + 2 max(0, -m)) u smax;
+    //  softmax: (2.23 d + 4) exp(-d) u, at most 4 u of the largest, d = m - l. The divisor is
+    //    off by 32.5 u (the terms' average, 2.23 x 3.34 + 4; 19 roundings of the sum;
+    //    rcp), one factor for the row, which counts only where a bias is added: by that
+    //    much of the scores' difference.
+    // Two values: twice that. The bias adds a rounding to each, u of the value.
+    // Group values that are sums of two scores: twice as much again, and a rounding.
+    constexpr float kU = 0x1p-24f;
+    const float near_one = smax * (softmax ? (a.bias != nullptr ? 44.f * kU : 11.f * kU)
+                                           : fmaf(fmaxf(-m, 0.f), 4.1f * kU, 11.f * kU));
+    auto near = [](float u, float v, float rel, float abs) {  // false where either is not finite
+      return fabsf(u - v) < fmaf(rel, fmaxf(fabsf(u), fabsf(v)), abs);
     };
     bool unsure = smax < 1e-30f;
     uint32_t certain = 1u;  // the kept groups, or 0 where they are in doubt
     if (G > 1) {
+      const float near_group = a.group_top == 2 ? 2.f * near_one : near_one;
       for (int g = sub; g < G; g += P) {
         float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
         auto see = [&](float u) {
@@ -792,7 +802,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
         int ahead = 0, sure = 0, maybe = 0;
         for (int h = 0; h < G; ++h) {
           const float o = gv[h];
-          const bool close = near(o, u);
+          const bool close = near(o, u, 4.f * kU, near_group);
           ahead += (o > u || (o == u && h < g)) ? 1 : 0;
           sure += (o > u && !close) ? 1 : 0;
           maybe += (h != g && (o > u || close)) ? 1 : 0;
@@ -840,7 +850,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
 #pragma unroll
     for (int i = 0; i < KD; ++i)
       if (i < a.k) {
-        unsure |= near(top.v[i], i + 1 < KD ? top.v[i + 1] : top.rest);
+        unsure |= near(top.v[i], i + 1 < KD ? top.v[i + 1] : top.rest, 4.f * kU, near_one);
         last = top.v[i];
       }
     unsure |= last == -CUDART_INF_F;  // fewer than k left
