@@ -155,3 +155,34 @@ def test_two_counterexamples():
                                                  "-0x1.b9f246p+2", "-0x1.b9dc84p+2")]], np.float32)
     for r in (rows, rows[:, [2, 3, 0, 1]]):
         _assert_choice(r, None, 2, "sigmoid", n_groups=2, topk_groups=1, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [8.0, 1000.0, 1e5])
+def test_group_sums_that_cancel(score, big):
+    """Biases of opposite signs and far above the scores: a group's sum is much
+    smaller than the two values whose fp32 roundings are in it."""
+    rng = np.random.default_rng(int(big))
+    T, E, G = 20000, 16, 8
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    bias = np.tile([big, -big], G).astype(np.float32)
+    _assert_choice(l, bias, 4, score, n_groups=G, topk_groups=3, group_top=2)
+    bias[4:8] = [big, -big + 0.5, big, 0.25]
+    _assert_choice(l, bias, 4, score, n_groups=G, topk_groups=3, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_past_fp32(score):
+    """Finite biases whose sums are not finite in fp32: they differ from one
+    another, and from those of masked groups, all the same."""
+    rng = np.random.default_rng(3)
+    T, E, G = 500, 16, 8
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[:, 0:2] = -np.inf
+    high = np.zeros(E, np.float32)
+    high[4:10] = [2e38, 2e38, 3e38, 3e38, 3e38, 2e38]
+    low = np.full(E, -3e38, np.float32)
+    low[12:] = [-2.5e38, -2.0e38, -3.4e38, -3.4e38]
+    for bias in (high, low):
+        for keep in (1, 2, 3):
+            _assert_choice(l, bias, 2, score, n_groups=G, topk_groups=keep, group_top=2)

@@ -765,7 +765,10 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     //    rcp), one factor for the row, which counts only where a bias is added: by that
     //    much of the scores' difference.
     // Two values: twice that. The bias adds a rounding to each, u of the value.
-    // Group values that are sums of two scores: twice as much again, and a rounding.
+    // Group values that are sums of two scores: twice as much again, and a rounding. Of
+    // two values that cancel more is left of their own roundings, 2 u of the smaller for
+    // each sum: with that above smax / 4 + |sum| / 8, or a sum past fp32's range (as
+    // biases can make both), the groups are in doubt.
     constexpr float kU = 0x1p-24f;
     const float near_one = smax * (softmax ? (a.bias != nullptr ? 44.f * kU : 11.f * kU)
                                            : fmaf(fmaxf(-m, 0.f), 4.1f * kU, 11.f * kU));
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     bool unsure = smax < 1e-30f;
     uint32_t certain = 1u;  // the kept groups, or 0 where they are in doubt
     if (G > 1) {
-      const float near_group = a.group_top == 2 ? 2.f * near_one : near_one;
+      const float near_group = a.group_top == 2 ? fmaf(kU, smax, 2.f * near_one) : near_one;
       for (int g = sub; g < G; g += P) {
         float v1 = -CUDART_INF_F, v2 = -CUDART_INF_F;
         auto see = [&](float u) {
@@ -793,7 +796,13 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
         } else {
           for (int q = 0; q < S; ++q) see(row[g * S + q]);
         }
-        gv[g] = a.group_top == 2 ? v1 + v2 : v1;
+        float v = v1;
+        if (a.group_top == 2) {
+          v = v1 + v2;
+          unsure |= v2 != -CUDART_INF_F &&
+                    (!(fabsf(v) < CUDART_INF_F) || fminf(v1, -v2) > fmaf(0.125f, fabsf(v), 0.25f * smax));
+        }
+        gv[g] = v;
       }
       __syncwarp();
       uint32_t kept = 0u;
@@ -802,7 +811,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
         int ahead = 0, sure = 0, maybe = 0;
         for (int h = 0; h < G; ++h) {
           const float o = gv[h];
-          const bool close = near(o, u, 4.f * kU, near_group);
+          const bool close = near(o, u, 4.5f * kU, near_group);
           ahead += (o > u || (o == u && h < g)) ? 1 : 0;
           sure += (o > u && !close) ? 1 : 0;
           maybe += (h != g && (o > u || close)) ? 1 : 0;
