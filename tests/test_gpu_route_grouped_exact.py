@@ -186,3 +186,24 @@ def test_group_sums_past_fp32(score):
     for bias in (high, low):
         for keep in (1, 2, 3):
             _assert_choice(l, bias, 2, score, n_groups=G, topk_groups=keep, group_top=2)
+
+
+def test_choice_where_scores_are_smallest():
+    """Softmax differences and sigmoid logits beyond 700: binary64 tells the scores
+    apart to exp(-745) and 1 / (1 + exp(709)), and beyond that they are equal."""
+    row = np.array([0, -705, -701, -703, -720, -742, -740, -800, -900, -702.5], np.float32)
+    rng = np.random.default_rng(0)
+    l = np.stack([row[rng.permutation(10)] for _ in range(64)])
+    l[::2] += np.float32(3.0)
+    l[::3] = np.where(l[::3] == l[::3].max(axis=1, keepdims=True), l[::3], l[::3] - 0.125)
+    for k in (3, 8):
+        _assert_choice(l, None, k, "softmax")
+        _assert_choice(l, np.full(10, 1e-30, np.float32), k, "softmax")
+    _assert_choice(l, None, 4, "softmax", n_groups=5, topk_groups=3, group_top=2)
+    low = np.array([-700.5, -703, -701, -708.25, -702, -699, -706, -701.5], np.float32)
+    s = np.stack([low[rng.permutation(8)] for _ in range(64)])
+    for k in (1, 4, 8):
+        _assert_choice(s, None, k, "sigmoid")
+    _assert_choice(s, None, 2, "sigmoid", n_groups=4, topk_groups=2, group_top=2)
+    far = np.tile(np.array([-900, -1000, -800, -1e30], np.float32), (3, 1))
+    assert (_route(far, None, 3, score="sigmoid")[0] == [0, 1, 2]).all()   # all are 0

@@ -183,11 +183,12 @@ __device__ __forceinline__ Two lanes_sum(Two v) {
 // 2^n of n in -126 .. 127
 __device__ __forceinline__ float power2(int n) { return __int_as_float((n + 127) << 23); }
 
-// exp(x) 2^-n to 45 bits: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor
-// series of exp(r) to r^13 / 13! (the next term is below 2^-57), its terms from
-// r^7 on (below 2^-22) in plain fp32. x is held to where fp64's exp has a value.
+// exp(x) 2^-n to 45 bits: x = n ln 2 + r with |r| <= ln 2 / 2 (the reduction of Cody
+// and Waite), and the Taylor series of exp(r) to r^13 / 13! (the next term is below
+// 2^-57), its terms from r^7 on (below 2^-22) in plain fp32. x is held to 750 either
+// way, past where fp64's exp is 0 or infinite.
 __device__ __forceinline__ Two exp_parts(Two x, int& n) {
-  if (!(fabsf(x.hi) < 700.f)) x = {copysignf(700.f, x.hi), 0.f};
+  if (!(fabsf(x.hi) < 750.f)) x = {copysignf(750.f, x.hi), 0.f};
   const float nf = rintf(x.hi * kLog2e);
   n = static_cast<int>(nf);
   // ln 2 in three parts; products of the first, of 12 bits, with n are exact
@@ -228,19 +229,28 @@ __device__ __forceinline__ Two exp_parts(Two x, int& n) {
 
 // The score as fp64: exp(x - m) / z, or the sigmoid of x. The latter's last two
 // steps are fp64's own: scores next to 1 are equal, or not, as they round there.
+// And so are all steps where the exponential is next to fp64's limits.
 __device__ __noinline__ double score64(float x, float m, bool softmax, Two z) {
   int n;
   Two v = exp_parts(softmax ? two_sum(x, -m) : Two{-x, 0.f}, n);
-  if (softmax) v = divide(v, z);
+  const bool inner = abs(n) <= 960;
+  if (softmax && inner) v = divide(v, z);
   double y = static_cast<double>(v.hi) + static_cast<double>(v.lo);
-  y = __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
+  if (inner) {
+    y = __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
+  } else {  // rounded once, to what is left of the bits, to 0 or to infinity
+    auto power = [](int e) { return __longlong_as_double(static_cast<long long>(e + 1023) << 52); };
+    y = y * power(n >> 1) * power(n - (n >> 1));
+    if (softmax) y /= static_cast<double>(z.hi) + static_cast<double>(z.lo);
+  }
   return softmax ? y : 1.0 / (1.0 + y);
 }
 
 // Only experts that may matter are evaluated so: those whose fp32 value is
 // within `slack` of the group_top-th of their group, then those within it of a
 // lower bound of the kept groups' k-th. All others rank below them whatever the
-// error. (A softmax with a bias needs its sum so too, hence all exponentials.)
+// error. (A softmax with a bias needs its sum so too, hence all exponentials, and so
+// does one with scores next to fp64's smallest, where the quotients may be equal.)
 // Few tokens come here, on any SM, and the last of them holds up the launch, so
 // loads are made at once and loops kept short.
 // known: the kept groups where they are not in doubt, else 0; kth: with them
@@ -253,7 +263,6 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   const uint32_t inv = a.n_groups > 1 ? 65536u / static_cast<uint32_t>(S) + 1u : 0u;  // e / S = e inv >> 16, e < 256
   const float* row = a.logits + static_cast<int64_t>(t) * E;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  const bool all = softmax && a.bias != nullptr;
   const long long kInf = order64(-CUDART_INF);
   float m = -CUDART_INF_F, smax = 0.f, z = 0.f, big = 0.f;
   float x[kPer], c[kPer];
@@ -267,6 +276,10 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   }
   m = lanes_max<32>(m);
   if (m == -CUDART_INF_F) m = 0.f;  // nothing unmasked
+  bool deep = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) deep |= x[i] != -CUDART_INF_F && x[i] - m < -690.f;
+  const bool all = softmax && (a.bias != nullptr || __any_sync(kFull, deep));
   Two zz{0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
@@ -305,7 +318,8 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   big = fmaxf(lanes_max<32>(big), smax);
   // fp32 errors are within 2^-18 of the largest value (2^-14 where the logits are
   // so low that exp's argument is what errs)
-  const float slack = big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
+  const float slack = smax < 1e-30f ? CUDART_INF_F  // fp32 holds them as 0, or nearly so
+                                    : big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
   __syncwarp();
   uint32_t kept = a.n_groups > 1 ? known : 1u;
   int n = 0;
