@@ -229,28 +229,39 @@ __device__ __forceinline__ Two exp_parts(Two x, int& n) {
 
 // The score as fp64: exp(x - m) / z, or the sigmoid of x. The latter's last two
 // steps are fp64's own: scores next to 1 are equal, or not, as they round there.
-// And so are all steps where the exponential is next to fp64's limits.
 __device__ __noinline__ double score64(float x, float m, bool softmax, Two z) {
   int n;
   Two v = exp_parts(softmax ? two_sum(x, -m) : Two{-x, 0.f}, n);
-  const bool inner = abs(n) <= 960;
-  if (softmax && inner) v = divide(v, z);
+  if (softmax) v = divide(v, z);
   double y = static_cast<double>(v.hi) + static_cast<double>(v.lo);
-  if (inner) {
-    y = __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
-  } else {  // rounded once, to what is left of the bits, to 0 or to infinity
-    auto power = [](int e) { return __longlong_as_double(static_cast<long long>(e + 1023) << 52); };
-    y = y * power(n >> 1) * power(n - (n >> 1));
-    if (softmax) y /= static_cast<double>(z.hi) + static_cast<double>(z.lo);
-  }
+  y = __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
   return softmax ? y : 1.0 / (1.0 + y);
+}
+
+// The same where the exponential is next to fp64's limits: rounded to the bits that
+// are left there, to 0 or to infinity, and all that follows in fp64, so that scores
+// are equal where it makes them so. The sum over the row's logits xs is formed here.
+__device__ __noinline__ double score64_far(float x, float m, bool softmax, const float* xs, int E) {
+  auto power = [](int e) { return __longlong_as_double(static_cast<long long>(e + 1023) << 52); };
+  int n;
+  Two v = exp_parts(softmax ? two_sum(x, -m) : Two{-x, 0.f}, n);
+  const double y = (static_cast<double>(v.hi) + static_cast<double>(v.lo)) * power(n >> 1) * power(n - (n >> 1));
+  if (!softmax) return 1.0 / (1.0 + y);
+  if (y == 0.0) return y;
+  double z = 0.0;
+#pragma unroll 1
+  for (int e = 0; e < E; ++e)
+    if (xs[e] != -CUDART_INF_F) {
+      v = exp_parts(two_sum(xs[e], -m), n);
+      if (n > -200) z += (static_cast<double>(v.hi) + static_cast<double>(v.lo)) * power(n);
+    }
+  return y / z;
 }
 
 // Only experts that may matter are evaluated so: those whose fp32 value is
 // within `slack` of the group_top-th of their group, then those within it of a
 // lower bound of the kept groups' k-th. All others rank below them whatever the
-// error. (A softmax with a bias needs its sum so too, hence all exponentials, and so
-// does one with scores next to fp64's smallest, where the quotients may be equal.)
+// error. (A softmax with a bias needs its sum so too, hence all exponentials.)
 // Few tokens come here, on any SM, and the last of them holds up the launch, so
 // loads are made at once and loops kept short.
 // known: the kept groups where they are not in doubt, else 0; kth: with them
@@ -263,6 +274,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   const uint32_t inv = a.n_groups > 1 ? 65536u / static_cast<uint32_t>(S) + 1u : 0u;  // e / S = e inv >> 16, e < 256
   const float* row = a.logits + static_cast<int64_t>(t) * E;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const bool all = softmax && a.bias != nullptr;
   const long long kInf = order64(-CUDART_INF);
   float m = -CUDART_INF_F, smax = 0.f, z = 0.f, big = 0.f;
   float x[kPer], c[kPer];
@@ -276,10 +288,6 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   }
   m = lanes_max<32>(m);
   if (m == -CUDART_INF_F) m = 0.f;  // nothing unmasked
-  bool deep = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) deep |= x[i] != -CUDART_INF_F && x[i] - m < -690.f;
-  const bool all = softmax && (a.bias != nullptr || __any_sync(kFull, deep));
   Two zz{0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
@@ -378,7 +386,8 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
       const float l = sc.x[e];
       double v = -CUDART_INF;
       if (l != -CUDART_INF_F) {
-        v = score64(l, m, softmax, zz);
+        v = fabsf(softmax ? l - m : l) < 660.f ? score64(l, m, softmax, zz)
+                                               : score64_far(l, m, softmax, sc.x, E);
         if (a.bias != nullptr) v += static_cast<double>(bias[e]);
       }
       sc.val[q] = order64(v);
