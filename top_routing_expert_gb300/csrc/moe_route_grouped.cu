@@ -483,9 +483,9 @@ __device__ __forceinline__ uint32_t find_masked(float (&l)[kV], uint32_t& status
 }
 
 // The lane's scores in pairs (softmax: exp(l - m), not yet divided by their sum
-// over the row), 0 where masked.
+// over the row), 0 where masked and past E.
 template <int L>
-__device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool softmax,
+__device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool softmax, int E, int sub,
                                        uint64_t (&s)[kV / 2], float& m) {
   m = 0.f;
   float x[kV];
@@ -495,6 +495,11 @@ __device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool s
     for (int i = 1; i + 1 < kV; i += 2) m = max3(m, l[i], l[i + 1]);
     m = fmaxf(m, l[kV - 1]);
     m = lanes_max<L>(m);
+    if (__any_sync(kFull, m == -kLowest)) {  // a row as low as what stands past E
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (4 * (sub + L * (i / 4)) + i % 4 >= E) mk |= 1u << i;
+    }
 #pragma unroll
     for (int i = 0; i < kV; i += 2)
       f32x2_get(f32x2_mul(f32x2_add(f32x2(l[i], l[i + 1]), f32x2(-m, -m)), f32x2(kLog2e, kLog2e)), x[i],
@@ -696,7 +701,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     float c0, c1;
     f32x2_get(chk, c0, c1);
-    const bool has_mask = __any_sync(kFull, !(c0 + c1 == 0.f));
+    bool has_mask = __any_sync(kFull, !(c0 + c1 == 0.f));
     uint32_t mk = 0u;
     if (has_mask) {
       m = -kLowest;
@@ -712,7 +717,15 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     m = lanes_max<P>(m);
     // scores: softmax not yet divided by their sum. Past E they are those of the
-    // lowest value: 0 unless the whole row is that low, which is decided again.
+    // lowest value: 0, unless the whole row is that low and they have to be left out.
+    if constexpr (!kWhole) {
+      if (__any_sync(kFull, m == -kLowest)) {
+        has_mask = true;
+#pragma unroll
+        for (int i = 0; i < kX; ++i)
+          if (4 * (sub + P * (i / 4)) + i % 4 >= E) mk |= 1u << i;
+      }
+    }
     if (softmax) {
       MOE_PIECES(i) {
 #pragma unroll
@@ -1080,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     float m = 0.f, iz = 0.f;
     if (need_p) {
       const uint32_t mk = find_masked(l, status);
-      scores<L>(l, mk, softmax, s, m);
+      scores<L>(l, mk, softmax, E, sub, s, m);
       const float z = lanes_sum<L>(pairs_sum(s));
       iz = z > 0.f ? rcp_approx(z) : 0.f;
     }
