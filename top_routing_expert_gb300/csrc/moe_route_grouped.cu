@@ -436,17 +436,17 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
 
 // ------------------------------------------------------------- kernel ----
 
-// The lane's kV logits of row t, pieces of four: sub, sub + L, ...; the type's
-// lowest value past E or T.
+// The lane's kV logits of row t, pieces of four: sub, sub + L, ...; `none` past E
+// or T.
 template <int L>
 __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64_t t, bool valid,
-                                         int E, int sub, float (&l)[kV]) {
+                                         int E, int sub, float none, float (&l)[kV]) {
   const float* row = logits + t * E;
   if ((E & 3) == 0) {
 #pragma unroll
     for (int h = 0; h < kV / 4; ++h) {
       const int e = 4 * (sub + L * h);
-      float4 v = make_float4(-kLowest, -kLowest, -kLowest, -kLowest);
+      float4 v = make_float4(none, none, none, none);
       if (valid && e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
       l[4 * h] = v.x;
       l[4 * h + 1] = v.y;
@@ -457,65 +457,50 @@ __device__ __forceinline__ void load_row(const float* __restrict__ logits, int64
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int e = 4 * (sub + L * (i / 4)) + i % 4;
-      l[i] = valid && e < E ? __ldg(row + e) : -kLowest;
+      l[i] = valid && e < E ? __ldg(row + e) : none;
     }
   }
 }
 
-// Masked experts of the lane (bits), their logits set to the lowest value. A
-// multiply-add per pair of logits finds whether there is any.
-__device__ __forceinline__ uint32_t find_masked(float (&l)[kV], uint32_t& status) {
+// Experts of the lane that are masked, or past E (bits).
+template <int L>
+__device__ __forceinline__ uint32_t left_out(const float (&l)[kV], int E, int sub) {
+  uint32_t mk = 0u;
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+    if (masked(l[i]) || 4 * (sub + L * (i / 4)) + i % 4 >= E) mk |= 1u << i;
+  return mk;
+}
+
+// The lane's softmax scores in pairs, exp(l - m) not yet divided by their sum over
+// the row; 0 where masked and past E, where `l` holds the type's lowest value.
+template <int L>
+__device__ __forceinline__ void softmax_scores(float (&l)[kV], int E, int sub, uint64_t (&s)[kV / 2], float& m) {
+  // a multiply-add per pair of logits finds whether one is not finite
   uint64_t chk = f32x2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < kV; i += 2) chk = f32x2_fma(f32x2(l[i], l[i + 1]), f32x2(0.f, 0.f), chk);
   float c0, c1;
   f32x2_get(chk, c0, c1);
-  if (!__any_sync(kFull, !(c0 + c1 == 0.f))) return 0u;
   uint32_t mk = 0u;
+  if (__any_sync(kFull, !(c0 + c1 == 0.f))) {
+    mk = left_out<L>(l, E, sub);
 #pragma unroll
-  for (int i = 0; i < kV; ++i)
-    if (masked(l[i])) {
-      mk |= 1u << i;
-      if (l[i] != -CUDART_INF_F) status |= MOE_DEV_NONFINITE;
-      l[i] = -kLowest;
-    }
-  return mk;
-}
-
-// The lane's scores in pairs (softmax: exp(l - m), not yet divided by their sum
-// over the row), 0 where masked and past E.
-template <int L>
-__device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool softmax, int E, int sub,
-                                       uint64_t (&s)[kV / 2], float& m) {
-  m = 0.f;
-  float x[kV];
-  if (softmax) {
-    m = l[0];
-#pragma unroll
-    for (int i = 1; i + 1 < kV; i += 2) m = max3(m, l[i], l[i + 1]);
-    m = fmaxf(m, l[kV - 1]);
-    m = lanes_max<L>(m);
-    if (__any_sync(kFull, m == -kLowest)) {  // a row as low as what stands past E
-#pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (4 * (sub + L * (i / 4)) + i % 4 >= E) mk |= 1u << i;
-    }
-#pragma unroll
-    for (int i = 0; i < kV; i += 2)
-      f32x2_get(f32x2_mul(f32x2_add(f32x2(l[i], l[i + 1]), f32x2(-m, -m)), f32x2(kLog2e, kLog2e)), x[i],
-                x[i + 1]);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) x[i] = exp2_approx(x[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kV; i += 2) {
-      float y0, y1;
-      f32x2_get(f32x2_mul(f32x2(l[i], l[i + 1]), f32x2(-kLog2e, -kLog2e)), y0, y1);
-      f32x2_get(f32x2_add(f32x2(exp2_approx(y0), exp2_approx(y1)), f32x2(1.f, 1.f)), y0, y1);
-      x[i] = rcp_approx(y0);
-      x[i + 1] = rcp_approx(y1);
-    }
+    for (int i = 0; i < kV; ++i)
+      if ((mk >> i) & 1u) l[i] = -kLowest;
   }
+  m = l[0];
+#pragma unroll
+  for (int i = 1; i + 1 < kV; i += 2) m = max3(m, l[i], l[i + 1]);
+  m = fmaxf(m, l[kV - 1]);
+  m = lanes_max<L>(m);
+  if (__any_sync(kFull, m == -kLowest)) mk |= left_out<L>(l, E, sub);  // a row as low as what stands past E
+  float x[kV];
+#pragma unroll
+  for (int i = 0; i < kV; i += 2)
+    f32x2_get(f32x2_mul(f32x2_add(f32x2(l[i], l[i + 1]), f32x2(-m, -m)), f32x2(kLog2e, kLog2e)), x[i], x[i + 1]);
+#pragma unroll
+  for (int i = 0; i < kV; ++i) x[i] = exp2_approx(x[i]);
   if (mk != 0u) {
 #pragma unroll
     for (int i = 0; i < kV; ++i)
@@ -523,6 +508,47 @@ __device__ __forceinline__ void scores(const float (&l)[kV], uint32_t mk, bool s
   }
 #pragma unroll
   for (int i = 0; i < kV; i += 2) s[i / 2] = f32x2(x[i], x[i + 1]);
+}
+
+// The lane's sigmoid slopes s (1 - s) in pairs, from e = exp(-l) as e s s (of a score
+// next to 1 the difference to 1 would be lost in s itself), and its sums of s and of
+// s h. Past E, where h is 0, `l` holds kFar, whose score of 2^-121 is nothing beside
+// the others' of logits above -60; `limit` tells by the sum of squares that all are
+// within 60 of zero, or the careful way is taken.
+constexpr float kFar = -84.f;
+__device__ __forceinline__ float square_limit(int past) { return 3600.f + static_cast<float>(past) * (kFar * kFar); }
+template <int L>
+__device__ __forceinline__ void sigmoid_slopes(float (&l)[kV], const uint64_t (&h)[kV / 2], float limit, int E,
+                                               int sub, uint64_t (&w)[kV / 2], float& sum, float& sum_h) {
+  uint64_t sq = f32x2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kV; i += 2) sq = f32x2_fma(f32x2(l[i], l[i + 1]), f32x2(l[i], l[i + 1]), sq);
+  float c0, c1;
+  f32x2_get(sq, c0, c1);
+  uint32_t mk = 0u;
+  if (__any_sync(kFull, !(c0 + c1 < limit))) {
+    mk = left_out<L>(l, E, sub);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) l[i] = (mk >> i) & 1u ? kFar : fmaxf(l[i], kFar);
+  }
+  const uint64_t one = f32x2(1.f, 1.f);
+  uint64_t z = f32x2(0.f, 0.f), zh = z;
+#pragma unroll
+  for (int i = 0; i < kV; i += 2) {
+    float y0, y1;
+    f32x2_get(f32x2_mul(f32x2(l[i], l[i + 1]), f32x2(-kLog2e, -kLog2e)), y0, y1);
+    const uint64_t e = f32x2(exp2_approx(y0), exp2_approx(y1));
+    f32x2_get(f32x2_add(e, one), y0, y1);
+    uint64_t s = f32x2(rcp_approx(y0), rcp_approx(y1));
+    if (mk != 0u) s = f32x2((mk >> i) & 1u ? 0.f : rcp_approx(y0), (mk >> (i + 1)) & 1u ? 0.f : rcp_approx(y1));
+    z = f32x2_add(z, s);
+    zh = f32x2_fma(s, h[i / 2], zh);
+    w[i / 2] = f32x2_mul(f32x2_mul(e, s), s);
+  }
+  f32x2_get(z, c0, c1);
+  sum = c0 + c1;
+  f32x2_get(zh, c0, c1);
+  sum_h = c0 + c1;
 }
 __device__ __forceinline__ float pairs_sum(const uint64_t (&s)[kV / 2]) {
   float a, b;
@@ -1041,7 +1067,11 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
                    e + 1 < E ? f * static_cast<float>(a.routed[e + 1]) : 0.f);
     }
   }
-  uint32_t status = 0;  // the forward has reported
+  const float none = softmax ? -kLowest : kFar;  // past E
+  int past = 0;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) past += 4 * (sub + L * (i / 4)) + i % 4 >= E ? 1 : 0;
+  const float limit = square_limit(past);
   const int64_t per_pass = static_cast<int64_t>(gridDim.x) * kWarps * kTok;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTok;
   // The next token's row and chosen logits, and the slots of the one after it,
@@ -1061,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     }
   };
   auto fetch = [&](int64_t t) {  // the token whose slots were fetched last
-    if (need_p) load_row<L>(a.logits, t < a.T ? t : 0, t < a.T, E, sub, next);
+    if (need_p) load_row<L>(a.logits, t < a.T ? t : 0, t < a.T, E, sub, none, next);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       next_e[q] = after_e[q];
@@ -1090,12 +1120,27 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     }
     fetch(t + per_pass);
     fetch_slots(t + 2 * per_pass);
-    float m = 0.f, iz = 0.f;
+    // s: softmax scores, or slopes of sigmoid scores
+    float m = 0.f, iz = 0.f, ph = 0.f;
     if (need_p) {
-      const uint32_t mk = find_masked(l, status);
-      scores<L>(l, mk, softmax, E, sub, s, m);
-      const float z = lanes_sum<L>(pairs_sum(s));
+      float z;
+      if (softmax) {
+        softmax_scores<L>(l, E, sub, s, m);
+        z = pairs_sum(s);
+        if (aux) {
+          uint64_t acc = f32x2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < kV / 2; ++i) acc = f32x2_fma(s[i], h[i], acc);
+          float u, v;
+          f32x2_get(acc, u, v);
+          ph = u + v;
+        }
+      } else {
+        sigmoid_slopes<L>(l, h, limit, E, sub, s, z, ph);
+      }
+      z = lanes_sum<L>(z);
       iz = z > 0.f ? rcp_approx(z) : 0.f;
+      if (aux) ph = lanes_sum<L>(ph) * iz;
     }
     // the chosen slots: in the first lanes of the token
     constexpr int kLanes = L < kMaxTopK ? L : kMaxTopK;
@@ -1142,22 +1187,11 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
 #pragma unroll
     for (int i = 0; i < kV / 2; ++i) grad[i] = f32x2(0.f, 0.f);
     if (need_p) {
-      float ph = 0.f;
-      if (aux) {
-        uint64_t acc = f32x2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kV / 2; ++i) acc = f32x2_fma(s[i], h[i], acc);
-        float u, v;
-        f32x2_get(acc, u, v);
-        ph = lanes_sum<L>(u + v) * iz;
-      }
       if (softmax && !a.renormalize) ph += dot;
       const float c = -ph * iz;
 #pragma unroll
       for (int i = 0; i < kV / 2; ++i) {
-        const uint64_t d = f32x2_fma(h[i], f32x2(iz, iz), f32x2(c, c));
-        const uint64_t p = softmax ? s[i] : f32x2_fma(f32x2_mul(s[i], f32x2(-1.f, -1.f)), s[i], s[i]);
-        grad[i] = f32x2_mul(p, d);
+        grad[i] = f32x2_mul(s[i], f32x2_fma(h[i], f32x2(iz, iz), f32x2(c, c)));
       }
     }
     // the chosen experts' part is added in shared memory
