@@ -50,6 +50,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+// Where a row's largest logit is below this, 1 + exp(l) is 1 to fp32 and far beyond
+// for all of it, and its sigmoid scores are ratios that shifting the row leaves as
+// they are: it is shifted up to here where shares s / sum s are formed, which hold then
+// where the scores themselves are below fp32's smallest value.
+constexpr float kLowRow = -41.f;
 
 template <int L, class T, class Op>
 __device__ __forceinline__ T lanes_reduce(T v, Op op) {
@@ -514,7 +519,8 @@ __device__ __forceinline__ void softmax_scores(float (&l)[kV], int E, int sub, u
 // next to 1 the difference to 1 would be lost in s itself), and its sums of s and of
 // s h. Past E, where h is 0, `l` holds kFar, whose score of 2^-121 is nothing beside
 // the others' of logits above -60; `limit` tells by the sum of squares that all are
-// within 60 of zero, or the careful way is taken.
+// within 60 of zero, or the careful way is taken: the clamp there changes nothing that
+// counts beside the row's largest, which is at kLowRow or above.
 constexpr float kFar = -84.f;
 __device__ __forceinline__ float square_limit(int past) { return 3600.f + static_cast<float>(past) * (kFar * kFar); }
 template <int L>
@@ -528,8 +534,15 @@ __device__ __forceinline__ void sigmoid_slopes(float (&l)[kV], const uint64_t (&
   uint32_t mk = 0u;
   if (__any_sync(kFull, !(c0 + c1 < limit))) {
     mk = left_out<L>(l, E, sub);
+    float m = -kLowest;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) l[i] = (mk >> i) & 1u ? kFar : fmaxf(l[i], kFar);
+    for (int i = 0; i < kV; ++i) {
+      if ((mk >> i) & 1u) l[i] = -kLowest;
+      m = fmaxf(m, l[i]);
+    }
+    m = lanes_max<L>(m);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) l[i] = fmaxf(m < kLowRow ? l[i] - m + kLowRow : l[i], kFar);
   }
   const uint64_t one = f32x2(1.f, 1.f);
   uint64_t z = f32x2(0.f, 0.f), zh = z;
@@ -752,6 +765,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
           if (4 * (sub + P * (i / 4)) + i % 4 >= E) mk |= 1u << i;
       }
     }
+    float f = 1.f;  // a score's factor
     if (softmax) {
       MOE_PIECES(i) {
 #pragma unroll
@@ -763,6 +777,14 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
         }
       }
     } else {
+      // P takes shares. f undoes the shift; its error is the same for the whole row,
+      // and that of the shifted logits within what `near` allows below.
+      if (stats && __any_sync(kFull, m < kLowRow)) {
+        if (m < kLowRow) f = exp2_approx((m - kLowRow) * kLog2e);
+#pragma unroll
+        for (int i = 0; i < kX; ++i)
+          if (m < kLowRow) x[i] = x[i] - m + kLowRow;
+      }
       MOE_PIECES(i) {
 #pragma unroll
         for (int q = 4 * i; q < 4 * i + 4; q += 2) {
@@ -802,7 +824,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
       }
     }
     // selection values, -inf where masked or past E
-    const float f = softmax ? iz : 1.f;
+    if (softmax) f = iz;
     MOE_PIECES(i) {
       const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sh_bias + 4 * (sub + P * i));
       f32x2_get(f32x2_fma(f32x2(x[4 * i], x[4 * i + 1]), f32x2(f, f), b.x), x[4 * i], x[4 * i + 1]);
