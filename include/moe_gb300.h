@@ -424,8 +424,9 @@ MOE_API moe_status moe_route_grouped(const moe_shape* s, const moe_route_config*
  *        grad_topk_w [T,k]; grad_aux [1] with routed_counts [E] (the
  *        gradient of aux, routed_counts taken as constants), or NULL.
  *   out: grad_logits [T,E], every element written; 0 at masked experts.
- * An index outside [0,E) contributes nothing; a token's others are distinct. n_groups, topk_groups and
- * group_top take no part. Needs no workspace. */
+ * An index outside [0,E) and one of a masked expert contribute nothing,
+ * whatever grad_topk_w holds there; a token's others are distinct. n_groups,
+ * topk_groups and group_top take no part. Needs no workspace. */
 MOE_API moe_status moe_route_grouped_bwd(const moe_shape* s, const moe_route_config* cfg,
                                          const float* logits, const int32_t* topk_idx,
                                          const float* grad_topk_w, const float* grad_aux,

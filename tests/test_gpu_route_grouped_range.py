@@ -174,3 +174,26 @@ def test_balance_gradient_of_large_sigmoid_scores(E, masked):
     # p and 1 - s to (48 + 1.5 |l|) u of themselves, sum p h to (48 + 1.5 max |l|) u where p counts
     tol = 4 * (48 + 1.5 * np.minimum(np.abs(x), 100.0)) * U * p * rest * (h + ph)
     assert (np.abs(mine - ref) <= tol + 1e-37).all()
+
+
+@pytest.mark.parametrize("E,k", [(16, 3), (100, 8), (255, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_slots_that_contribute_nothing(E, k, score):
+    """Whatever gradient stands in the slot of a masked expert or of an index outside
+    the experts: the token's others are as if it were 0."""
+    T = 70
+    rng = np.random.default_rng(k)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    l[np.arange(0, T, 3), idx[::3, 0]] = -np.inf
+    idx[1::3, 1] = np.where(np.arange(len(idx[1::3])) % 2 == 0, -1, E)
+    zero, bad = gw.copy(), gw.copy()
+    for x, v in ((zero, (0.0, 0.0)), (bad, (np.nan, np.inf))):
+        x[::3, 0], x[1::3, 1] = v
+    routed = rng.integers(0, 9, E)
+    for renormalize in (True, False):
+        for ga in (None, 2.0):
+            one, other = (_gradient(l, idx, g, score, renormalize, 1.5, ga, None if ga is None else routed)
+                          for g in (zero, bad))
+            assert np.isfinite(one).all() and np.array_equal(one, other)

@@ -1136,9 +1136,9 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
     for (int i = 0; i < kV; ++i) l[i] = next[i];
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      gj[q] = next_g[q];
       x[q] = next_x[q];
       ej[q] = masked(x[q]) ? -1 : next_e[q];
+      gj[q] = ej[q] < 0 ? 0.f : next_g[q];  // whatever stands there
     }
     fetch(t + per_pass);
     fetch_slots(t + 2 * per_pass);
