@@ -387,7 +387,8 @@ MOE_API moe_status moe_layer_fwd_host_fp8(const moe_shape* s, int64_t n_micro,
  * Equal values go to the lower index. The bias takes no part in the weights.
  * Which experts are chosen is what these formulas give in binary64, with
  * exponentials to a relative 2^-44 (fp32 arithmetic decides only where its
- * error cannot matter). Shares of a sum of scores (renormalised weights, P and
+ * error cannot matter); softmax scores below its normal range are compared as
+ * exp(l - max l) is there, before the division. Shares of a sum of scores (renormalised weights, P and
  * the gradient of aux) hold where the scores themselves would underflow: those
  * of a token with an unmasked expert sum to 1. A logit of -inf
  * masks its expert: its score is 0 and it comes after every other expert (a

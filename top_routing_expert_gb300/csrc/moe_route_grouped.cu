@@ -51,10 +51,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 // Where a row's largest logit is below this, 1 + exp(l) is 1 to fp32 and far beyond
-// for all of it, and its sigmoid scores are ratios that shifting the row leaves as
-// they are: it is shifted up to here where shares s / sum s are formed, which hold then
-// where the scores themselves are below fp32's smallest value.
+// for all of it, and shifting the row leaves the shares s / sum s of its sigmoid scores
+// as they are: the gradient shifts it up to here, and they hold where the scores
+// themselves are below fp32's smallest value.
 constexpr float kLowRow = -41.f;
+// The forward's rows that fp32 does not hold: their scores are below 1e-30, or they
+// are no higher than what stands past E. They are decided again, and counted in P there.
+__device__ __forceinline__ bool tiny_row(float m, bool softmax) { return m < (softmax ? -1e38f : -69.f); }
 
 template <int L, class T, class Op>
 __device__ __forceinline__ T lanes_reduce(T v, Op op) {
@@ -233,34 +236,18 @@ __device__ __forceinline__ Two exp_parts(Two x, int& n) {
 }
 
 // The score as fp64: exp(x - m) / z, or the sigmoid of x. The latter's last two
-// steps are fp64's own: scores next to 1 are equal, or not, as they round there.
+// steps are fp64's own: scores next to 1 are equal, or not, as they round there. 2^n
+// comes in two factors, so that next to fp64's limits the result is rounded once, to
+// the bits that are left, to 0 or to infinity.
 __device__ __noinline__ double score64(float x, float m, bool softmax, Two z) {
   int n;
   Two v = exp_parts(softmax ? two_sum(x, -m) : Two{-x, 0.f}, n);
   if (softmax) v = divide(v, z);
-  double y = static_cast<double>(v.hi) + static_cast<double>(v.lo);
-  y = __longlong_as_double(__double_as_longlong(y) + (static_cast<long long>(n) << 52));
+  const int half = n >> 1;
+  const double y = (static_cast<double>(v.hi) + static_cast<double>(v.lo)) *
+                   __longlong_as_double(static_cast<long long>(half + 1023) << 52) *
+                   __longlong_as_double(static_cast<long long>(n - half + 1023) << 52);
   return softmax ? y : 1.0 / (1.0 + y);
-}
-
-// The same where the exponential is next to fp64's limits: rounded to the bits that
-// are left there, to 0 or to infinity, and all that follows in fp64, so that scores
-// are equal where it makes them so. The sum over the row's logits xs is formed here.
-__device__ __noinline__ double score64_far(float x, float m, bool softmax, const float* xs, int E) {
-  auto power = [](int e) { return __longlong_as_double(static_cast<long long>(e + 1023) << 52); };
-  int n;
-  Two v = exp_parts(softmax ? two_sum(x, -m) : Two{-x, 0.f}, n);
-  const double y = (static_cast<double>(v.hi) + static_cast<double>(v.lo)) * power(n >> 1) * power(n - (n >> 1));
-  if (!softmax) return 1.0 / (1.0 + y);
-  if (y == 0.0) return y;
-  double z = 0.0;
-#pragma unroll 1
-  for (int e = 0; e < E; ++e)
-    if (xs[e] != -CUDART_INF_F) {
-      v = exp_parts(two_sum(xs[e], -m), n);
-      if (n > -200) z += (static_cast<double>(v.hi) + static_cast<double>(v.lo)) * power(n);
-    }
-  return y / z;
 }
 
 // Only experts that may matter are evaluated so: those whose fp32 value is
@@ -270,9 +257,10 @@ __device__ __noinline__ double score64_far(float x, float m, bool softmax, const
 // Few tokens come here, on any SM, and the last of them holds up the launch, so
 // loads are made at once and loops kept short.
 // known: the kept groups where they are not in doubt, else 0; kth: with them
-// known, the k-th largest value found in fp32. bias: in shared memory.
+// known, the k-th largest value found in fp32. bias: in shared memory. share: the
+// warp's sums of the shares of rows that fp32 does not hold, or nullptr.
 __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t known, float kth,
-                                         const float* bias, const ExactScratch& sc, int* cnt) {
+                                         const float* bias, const ExactScratch& sc, int* cnt, float* share) {
   constexpr int kPer = kMaxExperts / 32;  // lane l: experts l, l + 32, ...
   const int lane = threadIdx.x & 31;
   const int E = a.E, S = a.E / a.n_groups;
@@ -331,8 +319,19 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
   big = fmaxf(lanes_max<32>(big), smax);
   // fp32 errors are within 2^-18 of the largest value (2^-14 where the logits are
   // so low that exp's argument is what errs)
-  const float slack = smax < 1e-30f ? CUDART_INF_F  // fp32 holds them as 0, or nearly so
-                                    : big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
+  float slack = big * (softmax || smax > 1e-3f ? 0x1p-17f : 0x1p-13f);
+  if (tiny_row(m, softmax)) {
+    slack = CUDART_INF_F;  // fp32 holds the scores as 0, or nearly so
+    if (share != nullptr) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) z += exp2_approx((x[i] - m) * kLog2e);
+      z = rcp_approx(lanes_sum<32>(z));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (lane + 32 * i < E) share[lane + 32 * i] += exp2_approx((x[i] - m) * kLog2e) * z;
+    }
+  }
   __syncwarp();
   uint32_t kept = a.n_groups > 1 ? known : 1u;
   int n = 0;
@@ -391,8 +390,7 @@ __device__ __noinline__ void route_exact(const GroupedArgs& a, int t, uint32_t k
       const float l = sc.x[e];
       double v = -CUDART_INF;
       if (l != -CUDART_INF_F) {
-        v = fabsf(softmax ? l - m : l) < 660.f ? score64(l, m, softmax, zz)
-                                               : score64_far(l, m, softmax, sc.x, E);
+        v = score64(l, m, softmax, zz);
         if (a.bias != nullptr) v += static_cast<double>(bias[e]);
       }
       sc.val[q] = order64(v);
@@ -661,6 +659,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   __shared__ int sh_list[kFwdWarps][3][kList];
   __shared__ __align__(16) float sh_bias[kCols];  // -inf past E
   __shared__ int sh_cnt[kCols];
+  __shared__ float sh_share[kFwdWarps][kCols];
   grid_dependency_wait();
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -671,6 +670,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
   const bool vec = kWhole || (E & 3) == 0;
   for (int i = tid; i < kCols; i += kFwdThreads) {
     sh_cnt[i] = 0;
+#pragma unroll
+    for (int w = 0; w < kFwdWarps; ++w) sh_share[w][i] = 0.f;
     sh_bias[i] = i >= E ? -CUDART_INF_F : a.bias != nullptr ? a.bias[i] : 0.f;
   }
   // slots that nothing fills still name an expert
@@ -693,7 +694,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     const ExactScratch sc{val, f, f + kMaxExperts, reinterpret_cast<uint8_t*>(f + 2 * kMaxExperts), sh_pick[warp][0]};
     for (int q = 0; q < n_list; ++q) {
       const auto& w = sh_list[warp];
-      route_exact(a, w[0][q], static_cast<uint32_t>(w[1][q]), __int_as_float(w[2][q]), sh_bias, sc, cnt);
+      route_exact(a, w[0][q], static_cast<uint32_t>(w[1][q]), __int_as_float(w[2][q]), sh_bias, sc, cnt,
+                  stats ? sh_share[warp] : nullptr);
     }
     n_list = 0;
   };
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     float c0, c1;
     f32x2_get(chk, c0, c1);
-    bool has_mask = __any_sync(kFull, !(c0 + c1 == 0.f));
+    const bool has_mask = __any_sync(kFull, !(c0 + c1 == 0.f));
     uint32_t mk = 0u;
     if (has_mask) {
       m = -kLowest;
@@ -756,16 +758,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     }
     m = lanes_max<P>(m);
     // scores: softmax not yet divided by their sum. Past E they are those of the
-    // lowest value: 0, unless the whole row is that low and they have to be left out.
-    if constexpr (!kWhole) {
-      if (__any_sync(kFull, m == -kLowest)) {
-        has_mask = true;
-#pragma unroll
-        for (int i = 0; i < kX; ++i)
-          if (4 * (sub + P * (i / 4)) + i % 4 >= E) mk |= 1u << i;
-      }
-    }
-    float f = 1.f;  // a score's factor
+    // lowest value: 0, unless the whole row is that low.
     if (softmax) {
       MOE_PIECES(i) {
 #pragma unroll
@@ -777,14 +770,6 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
         }
       }
     } else {
-      // P takes shares. f undoes the shift; its error is the same for the whole row,
-      // and that of the shifted logits within what `near` allows below.
-      if (stats && __any_sync(kFull, m < kLowRow)) {
-        if (m < kLowRow) f = exp2_approx((m - kLowRow) * kLog2e);
-#pragma unroll
-        for (int i = 0; i < kX; ++i)
-          if (m < kLowRow) x[i] = x[i] - m + kLowRow;
-      }
       MOE_PIECES(i) {
 #pragma unroll
         for (int q = 4 * i; q < 4 * i + 4; q += 2) {
@@ -814,17 +799,17 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
       const float z = lanes_sum<P>(c0 + c1);
       iz = z > 0.f ? rcp_approx(z) : 0.f;
     }
-    const bool low = m < -1e38f;  // nothing there, or nothing above the lowest values
-    const float smax = low ? 0.f : softmax ? iz : rcp_approx(1.f + exp2_approx(-m * kLog2e));
+    const bool tiny = tiny_row(m, softmax);
+    const float smax = tiny ? 0.f : softmax ? iz : rcp_approx(1.f + exp2_approx(-m * kLog2e));
     if (stats) {
-      const float f = valid ? iz : 0.f;
+      const float f = valid && !tiny ? iz : 0.f;
       MOE_PIECES(i) {
         psum[2 * i] = f32x2_fma(f32x2(x[4 * i], x[4 * i + 1]), f32x2(f, f), psum[2 * i]);
         psum[2 * i + 1] = f32x2_fma(f32x2(x[4 * i + 2], x[4 * i + 3]), f32x2(f, f), psum[2 * i + 1]);
       }
     }
     // selection values, -inf where masked or past E
-    if (softmax) f = iz;
+    const float f = softmax ? iz : 1.f;
     MOE_PIECES(i) {
       const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sh_bias + 4 * (sub + P * i));
       f32x2_get(f32x2_fma(f32x2(x[4 * i], x[4 * i + 1]), f32x2(f, f), b.x), x[4 * i], x[4 * i + 1]);
@@ -859,7 +844,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     auto near = [](float u, float v, float rel, float abs) {  // false where either is not finite
       return fabsf(u - v) < fmaf(rel, fmaxf(fabsf(u), fabsf(v)), abs);
     };
-    bool unsure = smax < 1e-30f;
+    bool unsure = tiny;
     uint32_t certain = 1u;  // the kept groups, or 0 where they are in doubt
     if (G > 1) {
       const float near_group = a.group_top == 2 ? fmaf(kU, smax, 2.f * near_one) : near_one;
@@ -995,9 +980,11 @@ __global__ void __launch_bounds__(kFwdThreads, 4)
     __syncthreads();
     for (int e = tid; e < E; e += kFwdThreads) {
       float p = 0.f;
-      for (int w = 0; w < kFwdWarps; ++w)
+      for (int w = 0; w < kFwdWarps; ++w) {
 #pragma unroll
         for (int q = 0; q < kTok; ++q) p += sh_row[w][q * kPitch + e];
+        p += sh_share[w][e];
+      }
       a.ppart[static_cast<size_t>(e) * gridDim.x + blockIdx.x] = p;
       a.tile_cnt[static_cast<size_t>(e) * gridDim.x + blockIdx.x] = sh_cnt[e];
     }
