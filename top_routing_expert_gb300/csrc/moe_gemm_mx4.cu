@@ -176,7 +176,8 @@ __device__ __forceinline__ Tile decode(int L, const int* prefix, const int* offs
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= tt) lo = mid; else hi = mid - 1;
   }
-  // the expert's rows go evenly over its tiles, in 16s: no tile is a remnant
+  // the expert's rows go evenly over its tiles, in 16s: the last is shorter by the
+  // roundings alone (8192 rows: 34 tiles of 240 and one of 32)
   const int rows = offs[lo + 1] - offs[lo], tiles = prefix[lo + 1] - prefix[lo];
   const int each = ((rows + tiles - 1) / tiles + 15) & ~15;
   Tile t;
