@@ -456,7 +456,8 @@ MOE_API moe_status moe_quantize_rows_mx4(int64_t rows, int64_t K, const moe_bf16
                                          const int32_t* n_rows, uint8_t* x_q, uint8_t* x_scale,
                                          void* stream);
 
-/* MX4 rows back to bf16 [rows,K]: the values the codes stand for, exactly. */
+/* MX4 rows back to bf16 [rows,K]: the values the codes stand for, exactly (those
+ * past bf16's largest, which take a scale byte of 253 or 254, as infinities). */
 MOE_API moe_status moe_dequantize_rows_mx4(int64_t rows, int64_t K, const uint8_t* x_q,
                                            const uint8_t* x_scale, moe_bf16* x, void* stream);
 

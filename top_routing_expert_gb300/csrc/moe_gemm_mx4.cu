@@ -24,14 +24,15 @@
 // there are too few columns for the pairs.
 //
 // Measured with a cold L2, and what bounds it: 65536 rows x 4096 x 14336 over 8
-// experts 1.20 ms, 6.4 PFLOP/s (1.07 and 7.2 in short runs): the power limit
-// (2.0 GHz at 1370 W) and the 51 bytes a clock that each SM takes in; 98304 x 1408
-// x 2048 over 64 experts 139 us: requests to L2, whose rows of codes are 704
-// bytes; 16 rows over 8 experts of 4096 x 14336 44 us, 5.0 TB/s of weights; 96
-// over 64 of 2048 x 1408 with GELU 23 us, 3.4 TB/s, and 8191 over 16 of 1024 x
-// 2816 with GELU 29 us: a start and an end of some 7 us around two to four rounds
-// of tiles. Replayed from a graph, with weights left in L2, these three take 35,
-// 16 and 26 us; the comparisons below are such replays.
+// experts 1.17 to 1.21 ms, 6.4 to 6.6 PFLOP/s, at 1.76 GHz under the power limit of
+// 1373 W (1.07 and 7.2 in short runs); the tensor pipe works in 77 % of the clocks,
+// the issuer waits for stages in 12 % and for accumulators in 5. 98304 x 1408 x 2048
+// over 64 experts 137 to 140 us: tensor 44 %, waits 11 and 4 %, and the ends of tiles
+// of 5.5 stages. 16 rows over 8 experts of 4096 x 14336 40 to 44 us, 5.0 to 5.5 TB/s of
+// weights; 96 over 64 of 2048 x 1408 with GELU 22 to 23 us, 3.4 TB/s, and 8191 over 16
+// of 1024 x 2816 with GELU 29 us: a start and an end of some 7 us around two to four
+// rounds of tiles. Replayed from a graph, with weights left in L2, these three took
+// 35, 16 and 26 us; the comparisons below are such replays.
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -371,8 +372,9 @@ __device__ __noinline__ void issue_tail(const Block& b, int steps, bool wide, ui
 // kPair: a tile is 512 output columns x up to tile_tokens tokens on a cluster
 // pair, as two sub-tiles A and B of 256 columns (128 per CTA) that share the
 // tokens of a stage, each with an accumulator of its own. Per CTA a stage then
-// brings 49 KB for 960 clocks of UMMAs, 51 bytes a clock of the 64 or so that
-// an SM takes in from L2 (one 256-column sub-tile alone: 34 KB for 480, 71).
+// brings 49 KB for 960 clocks of UMMAs, 51 bytes a clock at the full rate (40 at the
+// large product's) of the 64 or so that an SM takes in from L2 (one 256-column
+// sub-tile alone: 34 KB for 480, 71).
 // Each CTA loads half of the tokens' codes and all of their scales, and the
 // leader (rank 0) issues the UMMAs, so stage barriers of both CTAs' copies live
 // there.

@@ -636,11 +636,11 @@ struct TopList {
 
 // KD: at least k, of 2, 4 and 8. N: 16-byte pieces per lane (8, or 2 for few
 // logits, which also keeps that code short). kWhole: E = 4 N P, no piece missing.
-// 131072 tokens of 128 experts, top-2 with bias and statistics: 31 us, where the
-// bytes take 10. 16 warps to an SM (128 registers a thread) issue in 45 % of the
+// 131072 tokens of 128 experts, top-2 with bias and statistics: 31 to 32 us, where the
+// bytes take 10. 16 warps to an SM (128 registers a thread) issue in 44 % of the
 // clocks, half of it comparisons of the lists; waits are for the row and for
-// shuffles, and the last tokens decided again add 3 us. 16 experts to a lane give
-// 20 or 24 warps and 36 us; fetching the next row ahead changes nothing.
+// shuffles, and the last tokens decided again add 3 us. 16 experts to a lane gave
+// 20 or 24 warps and 36 us; fetching the next row ahead changed nothing.
 template <int P, int KD, int N, bool kWhole>
 __global__ void __launch_bounds__(kFwdThreads, 4)
     route_grouped_kernel(const __grid_constant__ GroupedArgs a) {
@@ -1047,10 +1047,10 @@ __global__ void __launch_bounds__(kStatsThreads) grouped_stats_kernel(GroupedSta
 // and the balance loss, aux = E sum_e f_e mean_t p_te with f taken as constant,
 // h_e = grad_aux E f_e / T, p = s / sum s:
 //   softmax  dl_e += p_e (h_e - sum p h);  sigmoid  dl_e += p_e (1 - s_e) (h_e - sum p h)
-// 65536 tokens of 256 experts, sigmoid with the balance loss: 26 us for 138 MB,
-// 5.3 TB/s; 16 warps to an SM issue in 55 % of the clocks, and waits are for
-// shuffles and arithmetic. With 8 experts to a lane, whose sums over lanes serve
-// half as much work, 29.5 us; with 32 (a quarter of the threads) 31.
+// 65536 tokens of 256 experts, sigmoid with the balance loss: 27 us for 138 MB,
+// 5.1 TB/s (26 in replays); 16 warps to an SM issue in 58 % of the clocks, and waits
+// are for shuffles and arithmetic. With 8 experts to a lane, whose sums over lanes
+// serve half as much work, it took 29.5 us; with 32 (a quarter of the threads) 31.
 template <int L>
 __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __grid_constant__ GroupedBwdArgs a) {
   constexpr int kTok = 32 / L;
