@@ -197,3 +197,25 @@ def test_slots_that_contribute_nothing(E, k, score):
             one, other = (_gradient(l, idx, g, score, renormalize, 1.5, ga, None if ga is None else routed)
                           for g in (zero, bad))
             assert np.isfinite(one).all() and np.array_equal(one, other)
+
+
+def test_weights_of_scores_below_fp32_beside_larger_ones():
+    """Renormalised sigmoid weights are ratios to a few roundings, also of a score that
+    fp32 does not hold to one that it does; and so is their gradient."""
+    T, E, k = 200, 16, 5
+    rng = np.random.default_rng(4)
+    l = (-95.0 + 4.0 * rng.standard_normal((T, E))).astype(np.float32)
+    l[:, 3] = np.resize([-12.0, -25.0, -33.0, -39.0, -41.0, -70.0], T)
+    idx, w, _, _, _ = _statistics(l, k, "sigmoid")
+    want, ww, s = O.route_grouped(l.astype(np.float64), None, k, "sigmoid")
+    assert (idx == want).all() and ww.min() > 0
+    # ratios below fp32's smallest value (a logit 87 below the largest) are 0
+    tol = (48 + 1.5 * 120) * U
+    assert (np.abs(w - ww) <= tol * ww + 2.0 ** -126).all()
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    mine = _gradient(l, want, gw, "sigmoid", True)
+    q = ww[:, :, None] * (gw[:, :, None] - (ww * gw).sum(axis=1)[:, None, None])
+    mag = ww * (np.abs(gw) + (ww * np.abs(gw)).sum(axis=1, keepdims=True))
+    rest = 1.0 / (1.0 + np.exp(np.take_along_axis(l.astype(np.float64), want, axis=1)))
+    got = np.take_along_axis(mine, want, axis=1)
+    assert (np.abs(got - q[:, :, 0] * rest) <= 3 * tol * mag + 2.0 ** -126).all()

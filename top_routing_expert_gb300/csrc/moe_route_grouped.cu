@@ -118,15 +118,16 @@ __device__ __forceinline__ void write_slots(const GroupedArgs& a, int64_t t, con
   }
   float f = a.scale;
   if (a.renormalize) {
-    // Weights are ratios then: softmax scores are taken relative to the largest
-    // chosen logit, and so are sigmoid scores far below zero (where 1 + exp(l)
-    // is 1), which would underflow.
+    // Weights are ratios then, and scores, which could underflow, are taken relative
+    // to the largest chosen logit: softmax scores, and sigmoid scores where that is
+    // below zero, as exp(l - top) / (1 + exp(l)).
     top = lanes_reduce<kLanes>(top, [](float u, float v) { return fmaxf(u, v); });
-    const bool ratio = softmax || top < -40.f;
+    const bool ratio = softmax || top < 0.f;
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      const float y = ratio ? exp2_approx((x[q] - top) * kLog2e) : rcp_approx(1.f + exp2_approx(-x[q] * kLog2e));
+      float y = exp2_approx((ratio ? x[q] - top : -x[q]) * kLog2e);
+      if (!softmax) y = (ratio ? y : 1.f) * rcp_approx(1.f + (ratio ? exp2_approx(x[q] * kLog2e) : y));
       w[q] = x[q] == -CUDART_INF_F ? 0.f : y;
       sum += w[q];
     }
@@ -1161,16 +1162,16 @@ __global__ void __launch_bounds__(kThreads, 4) route_grouped_bwd_kernel(const __
         if (ej[q] >= 0) top = fmaxf(top, x[q]);
       top = lanes_reduce<kLanes>(top, [](float u, float v) { return fmaxf(u, v); });
     }
-    const bool ratio = a.renormalize && (softmax || top < -40.f);
+    const bool ratio = a.renormalize && (softmax || top < 0.f);
     const float shift = ratio ? top : m;
     float sj[kPer], dj[kPer];
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      const float y = exp2_approx((ratio || softmax ? x[q] - shift : -x[q]) * kLog2e);
-      sj[q] = ej[q] < 0 ? 0.f : ratio ? y : softmax ? y * iz : rcp_approx(1.f + y);
-      sum += sj[q];
       dj[q] = softmax ? 1.f : rcp_approx(1.f + exp2_approx(x[q] * kLog2e));  // 1 - s
+      const float y = exp2_approx((ratio || softmax ? x[q] - shift : -x[q]) * kLog2e);
+      sj[q] = ej[q] < 0 ? 0.f : ratio ? y * dj[q] : softmax ? y * iz : rcp_approx(1.f + y);
+      sum += sj[q];
     }
     if (a.renormalize) {
       sum = lanes_sum<kLanes>(sum);
