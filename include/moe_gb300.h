@@ -476,6 +476,100 @@ MOE_API moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64
                                        const uint8_t* w_scale, int gelu, moe_bf16* D,
                                        uint32_t* dev_status, void* stream);
 
+/* --------------------------------------- training the experts' products ----
+ * The grouped product alone, and its gradients. Rows x [rows,K] lie in
+ * segments, expert e's being offsets[e] <= r < offsets[e+1] (offsets [E+1],
+ * as moe_permute writes them; segments may be empty, rows in none of them are
+ * neither read into a result nor written). bf16 operands, fp32 accumulation,
+ * one rounding. 1 <= E <= 256; 0 <= rows < 2^31; K and N multiples of 64,
+ * <= 65536. dev_status is required (MOE_DEV_TIMEOUT). The forward and the
+ * gradient of a layer's experts, u = x W1, a = gelu(u), y = a W2:
+ *   a, u  = moe_expert_gemm(x, W1, GELU)       y  = moe_expert_gemm(a, W2)
+ *   du    = moe_expert_gemm(dy, W2, transposed, GELU_GRAD of u)
+ *   dx    = moe_expert_gemm(du, W1, transposed)
+ *   dW2   = moe_expert_wgrad(a, dy)            dW1 = moe_expert_wgrad(x, du) */
+
+typedef enum {
+  MOE_EPILOGUE_NONE = 0,      /* D = bf16(acc) */
+  MOE_EPILOGUE_GELU = 1,      /* D = bf16(gelu_tanh(acc)); pre = bf16(acc) if given */
+  MOE_EPILOGUE_GELU_GRAD = 2  /* D = bf16(acc * gelu_tanh'(pre)) */
+} moe_epilogue;
+
+typedef enum { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype;
+
+/* D [rows,N] bf16: D[r] = x[r] . W[e] with W [E,K,N], or (transposed 1) x[r] .
+ * W[e]^T with W [E,N,K]. pre [rows,N]: written or read as the epilogue says,
+ * NULL with MOE_EPILOGUE_NONE. D may not overlap x or pre. */
+MOE_API moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N,
+                                   const moe_bf16* x, const int32_t* offsets, const moe_bf16* W,
+                                   int transposed, int epilogue, moe_bf16* pre, moe_bf16* D,
+                                   uint32_t* dev_status, void* stream);
+
+/* dW [E,K,N] = sum over each expert's rows of x[r]^T g[r], x [rows,K] and
+ * g [rows,N]; 0 for an expert without rows. dtype is dW's (moe_dtype).
+ * accumulate 1 (fp32 only): added to what dW holds. The same inputs give the
+ * same bits. */
+MOE_API moe_status moe_expert_wgrad(int64_t E, int64_t rows, int64_t K, int64_t N,
+                                    const moe_bf16* x, const moe_bf16* g, const int32_t* offsets,
+                                    void* dW, int dtype, int accumulate, uint32_t* dev_status,
+                                    void* stream);
+
+/* ------------------------------------------------- between two blocks ----
+ * The end of one block of a model and the norm that the next one begins with,
+ * in one pass over each token:
+ *   c   = sum_j w_j y_j, the token's rows of the block's output;
+ *   n   = c / sqrt(mean(c^2) + eps) * post_weight   (post_norm 1), or c * post_weight;
+ *   out = residual_scale * residual + gate * n;
+ *   xn  = out / sqrt(mean(out^2) + eps) * pre_weight, of out before its rounding.
+ * Sums are fp32, each output is rounded once. */
+typedef struct {
+  int64_t T;             /* tokens */
+  int64_t H;             /* width: a multiple of 64, <= 16384 */
+  int64_t rows;          /* rows that y holds */
+  int64_t top_k;         /* slots per token, 1 to 8 */
+  int32_t post_norm;     /* 0 or 1 */
+  float residual_scale;  /* finite */
+  float eps;             /* finite, > 0 */
+} moe_block;
+
+/* in : residual [T,H] bf16; y [rows,H] bf16, or NULL: no block output, out =
+ *      residual_scale * residual (the first block's norm); dest_row [T,k]
+ *      int32 (a row outside [0,rows) is no row: dropped slots have -1), or
+ *      NULL: token t's one row is t (top_k 1, rows >= T); topk_w [T,k] fp32 or
+ *      NULL (1); post_weight, pre_weight [H] fp32 or NULL (1); gate [T] fp32
+ *      or NULL (1).
+ * out: out, xn [T,H] bf16, either of them NULL (not wanted). out may be the
+ *      residual itself; nothing else may overlap. */
+MOE_API moe_status moe_block_norm(const moe_block* b, const moe_bf16* residual, const moe_bf16* y,
+                                  const int32_t* dest_row, const float* topk_w,
+                                  const float* post_weight, const float* gate,
+                                  const float* pre_weight, moe_bf16* out, moe_bf16* xn,
+                                  void* stream);
+
+/* Bytes of workspace for moe_block_norm_bwd. Host only. */
+MOE_API moe_status moe_block_norm_workspace_size(int64_t T, int64_t H, size_t* bytes);
+
+/* Gradient of moe_block_norm with respect to everything that enters it.
+ *   in : h [T,H] bf16, the stream the forward wrote as out, at which the second
+ *        norm's gradient is taken (needed with grad_xn); y, dest_row, topk_w,
+ *        the weights and gate as the forward had them; grad_out, grad_xn [T,H]
+ *        bf16 (NULL: no such gradient; not both NULL).
+ *   out: grad_residual [T,H] bf16; grad_y [rows,H] bf16, the rows that dest_row
+ *        names (others are left as they were); grad_topk_w [T,k] fp32 (0 at
+ *        dropped slots); grad_post, grad_pre [H] fp32; grad_gate [T] fp32.
+ *        Each may be NULL. dest_row names a row once at most.
+ * ws, needed for grad_post and grad_pre alone: moe_block_norm_workspace_size.
+ * grad_residual may be grad_out itself; nothing else may overlap. The same
+ * inputs give the same bits. */
+MOE_API moe_status moe_block_norm_bwd(const moe_block* b, const moe_bf16* h, const moe_bf16* y,
+                                      const int32_t* dest_row, const float* topk_w,
+                                      const float* post_weight, const float* gate,
+                                      const float* pre_weight, const moe_bf16* grad_out,
+                                      const moe_bf16* grad_xn, moe_bf16* grad_residual,
+                                      moe_bf16* grad_y, float* grad_topk_w, float* grad_post,
+                                      float* grad_gate, float* grad_pre, void* ws,
+                                      size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------- expert parallelism ----
  * Experts spread over `world` ranks, rank g holding the E/world consecutive
  * experts g*E/world .. (g+1)*E/world - 1, and each token's rows sent to the

@@ -634,3 +634,103 @@ def pack_mx4_weight_scale(byte: np.ndarray) -> np.ndarray:
         for b in range(n):
             out[c // 128, b // 4, c % 32, c % 128 // 32, b % 4] = byte[c, b]
     return out
+
+
+# -------------------------------------- training the experts' products ----
+
+def gelu_tanh_slope(u: np.ndarray) -> np.ndarray:
+    """Derivative of gelu_tanh."""
+    u = np.asarray(u, np.float64)
+    c = np.sqrt(2.0 / np.pi)
+    t = np.tanh(c * (u + 0.044715 * u ** 3))
+    return 0.5 * (1.0 + t) + 0.5 * u * (1.0 - t * t) * c * (1.0 + 3 * 0.044715 * u * u)
+
+
+def expert_weight_grad(x, g, offsets) -> np.ndarray:
+    """dW [E, K, N]: each segment's rows of x transposed times those of g."""
+    x, g = np.asarray(x, np.float64), np.asarray(g, np.float64)
+    E = len(offsets) - 1
+    dW = np.zeros((E, x.shape[1], g.shape[1]))
+    for e in range(E):
+        for r in range(offsets[e], offsets[e + 1]):
+            dW[e] += np.outer(x[r], g[r])
+    return dW
+
+
+# ------------------------------------------------- between two blocks ----
+
+def _token_rows(y, dest, T, k):
+    """The rows of y that belong to each token [T, k, H], zeros where there is none."""
+    if dest is None:
+        return y[:T, None, :], np.ones((T, 1), bool)
+    kept = (dest >= 0) & (dest < len(y))
+    return np.where(kept[:, :, None], y[np.where(kept, dest, 0)], 0.0), kept
+
+
+def block_norm(residual, y, dest, w, post, gate, pre, post_norm, scale, eps):
+    """-> (out, xn) [T, H], before any rounding."""
+    residual = np.asarray(residual, np.float64)
+    T, H = residual.shape
+    out = scale * residual
+    if y is not None:
+        rows, kept = _token_rows(np.asarray(y, np.float64), dest, T, 1 if dest is None else dest.shape[1])
+        ww = np.where(kept, 1.0 if w is None else w, 0.0)
+        n = np.einsum("tk,tkh->th", ww, rows)
+        if post_norm:
+            n = n / np.sqrt((n * n).mean(1, keepdims=True) + eps)
+        if post is not None:
+            n = n * post
+        out = out + (n if gate is None else gate[:, None] * n)
+    xn = out / np.sqrt((out * out).mean(1, keepdims=True) + eps)
+    return out, xn if pre is None else xn * pre
+
+
+def block_norm_grad(h, y, dest, w, post, gate, pre, post_norm, scale, eps, g_out, g_xn):
+    """Gradients of block_norm, the second norm's taken at h, as a dict."""
+    return _block_grad(h, y, dest, w, post, gate, pre, post_norm, scale, eps, g_out, g_xn, False)
+
+
+def block_norm_grad_magnitude(h, y, dest, w, post, gate, pre, post_norm, scale, eps, g_out, g_xn):
+    """The same sums over magnitudes, where no term cancels another (what an error
+    bound of the sums goes by); the reciprocal norms are those of the values."""
+    return _block_grad(h, y, dest, w, post, gate, pre, post_norm, scale, eps, g_out, g_xn, True)
+
+
+def _block_grad(h, y, dest, w, post, gate, pre, post_norm, scale, eps, g_out, g_xn, magnitude):
+    f64 = lambda v: None if v is None else np.asarray(v, np.float64)
+    mag = (lambda v: None if v is None else np.abs(v)) if magnitude else (lambda v: v)
+    sign = 1.0 if magnitude else -1.0
+    root = lambda v: 1.0 / np.sqrt((v * v).mean(1, keepdims=True) + eps)
+    h = mag(f64(h))
+    T, H = h.shape
+    res = {}
+    G = np.zeros((T, H)) if g_out is None else mag(f64(g_out))
+    if g_xn is not None:
+        gx = mag(f64(g_xn))
+        r = root(h)
+        v = gx if pre is None else gx * mag(f64(pre))
+        G = G + r * (v + sign * h * r * r * (v * h).mean(1, keepdims=True))
+        res["g_pre"] = (gx * h * r).sum(0)
+    res["g_residual"] = mag(np.float64(scale)) * G
+    if y is None:
+        return res
+    rows, kept = _token_rows(f64(y), dest, T, 1 if dest is None else dest.shape[1])
+    ww = np.where(kept, 1.0 if w is None else f64(w), 0.0)
+    c = np.einsum("tk,tkh->th", ww, rows)
+    rc = root(c) if post_norm else np.ones((T, 1))
+    ww, rows = mag(ww), mag(rows)
+    c = np.einsum("tk,tkh->th", ww, rows)
+    post = 1.0 if post is None else mag(f64(post))
+    gt = 1.0 if gate is None else mag(f64(gate))[:, None]
+    n = c * rc
+    res["g_gate"], res["g_post"] = (G * post * n).sum(1), (gt * G * n).sum(0)
+    u = gt * G * post
+    gc = rc * (u + sign * n * (u * n).mean(1, keepdims=True)) if post_norm else u
+    res["g_w"] = np.where(kept, (gc[:, None, :] * rows).sum(2), 0.0)
+    res["g_y"] = np.full(y.shape, np.nan)   # rows that no slot names have no gradient
+    if dest is None:
+        res["g_y"][:T] = gc
+    else:
+        t, j = np.nonzero(kept)
+        res["g_y"][dest[t, j]] = ww[t, j][:, None] * gc[t]
+    return res

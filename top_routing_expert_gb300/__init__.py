@@ -28,6 +28,8 @@ __all__ = [
     "moe_ep_permute", "moe_ep_regroup", "DevicePipeline", "moe_layer_fwd_pipelined",
     "RouteConfig", "moe_route_grouped", "moe_route_grouped_bwd", "moe_quantize_rows_mx4",
     "moe_dequantize_rows_mx4", "moe_quantize_weights_mx4", "moe_expert_gemm_mx4", "Mx4Weights",
+    "moe_expert_gemm", "moe_expert_wgrad", "BlockConfig", "BlockWorkspace",
+    "block_workspace_size", "moe_block_norm", "moe_block_norm_bwd",
     "Workspace", "DEV_BAD_INDEX", "DEV_DUP_INDEX",
     "DEV_NONFINITE", "DEV_TIMEOUT", "LAYER_NUM_EVENTS", "EXPORTED_SYMBOLS", "build",
 ]
@@ -44,7 +46,9 @@ EXPORTED_SYMBOLS = ["moe_abi_version", "moe_capacity", "moe_workspace_size", "mo
                     "moe_layer_fwd_host_fp8", "moe_ep_permute", "moe_ep_regroup",
                     "moe_pipelined_workspace_size", "moe_layer_fwd_pipelined",
                     "moe_route_grouped", "moe_route_grouped_bwd", "moe_quantize_rows_mx4",
-                    "moe_dequantize_rows_mx4", "moe_quantize_weights_mx4", "moe_expert_gemm_mx4"]
+                    "moe_dequantize_rows_mx4", "moe_quantize_weights_mx4", "moe_expert_gemm_mx4",
+                    "moe_expert_gemm", "moe_expert_wgrad", "moe_block_norm",
+                    "moe_block_norm_workspace_size", "moe_block_norm_bwd"]
 
 
 class MoeError(RuntimeError):
@@ -80,6 +84,25 @@ class RouteConfig(ctypes.Structure):
             raise ValueError(f'score must be "softmax" or "sigmoid", got {score!r}')
         return cls(int(score == "sigmoid"), int(n_groups), int(topk_groups), int(group_top),
                    int(bool(renormalize)), float(scale))
+
+
+class _Block(ctypes.Structure):
+    """moe_block in the header."""
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("top_k", ctypes.c_int64), ("post_norm", ctypes.c_int32),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class BlockConfig:
+    """How moe_block_norm ends a block: whether the block's output is normalised
+    (post_norm), the factor of the residual, and eps of both norms."""
+    __slots__ = ("post_norm", "residual_scale", "eps")
+
+    @classmethod
+    def make(cls, post_norm=True, residual_scale=1.0, eps=1e-6) -> "BlockConfig":
+        c = cls()
+        c.post_norm, c.residual_scale, c.eps = int(bool(post_norm)), float(residual_scale), float(eps)
+        return c
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -166,6 +189,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_quantize_weights_mx4.argtypes = [I64, I64, I64] + [_P] * 4
     lib.moe_expert_gemm_mx4.restype = ctypes.c_int
     lib.moe_expert_gemm_mx4.argtypes = [I64] * 4 + [_P] * 5 + [ctypes.c_int] + [_P] * 3
+    lib.moe_expert_gemm.restype = ctypes.c_int
+    lib.moe_expert_gemm.argtypes = [I64] * 4 + [_P] * 3 + [ctypes.c_int] * 2 + [_P] * 4
+    lib.moe_expert_wgrad.restype = ctypes.c_int
+    lib.moe_expert_wgrad.argtypes = [I64] * 4 + [_P] * 4 + [ctypes.c_int] * 2 + [_P] * 2
+    B = ctypes.POINTER(_Block)
+    lib.moe_block_norm.restype = ctypes.c_int
+    lib.moe_block_norm.argtypes = [B] + [_P] * 10
+    lib.moe_block_norm_workspace_size.restype = ctypes.c_int
+    lib.moe_block_norm_workspace_size.argtypes = [I64, I64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.moe_block_norm_bwd.restype = ctypes.c_int
+    lib.moe_block_norm_bwd.argtypes = [B] + [_P] * 16 + [ctypes.c_size_t, _P]
     _lib = lib
     return lib
 
@@ -813,6 +847,150 @@ def moe_expert_gemm_mx4(x_q, x_scale, offsets, Wq, w_scale, out, gelu=False, dev
         _address(w_scale, torch.uint8, "w_scale", dev), 1 if gelu else 0,
         _address(out, torch.bfloat16, "out", dev), _ptr(dev_status, torch.int32, "dev_status", 1),
         _stream(stream)))
+
+
+# ------------------------------------ training the experts' products ----
+
+_EPILOGUES = {None: 0, "gelu": 1, "gelu_grad": 2}
+
+
+def moe_expert_gemm(x, offsets, W, out, transposed=False, epilogue=None, pre=None, dev_status=None,
+                    stream=None):
+    """out [rows, N] bf16 = each row of x [rows, K] times its expert's weights W
+    [E, K, N], or (transposed) the transpose of W [E, N, K]; segments offsets
+    [E+1]. epilogue: None; "gelu" (the value before it kept in pre [rows, N], if
+    given); "gelu_grad" (the product times GELU's slope at pre). dev_status
+    (int32, one element) is required."""
+    if epilogue not in _EPILOGUES:
+        raise ValueError(f'epilogue must be None, "gelu" or "gelu_grad", got {epilogue!r}')
+    if x.dim() != 2 or W.dim() != 3:
+        raise ValueError("x must be [rows, K] and W [E, K, N] or, transposed, [E, N, K]")
+    rows, K = x.shape
+    E, Kw, N = (W.shape[0], W.shape[2], W.shape[1]) if transposed else W.shape
+    if K != Kw:
+        raise ValueError(f"x has K = {K}, W has K = {Kw}")
+    for t, name in ((out, "out"), (pre, "pre")):
+        if t is not None and t.shape != (rows, N):
+            raise ValueError(f"{name} must be [rows, N] = [{rows}, {N}], got {list(t.shape)}")
+    dev = _device_of(x, "x")
+    bf16 = torch.bfloat16
+    _check("moe_expert_gemm", load_library().moe_expert_gemm(
+        E, rows, K, N, _address(x, bf16, "x", dev), _ptr(offsets, torch.int32, "offsets", E + 1),
+        _address(W, bf16, "W", dev), 1 if transposed else 0, _EPILOGUES[epilogue],
+        None if pre is None else _address(pre, bf16, "pre", dev), _address(out, bf16, "out", dev),
+        _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+def moe_expert_wgrad(x, grad, offsets, dW, accumulate=False, dev_status=None, stream=None):
+    """dW [E, K, N] (fp32 or bf16) = each expert's x [rows, K] transposed times
+    its grad [rows, N] (bf16, segments offsets [E+1]); added to dW (fp32) if
+    accumulate. dev_status (int32, one element) is required."""
+    if x.dim() != 2 or grad.dim() != 2 or dW.dim() != 3:
+        raise ValueError("x must be [rows, K], grad [rows, N] and dW [E, K, N]")
+    rows, K = x.shape
+    E, Kw, N = dW.shape
+    if K != Kw or grad.shape != (rows, N):
+        raise ValueError(f"dW is {list(dW.shape)}: x must be [rows, {Kw}] and grad [rows, {N}], got "
+                         f"{list(x.shape)} and {list(grad.shape)}")
+    if dW.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dW must be torch.float32 or torch.bfloat16, got {dW.dtype}")
+    dev = _device_of(x, "x")
+    _check("moe_expert_wgrad", load_library().moe_expert_wgrad(
+        E, rows, K, N, _address(x, torch.bfloat16, "x", dev),
+        _address(grad, torch.bfloat16, "grad", dev), _ptr(offsets, torch.int32, "offsets", E + 1),
+        _address(dW, dW.dtype, "dW", dev), 1 if dW.dtype == torch.bfloat16 else 0,
+        1 if accumulate else 0, _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+
+
+# ------------------------------------------------- between two blocks ----
+
+def block_workspace_size(T: int, H: int) -> int:
+    """Bytes of workspace moe_block_norm_bwd needs for T tokens of width H."""
+    out = ctypes.c_size_t()
+    _check("moe_block_norm_workspace_size", load_library().moe_block_norm_workspace_size(
+        int(T), int(H), ctypes.byref(out)))
+    return out.value
+
+
+class BlockWorkspace:
+    """Device scratch of moe_block_norm_bwd for up to T tokens of width H."""
+
+    def __init__(self, T: int, H: int, device="cuda"):
+        self.nbytes = block_workspace_size(T, H)
+        self.buf = torch.empty(max(self.nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def _block(cfg: BlockConfig, stream_t, name, y, dest_row, topk_w, post_weight, gate, pre_weight):
+    """The moe_block of a call and the addresses of the arguments that both
+    directions share; stream_t [T, H] gives the sizes."""
+    if stream_t.dim() != 2:
+        raise ValueError(f"{name} must be [T, H]")
+    T, H = stream_t.shape
+    rows, k = 0, 1
+    if y is not None:
+        if y.dim() != 2 or y.shape[1] != H:
+            raise ValueError(f"y must be [rows, {H}], got {list(y.shape)}")
+        rows = y.shape[0]
+    if dest_row is not None:
+        if dest_row.dim() != 2 or dest_row.shape[0] != T:
+            raise ValueError(f"dest_row must be [{T}, k], got {list(dest_row.shape)}")
+        k = dest_row.shape[1]
+    if topk_w is not None and topk_w.shape != (T, k):
+        raise ValueError(f"topk_w must be [T, k] = [{T}, {k}], got {list(topk_w.shape)}")
+    f32 = torch.float32
+    for t, n, want in ((post_weight, "post_weight", (H,)), (pre_weight, "pre_weight", (H,)),
+                       (gate, "gate", (T,))):
+        if t is not None and t.shape != want:
+            raise ValueError(f"{n} must be {list(want)}, got {list(t.shape)}")
+    b = _Block(T, H, rows, k, cfg.post_norm, cfg.residual_scale, cfg.eps)
+    return b, (_ptr(y, torch.bfloat16, "y"), _ptr(dest_row, torch.int32, "dest_row"),
+               _ptr(topk_w, f32, "topk_w"), _ptr(post_weight, f32, "post_weight"),
+               _ptr(gate, f32, "gate"), _ptr(pre_weight, f32, "pre_weight"))
+
+
+def _same_shape(t, like, name):
+    if t is not None and t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+
+
+def moe_block_norm(cfg: BlockConfig, residual, y, out, xn=None, dest_row=None, topk_w=None,
+                   post_weight=None, gate=None, pre_weight=None, stream=None):
+    """out [T, H] = residual_scale * residual + gate * norm(sum_j topk_w_j
+    y[dest_row_j]) * post_weight, xn [T, H] = norm(out) * pre_weight (bf16; see
+    moe_block_norm in the header for what may be None)."""
+    b, shared = _block(cfg, residual, "residual", y, dest_row, topk_w, post_weight, gate, pre_weight)
+    bf16 = torch.bfloat16
+    _same_shape(out, residual, "out")
+    _same_shape(xn, residual, "xn")
+    _check("moe_block_norm", load_library().moe_block_norm(
+        ctypes.byref(b), _ptr(residual, bf16, "residual"), *shared, _ptr(out, bf16, "out"),
+        _ptr(xn, bf16, "xn"), _stream(stream)))
+
+
+def moe_block_norm_bwd(cfg: BlockConfig, h, y, grad_out, grad_residual, grad_y, grad_xn=None,
+                       dest_row=None, topk_w=None, post_weight=None, gate=None, pre_weight=None,
+                       grad_topk_w=None, grad_post=None, grad_gate=None, grad_pre=None,
+                       ws: Optional[BlockWorkspace] = None, stream=None):
+    """Gradient of moe_block_norm from grad_out and grad_xn [T, H] (bf16, either
+    may be None), h [T, H] being what the forward wrote as out. Gradients that
+    are None are not formed; ws is needed for grad_post and grad_pre."""
+    b, shared = _block(cfg, h, "h", y, dest_row, topk_w, post_weight, gate, pre_weight)
+    bf16, f32 = torch.bfloat16, torch.float32
+    for t, n in ((grad_out, "grad_out"), (grad_xn, "grad_xn"), (grad_residual, "grad_residual")):
+        _same_shape(t, h, n)
+    if grad_y is not None and (y is None or grad_y.shape != y.shape):
+        raise ValueError("grad_y must have the shape of y")
+    for t, n, want in ((grad_topk_w, "grad_topk_w", (b.T, b.top_k)), (grad_post, "grad_post", (b.H,)),
+                       (grad_pre, "grad_pre", (b.H,)), (grad_gate, "grad_gate", (b.T,))):
+        if t is not None and t.shape != want:
+            raise ValueError(f"{n} must be {list(want)}, got {list(t.shape)}")
+    wp, wn = (None, 0) if ws is None else (_ptr(ws.buf, torch.uint8, "ws"), ws.nbytes)
+    _check("moe_block_norm_bwd", load_library().moe_block_norm_bwd(
+        ctypes.byref(b), _ptr(h, bf16, "h"), *shared, _ptr(grad_out, bf16, "grad_out"),
+        _ptr(grad_xn, bf16, "grad_xn"), _ptr(grad_residual, bf16, "grad_residual"),
+        _ptr(grad_y, bf16, "grad_y"), _ptr(grad_topk_w, f32, "grad_topk_w"),
+        _ptr(grad_post, f32, "grad_post"), _ptr(grad_gate, f32, "grad_gate"),
+        _ptr(grad_pre, f32, "grad_pre"), wp, wn, _stream(stream)))
 
 
 # ------------------------------------------------- expert parallelism ----

@@ -278,6 +278,21 @@ bool tmap_bf16_experts(CUtensorMap* m, const void* ptr, uint64_t N, uint64_t K, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// dW [E][K][N] in boxes of 32 rows x 128 bytes of one expert, for stores: rows
+// and columns past an expert's matrix are left out by the copy.
+bool tmap_wgrad_out(CUtensorMap* m, void* ptr, uint64_t N, uint64_t K, uint64_t E, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const uint64_t size = bf16 ? 2 : 4;
+  const cuuint64_t gdim[3] = {N, K, E};
+  const cuuint64_t gstride[2] = {N * size, N * K * size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), 32, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr,
+            gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A byte (e4m3, or two 4-bit codes) row-major matrix [outer, inner] in boxes
 // of 128 bytes x box_outer rows (one 128-byte swizzle row of K per box row);
 // inner must be a multiple of 16.
@@ -1535,6 +1550,225 @@ moe_status moe_expert_gemm_mx4(int64_t E, int64_t rows, int64_t K, int64_t N, co
   if (!tmap_bf16_2d(&tm_d, D, N, rows, 32, 16, CU_TENSOR_MAP_SWIZZLE_64B)) return MOE_ERR_CUDA;
   MOE_CUDA(launch_expert_gemm_mx4(tm_w, tm_x, tm_ws, tm_d, a, pair, num_sms(),
                                   static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+// --------------------------------------- training the experts' products ----
+
+namespace {
+
+moe_status check_expert_product(int64_t E, int64_t rows, int64_t K, int64_t N) {
+  if (E <= 0 || rows < 0 || K <= 0 || N <= 0) return MOE_ERR_SHAPE;
+  if (E > kMaxExperts || rows >= (int64_t(1) << 31) || K % 64 != 0 || N % 64 != 0 || K > kMaxDim ||
+      N > kMaxDim)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N, const moe_bf16* x,
+                           const int32_t* offsets, const moe_bf16* W, int transposed, int epilogue,
+                           moe_bf16* pre, moe_bf16* D, uint32_t* dev_status, void* stream) {
+  MOE_TRY(check_expert_product(E, rows, K, N));
+  if (transposed != 0 && transposed != 1) return MOE_ERR_SHAPE;
+  if (epilogue != MOE_EPILOGUE_NONE && epilogue != MOE_EPILOGUE_GELU &&
+      epilogue != MOE_EPILOGUE_GELU_GRAD)
+    return MOE_ERR_SHAPE;
+  if (epilogue == MOE_EPILOGUE_NONE && pre != nullptr) return MOE_ERR_SHAPE;
+  // W [E][N][K] is read as one matrix of E * N rows
+  if (transposed && E * N >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(x);
+  MOE_REQUIRE(offsets);
+  MOE_REQUIRE(W);
+  MOE_REQUIRE(D);
+  if (epilogue == MOE_EPILOGUE_GELU_GRAD) MOE_REQUIRE(pre);
+  MOE_OPTIONAL(pre);
+  MOE_REQUIRE(dev_status);
+  CUtensorMap tm_a, tm_b;
+  if (!tmap_bf16_kblocks(&tm_a, x, K, rows, 128, 2)) return MOE_ERR_CUDA;
+  if (transposed ? !tmap_bf16_kblocks(&tm_b, W, K, static_cast<uint64_t>(E) * N, 128, 2)
+                 : !tmap_bf16_experts(&tm_b, W, N, K, E, 2 * kBlockK))
+    return MOE_ERR_CUDA;
+  GemmArgs g = {};
+  g.offsets = offsets;
+  g.E = static_cast<int>(E);
+  g.K = static_cast<int>(K);
+  g.N = static_cast<int>(N);
+  g.rows = static_cast<int>(rows);
+  g.D = D;
+  g.gelu = epilogue == MOE_EPILOGUE_GELU ? kEpiGelu
+           : epilogue == MOE_EPILOGUE_GELU_GRAD ? kEpiGeluGrad : kEpiNone;
+  g.U = pre;
+  g.dev_status = dev_status;
+  g.timeout_ns = wait_timeout_ns();
+  MOE_CUDA(launch_expert_gemm(tm_a, tm_b, g, transposed != 0, num_sms(),
+                              static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_expert_wgrad(int64_t E, int64_t rows, int64_t K, int64_t N, const moe_bf16* x,
+                            const moe_bf16* g, const int32_t* offsets, void* dW, int dtype,
+                            int accumulate, uint32_t* dev_status, void* stream) {
+  MOE_TRY(check_expert_product(E, rows, K, N));
+  if (dtype != MOE_DTYPE_FP32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_SHAPE;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_SHAPE;
+  if (accumulate && dtype != MOE_DTYPE_FP32) return MOE_ERR_UNSUPPORTED;
+  MOE_REQUIRE(dW);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (!accumulate)
+      MOE_CUDA(cudaMemsetAsync(dW, 0, static_cast<size_t>(E) * K * N * (dtype == MOE_DTYPE_BF16 ? 2 : 4), st));
+    return MOE_OK;
+  }
+  MOE_REQUIRE(x);
+  MOE_REQUIRE(g);
+  MOE_REQUIRE(offsets);
+  MOE_REQUIRE(dev_status);
+  CUtensorMap tm_x, tm_g, tm_d;
+  if (!tmap_bf16_kblocks(&tm_x, x, K, rows, 128, 2)) return MOE_ERR_CUDA;
+  if (!tmap_bf16_kblocks(&tm_g, g, N, rows, 128, 2)) return MOE_ERR_CUDA;
+  if (!tmap_wgrad_out(&tm_d, dW, N, K, E, dtype == MOE_DTYPE_BF16)) return MOE_ERR_CUDA;
+  WgradArgs a;
+  a.offsets = offsets;
+  a.E = static_cast<int>(E);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.rows = static_cast<int>(rows);
+  a.bf16_out = dtype == MOE_DTYPE_BF16;
+  a.accumulate = accumulate;
+  a.dev_status = dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  MOE_CUDA(launch_wgrad(tm_x, tm_g, tm_d, a, num_sms(), st));
+  return MOE_OK;
+}
+
+// ------------------------------------------------------ between two blocks ----
+
+namespace {
+
+moe_status check_block(const moe_block* b) {
+  if (b == nullptr) return MOE_ERR_NULL;
+  if (b->T < 0 || b->H <= 0 || b->rows < 0 || b->top_k <= 0) return MOE_ERR_SHAPE;
+  if (b->post_norm != 0 && b->post_norm != 1) return MOE_ERR_SHAPE;
+  if (!isfinite(b->residual_scale) || !isfinite(b->eps) || !(b->eps > 0.f)) return MOE_ERR_SHAPE;
+  if (b->H % 64 != 0 || b->H > kBlockMaxWidth || b->top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+  if (b->T > (int64_t(1) << 31) || b->T * b->top_k >= (int64_t(1) << 31) ||
+      b->rows >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The part of the arguments that both directions share. Without dest_row a
+// token's one row is its own.
+moe_status block_args(const moe_block* b, const moe_bf16* y, const int32_t* dest_row,
+                      const float* topk_w, const float* post_weight, const float* gate,
+                      const float* pre_weight, BlockArgs* a) {
+  MOE_OPTIONAL(y);
+  MOE_OPTIONAL(dest_row);
+  MOE_OPTIONAL(topk_w);
+  MOE_OPTIONAL(post_weight);
+  MOE_OPTIONAL(gate);
+  MOE_OPTIONAL(pre_weight);
+  if (y != nullptr && dest_row == nullptr && (b->top_k != 1 || b->rows < b->T)) return MOE_ERR_SHAPE;
+  a->T = b->T;
+  a->H = static_cast<int>(b->H);
+  a->rows = static_cast<int>(b->rows);
+  a->k = static_cast<int>(b->top_k);
+  a->post_norm = b->post_norm;
+  a->scale = b->residual_scale;
+  a->eps = b->eps;
+  a->residual = nullptr;
+  a->y = y;
+  a->dest_row = dest_row;
+  a->topk_w = topk_w;
+  a->post_weight = post_weight;
+  a->gate = gate;
+  a->pre_weight = pre_weight;
+  a->out = nullptr;
+  a->xn = nullptr;
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_block_norm(const moe_block* b, const moe_bf16* residual, const moe_bf16* y,
+                          const int32_t* dest_row, const float* topk_w, const float* post_weight,
+                          const float* gate, const float* pre_weight, moe_bf16* out, moe_bf16* xn,
+                          void* stream) {
+  MOE_TRY(check_block(b));
+  if (b->T == 0) return MOE_OK;
+  MOE_REQUIRE(residual);
+  if (out == nullptr && xn == nullptr) return MOE_ERR_NULL;
+  MOE_OPTIONAL(out);
+  MOE_OPTIONAL(xn);
+  BlockArgs a;
+  MOE_TRY(block_args(b, y, dest_row, topk_w, post_weight, gate, pre_weight, &a));
+  a.residual = residual;
+  a.out = out;
+  a.xn = xn;
+  MOE_CUDA(launch_block(a, num_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_block_norm_workspace_size(int64_t T, int64_t H, size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_NULL;
+  if (T < 0 || H <= 0) return MOE_ERR_SHAPE;
+  if (H % 64 != 0 || H > kBlockMaxWidth || T >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  *bytes = static_cast<size_t>(block_bwd_groups(T, static_cast<int>(H))) * 2 * H * 4;
+  return MOE_OK;
+}
+
+moe_status moe_block_norm_bwd(const moe_block* b, const moe_bf16* h, const moe_bf16* y,
+                              const int32_t* dest_row, const float* topk_w,
+                              const float* post_weight, const float* gate, const float* pre_weight,
+                              const moe_bf16* grad_out, const moe_bf16* grad_xn,
+                              moe_bf16* grad_residual, moe_bf16* grad_y, float* grad_topk_w,
+                              float* grad_post, float* grad_gate, float* grad_pre, void* ws,
+                              size_t ws_bytes, void* stream) {
+  MOE_TRY(check_block(b));
+  MOE_OPTIONAL(grad_residual);
+  MOE_OPTIONAL(grad_y);
+  MOE_OPTIONAL(grad_topk_w);
+  MOE_OPTIONAL(grad_post);
+  MOE_OPTIONAL(grad_gate);
+  MOE_OPTIONAL(grad_pre);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (b->T == 0) {
+    const size_t row = static_cast<size_t>(b->H) * sizeof(float);
+    if (grad_post != nullptr) MOE_CUDA(cudaMemsetAsync(grad_post, 0, row, st));
+    if (grad_pre != nullptr) MOE_CUDA(cudaMemsetAsync(grad_pre, 0, row, st));
+    return MOE_OK;
+  }
+  // a gradient of what is not there, or from nothing
+  if (grad_out == nullptr && grad_xn == nullptr) return MOE_ERR_NULL;
+  MOE_OPTIONAL(grad_out);
+  MOE_OPTIONAL(grad_xn);
+  if (grad_xn != nullptr) MOE_REQUIRE(h);
+  if (grad_xn == nullptr && grad_pre != nullptr) return MOE_ERR_NULL;
+  if (y == nullptr && (grad_y || grad_topk_w || grad_post || grad_gate)) return MOE_ERR_NULL;
+  BlockArgs a;
+  MOE_TRY(block_args(b, y, dest_row, topk_w, post_weight, gate, pre_weight, &a));
+  BlockGrads g;
+  g.h = h;
+  g.out = grad_out;
+  g.xn = grad_xn;
+  g.residual = grad_residual;
+  g.y = grad_y;
+  g.w = grad_topk_w;
+  g.gate = grad_gate;
+  g.post = grad_post;
+  g.pre = grad_pre;
+  g.partial = nullptr;
+  if (grad_post != nullptr || grad_pre != nullptr) {
+    MOE_REQUIRE(ws);
+    size_t need = 0;
+    MOE_TRY(moe_block_norm_workspace_size(b->T, b->H, &need));
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    g.partial = static_cast<float*>(ws);
+  }
+  MOE_CUDA(launch_block_bwd(a, g, st));
   return MOE_OK;
 }
 

@@ -99,6 +99,35 @@ __device__ __forceinline__ float gelu_tanh_f(float u) {
   return __fdividef(u, 1.0f + __expf(-z2));
 }
 
+// Slope of gelu_tanh_f: with s = 1 / (1 + e), e = exp(-2 z),
+//   d/du u s(u) = s + u e s^2 2 dz/du,  2 dz/du = 2 sqrt(2/pi) (1 + 3 * 0.044715 u^2).
+// e s^2 is s (1 - s) without the difference next to 1. Beyond +-8 the slope is
+// 0 or 1 to fp32's last place and the cube would run out of range, so u is
+// held there (a NaN stays one).
+__device__ __forceinline__ float gelu_slope(float u) {
+  float x;
+  asm("min.NaN.f32 %0, %1, 0f41000000;" : "=f"(x) : "f"(u));
+  asm("max.NaN.f32 %0, %0, 0fC1000000;" : "+f"(x));
+  const float x2 = x * x;
+  const float e = __expf(-1.5957691216057308f * fmaf(0.044715f * x2, x, x));
+  const float s = __fdividef(1.0f, 1.0f + e);
+  return fmaf(x * (e * s), s * fmaf(0.2140644488f, x2, 1.5957691216057308f), s);
+}
+
+// 32 fp32 accumulator words to bf16, 64 bytes of one output row. Outputs are
+// read once, by the next kernel: streamed past L2.
+__device__ __forceinline__ void store_row_chunk(uint16_t* dst, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 v;
+    v.x = pack_bf16x2(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
+    v.y = pack_bf16x2(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
+    v.z = pack_bf16x2(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
+    v.w = pack_bf16x2(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
+    st_global_cs_v4(reinterpret_cast<uint4*>(dst) + i, v);
+  }
+}
+
 // kFp8: A and B are e4m3 (both K-major, 128 elements = 128 bytes per
 // stage row), the UMMA is kind::f8f6f4 and the epilogue multiplies by the
 // row scale of A and the column scale of B. Otherwise bf16 A (K-major) and
@@ -111,7 +140,11 @@ __device__ __forceinline__ float gelu_tanh_f(float u) {
 // of a row - exactly the columns one epilogue warp holds - formed from the
 // bf16-rounded values: a first pass over the warp's TMEM chunks finds the
 // block maximum, a second one converts and stores.
-template <bool kFp8, bool kQOut, bool kGather>
+// kTrans (bf16): B is [E][N][K], K-major like A: the product with the
+// transposed weights, as a gradient to the rows takes them.
+// kTrain (bf16): the epilogues of training (GemmArgs::gelu and U): GELU with
+// the value before it kept, or the product times GELU's slope at kept values.
+template <bool kFp8, bool kQOut, bool kGather, bool kTrans, bool kTrain>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                              const __grid_constant__ CUtensorMap tm_b, GemmArgs p) {
@@ -271,7 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               // A: {64 k, 128 rows, kKBS k-blocks}
               tma_load_3d_pair_hint(sa, &tm_a, bar, 0, c.row0, kb * kKBS, pol_a);
             }
-            if constexpr (!kFp8) {
+            if constexpr (kTrans) {
+              // B [E*N, K]: this CTA's 128 output columns as K-major rows
+              tma_load_3d_pair(sb, &tm_b, bar, 0, c.e * p.N + b_col, kb * kKBS);
+            } else if constexpr (!kFp8) {
               // B [E][K][N]: this CTA's two 64-column blocks x 64*kKBS k-rows
               // of expert e in one copy (a copy's cost is mostly per
               // instruction: three per stage held the shared-memory fill
@@ -328,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && leader) {
       // ------------------------------------------- UMMA issuer (leader) ----
       const uint32_t idesc_full =
-          kFp8 ? idesc_e4m3_f32(2 * kBM, kBN) : idesc_bf16_f32(2 * kBM, kBN, false, true);
+          kFp8 ? idesc_e4m3_f32(2 * kBM, kBN) : idesc_bf16_f32(2 * kBM, kBN, false, !kTrans);
       const uint32_t idesc_half = kFp8 ? idesc_e4m3_f32(2 * kBM, kBN / 2)
-                                       : idesc_bf16_f32(2 * kBM, kBN / 2, false, true);
+                                       : idesc_bf16_f32(2 * kBM, kBN / 2, false, !kTrans);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -362,6 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // B: K-major like A
                 const uint64_t bd = smem_desc_sw128(b_addr + kBBytes * r + 32u * kk, 16u, 1024u);
                 umma_f8_pair(d_tmem, ad, bd, idesc, acc_in);
+              } else if constexpr (kTrans) {
+                const uint64_t bd = smem_desc_sw128(b_addr + kBBytes * r + 32u * kk, 16u, 1024u);
+                umma_bf16_pair(d_tmem, ad, bd, idesc, acc_in);
               } else {
                 // B: MN-major, one 128-byte row per k (16-row K step = 2 KB,
                 // k-block r at r * 8 KB), this CTA's two 64-column blocks
@@ -418,6 +457,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<float4*>(wscale)[lane] = v;
         if (valid) rs = p.a_scale[row];
         __syncwarp();
+      }
+      // the first kept values are fetched before the accumulator wait, each
+      // later chunk's while the one before it is worked on
+      const uint16_t* urow = nullptr;
+      uint4 uv[4];
+      if constexpr (kTrain) {
+        if (p.gelu == kEpiGeluGrad && valid && n_chunks > 0) {
+          urow = p.U + static_cast<size_t>(row) * p.N + col0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) uv[i] = ld_global_cs_v4(urow + 8 * i);
+        }
       }
       if (!pair_wait(&tfull[acc], acc_phase)) break;
       tc_fence_after();
@@ -488,7 +538,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t(&r)[32] = (cc & 1) ? rb : ra;
             uint32_t(&nx)[32] = (cc & 1) ? ra : rb;
             if (cc + 1 < n_chunks) tmem_ld_32x32b_x32(t_base + 32u * (cc + 1), nx);
-            if (valid) {
+            if constexpr (kTrain) {
+              if (valid) {
+                if (p.gelu == kEpiGeluGrad) {
+                  uint32_t u[16];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    u[4 * i] = uv[i].x;
+                    u[4 * i + 1] = uv[i].y;
+                    u[4 * i + 2] = uv[i].z;
+                    u[4 * i + 3] = uv[i].w;
+                  }
+                  if (cc + 1 < n_chunks) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      uv[i] = ld_global_cs_v4(urow + 32 * (cc + 1) + 8 * i);
+                  }
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) * gelu_slope(bf16_lo(u[i])));
+                    r[2 * i + 1] =
+                        __float_as_uint(__uint_as_float(r[2 * i + 1]) * gelu_slope(bf16_hi(u[i])));
+                  }
+                } else if (p.gelu == kEpiGelu) {
+                  if (p.U != nullptr) store_row_chunk(p.U + static_cast<size_t>(row) * p.N + col0 + 32 * cc, r);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    r[i] = __float_as_uint(gelu_tanh_f(__uint_as_float(r[i])));
+                }
+                store_row_chunk(drow + col0 + 32 * cc, r);
+              }
+            } else if (valid) {
               uint32_t packed[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -547,7 +627,7 @@ size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage) {
          8 * (2 * stages + 6) + 16 + 8 * static_cast<size_t>(E + 1);
 }
 
-template <bool kFp8, bool kQOut, bool kGather>
+template <bool kFp8, bool kQOut, bool kGather, bool kTrans = false, bool kTrain = false>
 cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const GemmArgs& a,
                         int num_sms, cudaStream_t st) {
   // the deepest ring that fits: every stage in flight hides TMA latency
@@ -563,7 +643,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
          gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs) > static_cast<size_t>(optin))
     --args.stages;
   const size_t smem = gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs);
-  err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather>,
+  err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
@@ -583,7 +663,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kFp8, kQOut, kGather>, tm_a, tm_b,
+  err = cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>, tm_a, tm_b,
                            args);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
@@ -593,6 +673,13 @@ cudaError_t launch_grouped_gemm_pair(const CUtensorMap& tm_a, const CUtensorMap&
                                      const GemmArgs& a, int num_sms, cudaStream_t st) {
   if (a.a_rows != nullptr) return launch_pair<false, false, true>(tm_a, tm_b, a, num_sms, st);
   return launch_pair<false, false, false>(tm_a, tm_b, a, num_sms, st);
+}
+
+cudaError_t launch_expert_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
+                               const GemmArgs& a, bool transposed, int num_sms, cudaStream_t st) {
+  if (transposed)
+    return launch_pair<false, false, false, true, true>(tm_a, tm_b, a, num_sms, st);
+  return launch_pair<false, false, false, false, true>(tm_a, tm_b, a, num_sms, st);
 }
 
 cudaError_t launch_grouped_gemm_pair_fp8(const CUtensorMap& tm_a, const CUtensorMap& tm_b,

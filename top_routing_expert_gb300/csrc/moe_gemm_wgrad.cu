@@ -1,0 +1,456 @@
+// Gradient of the experts' grouped product to the weights:
+//   dW[e] = sum over the rows r of expert e's segment of x[r]^T g[r],
+// a product of [K x n_e] by [n_e x N] per expert whose contraction runs over a
+// ragged segment of rows.
+//
+// Both operands lie with the contraction as their outer dimension, so both are
+// MN-major UMMA operands: a TMA box of 128 rows x 2 blocks of 64 columns (32 KB)
+// is a CTA's share of one operand in a stage, as memory has it. A CTA pair
+// computes 256 x 256 of dW[e] (cta_group::2, M = 256, N = 256): each CTA holds
+// 128 columns of x and 128 of g, and its own 128 rows of the result.
+//
+// A segment starts at any row and its length is no multiple of anything, while
+// a box always has 128 rows: those behind the segment belong to the next expert
+// or to nothing, and may hold infinities or NaN. Only ceil(n / 16) of a stage's
+// eight K steps are issued, and where the last one has rows of both kinds the
+// stage takes a longer way: its loads count on barriers of their own CTA, two
+// warps (one per operand) wait for them, write zeros over the rows behind the
+// segment in both operands, and hand the stage to the issuer.
+//
+// Roles per CTA (384 threads): warp 0 TMA producer; warp 1 UMMA issuer (leader)
+// and TMEM allocation; warps 2, 3 the zeros behind a segment; warps 4-11 the
+// epilogue, each 32 rows x 128 columns of the CTA's 128 x 256: TMEM to registers,
+// through 4 KB of swizzled shared memory, and out by TMA (which cuts the tile at
+// K and N, and with `accumulate` adds in the fp32 gradient's place).
+//
+// Tiles of one expert cost as many stages as its segment has; experts are taken
+// from the longest segment down, so that the round-robin over pairs ends with
+// the cheapest tiles.
+#include "moe_internal.h"
+#include "moe_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 256;          // rows and columns of dW per pair
+constexpr int kDepth = 128;         // rows of x and g per stage
+constexpr int kStages = 3;
+constexpr int kEpiWarps = 8;
+constexpr int kFirstEpi = 4;
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr uint32_t kOpBytes = kDepth * 128 * 2;      // 32 KB: 128 rows x 128 columns
+constexpr uint32_t kBlockBytes = kDepth * 128;       // 16 KB: one block of 64 columns
+constexpr uint32_t kStageBytes = 2 * kOpBytes;
+constexpr uint32_t kOutBytes = 32 * 128;             // one warp's 32 rows x 128 bytes
+constexpr uint32_t kTmemCols = 2 * kTile;
+constexpr int kGroup = 8;           // m-tiles per raster group
+
+struct WgTile {
+  int lo, len, m0, n0, e;
+};
+
+__device__ __forceinline__ WgTile decode_wg(int L, const int* offs, const uint8_t* order, int mt,
+                                            int nt) {
+  const int per_e = mt * nt;
+  WgTile t;
+  t.e = order[L / per_e];
+  t.lo = offs[t.e];
+  t.len = offs[t.e + 1] - t.lo;
+  const int r = L % per_e;
+  const int g = r / (kGroup * nt);
+  const int gsz = min(kGroup, mt - g * kGroup);
+  const int q = r - g * kGroup * nt;
+  t.m0 = (g * kGroup + q % gsz) * kTile;
+  t.n0 = q / gsz * kTile;
+  return t;
+}
+
+// Whether stage kb of a segment of len rows has a K step with rows behind it.
+__device__ __forceinline__ bool is_tail(int len, int kb) {
+  const int left = len - kb * kDepth;
+  return left < kDepth && (left & 15) != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_g,
+                 const __grid_constant__ CUtensorMap tm_d, WgradArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_up_1024(smem_raw);
+  uint8_t* out_buf = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_buf + kEpiWarps * kOutBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tail_ld = empty + kStages;  // own CTA's loads of a stage with a cut K step
+  uint64_t* tail_ok = tail_ld + kStages;  // leader: such a stage has its zeros in both CTAs
+  uint64_t* tfull = tail_ok + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint64_t* xbar = drain + 1;  // leader: the peer's count of loaded stages has arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
+  uint32_t* abort_flag = tmem_slot + 1;
+  uint32_t* peer_issued = abort_flag + 1;
+  int* offs = reinterpret_cast<int*>(peer_issued + 1);        // [E+1]
+  uint8_t* order = reinterpret_cast<uint8_t*>(offs + p.E + 1);  // [E] longest segment first
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = p.E;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == 2 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail_ld[s], 1);
+      mbar_init(&tail_ok[s], 4);  // two warps of each CTA
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpiWarps * 32);
+    }
+    mbar_init(drain, 1);
+    mbar_init(xbar, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 3 && lane == 0) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_g);
+    tma_prefetch_desc(&tm_d);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int i = tid; i <= E; i += kThreads) {
+    const int v = p.offsets[i];
+    offs[i] = v < 0 ? 0 : (v > p.rows ? p.rows : v);
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int i = 1; i <= E; ++i) offs[i] = offs[i] < offs[i - 1] ? offs[i - 1] : offs[i];
+  __syncthreads();
+  for (int e = tid; e < E; e += kThreads) {
+    const int n = offs[e + 1] - offs[e];
+    int before = 0;
+    for (int i = 0; i < E; ++i) {
+      const int m = offs[i + 1] - offs[i];
+      before += m > n || (m == n && i < e);
+    }
+    order[before] = static_cast<uint8_t>(e);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barrier initialisation visible to the peer before any remote use
+  tc_fence_after();
+
+  const uint32_t tmem_base = *tmem_slot;
+  const int mt = (p.K + kTile - 1) / kTile, nt = (p.N + kTile - 1) / kTile;
+  const int total = E * mt * nt;
+  const WaitCtl wc{abort_flag, p.dev_status, p.timeout_ns};
+  const uint32_t peer_abort = mapa_shared(smem_u32(abort_flag), rank ^ 1u);
+  auto pair_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_wait(bar, parity, wc)) return true;
+    st_u32_cluster(peer_abort, 1u);
+    return false;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer ----
+      int stage = 0;
+      uint32_t phase = 0;
+      // per stage, as bits: parity of the next use of full and of tail_ld, and
+      // whether the last use was a tail
+      uint32_t full_par = 0, tail_par = 0, was_tail = 0;
+      int issued = 0;
+      bool aborted = false;
+      for (int L = cluster; L < total && !aborted; L += n_clusters) {
+        const WgTile c = decode_wg(L, offs, order, mt, nt);
+        const int nk = (c.len + kDepth - 1) / kDepth;
+        const bool half_n = p.N - c.n0 <= kTile / 2;
+        const int xb = (c.m0 + static_cast<int>(rank) * (kTile / 2)) / 64;
+        const int gb = (c.n0 + static_cast<int>(rank) * (half_n ? kTile / 4 : kTile / 2)) / 64;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!pair_wait(&empty[stage], phase ^ 1u)) {
+            aborted = true;
+            break;
+          }
+          const uint32_t bit = 1u << stage;
+          uint32_t bar;
+          if (is_tail(c.len, kb)) {
+            mbar_arrive_expect_tx(&tail_ld[stage], kStageBytes);
+            bar = mapa_shared(smem_u32(&tail_ld[stage]), rank);
+            tail_par ^= bit;
+            was_tail |= bit;
+          } else {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+            bar = mapa_shared(smem_u32(&full[stage]), 0);
+            full_par ^= bit;
+            was_tail &= ~bit;
+          }
+          uint8_t* sx = smem + stage * kStageBytes;
+          const int row = c.lo + kb * kDepth;
+          tma_load_3d_pair(sx, &tm_x, bar, 0, row, xb);
+          tma_load_3d_pair(sx + kOpBytes, &tm_g, bar, 0, row, gb);
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // No CTA exits before its loads have landed (the kernel ends with a
+      // cluster barrier). Loads of a tail count on their own CTA's barrier; the
+      // others of both CTAs on the leader's. After an abort the two may have
+      // stopped at different stages: the peer reports how many it loaded, and
+      // the leader makes the accounting of each stage in flight whole before it
+      // waits. (Both walk the same tiles, so stage i is of one kind in both;
+      // where the leader never reached it, waiting for a tail as for another
+      // stage only runs into the limit.)
+      if (!leader) {
+        st_async_u32_cluster(mapa_shared(smem_u32(peer_issued), 0), static_cast<uint32_t>(issued),
+                             mapa_shared(smem_u32(xbar), 0));
+        for (int i = max(0, issued - kStages); i < issued; ++i) {
+          const int s = i % kStages;
+          if (was_tail >> s & 1u) mbar_wait_drain(&tail_ld[s], (tail_par >> s & 1u) ^ 1u, kDrainLimitNs);
+        }
+      } else {
+        mbar_arrive_expect_tx(xbar, 4);
+        int theirs = issued;
+        if (mbar_wait_drain(xbar, 0, p.timeout_ns + kDrainLimitNs)) {
+          theirs = min(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(peer_issued)),
+                       issued + kStages);
+        } else {
+          atomicOr(p.dev_status, MOE_DEV_TIMEOUT);
+        }
+        const int hi = max(issued, theirs);
+        for (int i = max(0, hi - kStages); i < hi; ++i) {
+          const int s = i % kStages;
+          if (i >= issued) {
+            mbar_arrive_expect_tx(&full[s], kStageBytes);  // the peer's half alone
+            mbar_wait_drain(&full[s], full_par >> s & 1u, kDrainLimitNs);
+          } else if (was_tail >> s & 1u) {
+            mbar_wait_drain(&tail_ld[s], (tail_par >> s & 1u) ^ 1u, kDrainLimitNs);
+          } else {
+            if (i >= theirs) mbar_complete_tx(&full[s], kStageBytes);  // will never come
+            mbar_wait_drain(&full[s], (full_par >> s & 1u) ^ 1u, kDrainLimitNs);
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------- UMMA issuer (leader) ----
+      int stage = 0;
+      uint32_t full_par = 0, tail_par = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool aborted = false;
+      for (int L = cluster; L < total && !aborted; L += n_clusters) {
+        const WgTile c = decode_wg(L, offs, order, mt, nt);
+        if (c.len == 0) continue;
+        if (!pair_wait(&tempty[acc], acc_phase ^ 1u)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
+        const uint32_t idesc = idesc_bf16_f32(kTile, p.N - c.n0 <= kTile / 2 ? kTile / 2 : kTile,
+                                              true, true);
+        const int nk = (c.len + kDepth - 1) / kDepth;
+        for (int kb = 0; kb < nk; ++kb) {
+          const uint32_t bit = 1u << stage;
+          bool ok;
+          if (is_tail(c.len, kb)) {
+            ok = mbar_wait<true>(&tail_ok[stage], tail_par >> stage & 1u, wc);
+            if (!ok) st_u32_cluster(peer_abort, 1u);
+            tail_par ^= bit;
+          } else {
+            ok = pair_wait(&full[stage], full_par >> stage & 1u);
+            full_par ^= bit;
+          }
+          if (!ok) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t x_addr = smem_u32(smem + stage * kStageBytes);
+          const uint32_t g_addr = x_addr + kOpBytes;
+          const int steps = min(kDepth / 16, (c.len - kb * kDepth + 15) / 16);
+#pragma unroll
+          for (int kk = 0; kk < kDepth / 16; ++kk) {
+            if (kk < steps) {
+              // one 128-byte row per k: a 16-row K step is 2 KB; blocks of 64
+              // columns are 16 KB apart
+              const uint64_t xd = smem_desc_sw128(x_addr + 2048u * kk, kBlockBytes, 1024u);
+              const uint64_t gd = smem_desc_sw128(g_addr + 2048u * kk, kBlockBytes, 1024u);
+              umma_bf16_pair(d_tmem, xd, gd, idesc, (kb | kk) != 0 ? 1u : 0u);
+            }
+          }
+          umma_commit_pair_multicast(&empty[stage], 0x3);
+          if (++stage == kStages) stage = 0;
+        }
+        if (aborted) break;
+        umma_commit_pair_multicast(&tfull[acc], 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      // every UMMA issued must finish before TMEM is released
+      umma_commit_pair(drain);
+      mbar_wait_drain(drain, 0, kDrainLimitNs);
+    }
+  } else if (warp < kFirstEpi) {
+    // ------------------------------------- zeros behind a segment's end ----
+    // this warp's operand of each tail stage: whole 128-byte rows, which the
+    // swizzle keeps together
+    const uint32_t op = smem_u32(smem) + (warp == 3 ? kOpBytes : 0u);
+    int stage = 0;
+    uint32_t tail_par = 0;
+    bool aborted = false;
+    for (int L = cluster; L < total && !aborted; L += n_clusters) {
+      const WgTile c = decode_wg(L, offs, order, mt, nt);
+      const int nk = (c.len + kDepth - 1) / kDepth;
+      if (nk == 0) continue;
+      const int s = (stage + nk - 1) % kStages;
+      stage = (stage + nk) % kStages;
+      if (!is_tail(c.len, nk - 1)) continue;
+      if (!pair_wait(&tail_ld[s], tail_par >> s & 1u)) {
+        aborted = true;
+        break;
+      }
+      tail_par ^= 1u << s;
+      const int left = c.len - (nk - 1) * kDepth;
+      const int words = (((left + 15) & ~15) - left) * 8;  // 16-byte words per block
+      const uint32_t at = op + s * kStageBytes + 128u * left;
+      for (int i = lane; i < 2 * words; i += 32)
+        st_shared_v4(at + (i >= words ? kBlockBytes + 16u * (i - words) : 16u * i),
+                     make_uint4(0, 0, 0, 0));
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release_shared(mapa_shared(smem_u32(&tail_ok[s]), 0));
+    }
+  } else {
+    // ------------------------------------------------------ epilogue ----
+    const int q = warp & 3;
+    const int half = (warp - kFirstEpi) >> 2;
+    const uint32_t buf = smem_u32(out_buf) + static_cast<uint32_t>(warp - kFirstEpi) * kOutBytes;
+    // this lane's row of the buffer: 128 bytes in eight 16-byte words, word w at
+    // w ^ (row & 7) as the 128-byte swizzle of the store has it
+    const uint32_t my = buf + 128u * lane;
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
+                                       mapa_shared(smem_u32(&tempty[1]), 0)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int L = cluster; L < total; L += n_clusters) {
+      const WgTile c = decode_wg(L, offs, order, mt, nt);
+      if (c.len == 0 && p.accumulate) continue;
+      if (c.len > 0) {
+        if (!pair_wait(&tfull[acc], acc_phase)) break;
+        tc_fence_after();
+      }
+      const int row = c.m0 + static_cast<int>(rank) * (kTile / 2) + 32 * q;
+      const int col0 = c.n0 + half * (kTile / 2);
+      const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                              static_cast<uint32_t>(acc * kTile + half * (kTile / 2));
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        const int col = col0 + 32 * cc;
+        if (col >= p.N || row >= p.K) break;  // N and K are multiples of 64
+        uint32_t r[32];
+        if (c.len > 0) {
+          tmem_ld_32x32b_x32(t_base + 32u * cc, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+        if (p.bf16_out) {
+          // two chunks share a buffer of 64 columns
+          if ((cc & 1) == 0) {
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
+            v.y = pack_bf16x2(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
+            v.z = pack_bf16x2(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
+            v.w = pack_bf16x2(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
+            st_shared_v4(my + 16u * ((4 * (cc & 1) + i) ^ (lane & 7)), v);
+          }
+          if ((cc & 1) == 1) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tma_store_3d(&tm_d, buf, col - 32, row, c.e);
+          }
+        } else {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            st_shared_v4(my + 16u * (i ^ (lane & 7)),
+                         make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            if (p.accumulate) tma_reduce_add_3d(&tm_d, buf, col, row, c.e);
+            else tma_store_3d(&tm_d, buf, col, row, c.e);
+          }
+        }
+      }
+      if (c.len > 0) {
+        tc_fence_before();
+        mbar_arrive_cluster(tempty_leader[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) tma_store_wait();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the peer may still signal it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
+}
+
+size_t wgrad_smem_bytes(int E) {
+  return 1024 + kStages * kStageBytes + kEpiWarps * kOutBytes + 8 * (4 * kStages + 6) + 16 +
+         4 * static_cast<size_t>(E + 1) + static_cast<size_t>(E);
+}
+
+}  // namespace
+
+cudaError_t launch_wgrad(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
+                         const WgradArgs& a, int num_sms, cudaStream_t st) {
+  const size_t smem = wgrad_smem_bytes(a.E);
+  cudaError_t err = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (num_sms / 2)), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, wgrad_kernel, tm_x, tm_g, tm_d, a);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace moe

@@ -130,6 +130,37 @@ struct GroupedBwdArgs {
   float* grad_logits;      // [T,E]
 };
 
+// The step between two blocks and its gradient (csrc/moe_block.cu).
+constexpr int kBlockMaxWidth = 16384;
+constexpr int kBlockMaxGroups = 1216;  // partial rows of the gradient's sums over tokens
+struct BlockArgs {
+  int64_t T;
+  int H, rows, k;             // width; rows of y; slots per token
+  int post_norm;
+  float scale, eps;
+  const uint16_t* residual;   // [T,H] (forward)
+  const uint16_t* y;          // [rows,H] or nullptr (no block output)
+  const int32_t* dest_row;    // [T,k] or nullptr (token t's row is t)
+  const float* topk_w;        // [T,k] or nullptr (1)
+  const float* post_weight;   // [H] or nullptr (1)
+  const float* gate;          // [T] or nullptr (1)
+  const float* pre_weight;    // [H] or nullptr (1)
+  uint16_t* out;              // [T,H] or nullptr (forward)
+  uint16_t* xn;               // [T,H] or nullptr (forward)
+};
+struct BlockGrads {
+  const uint16_t* h;          // [T,H] the stream as the forward stored it, with xn
+  const uint16_t* out;        // [T,H] gradient of out, or nullptr (0)
+  const uint16_t* xn;         // [T,H] gradient of xn, or nullptr
+  uint16_t* residual;         // [T,H], and the others below: or nullptr (not formed)
+  uint16_t* y;                // [rows,H]
+  float* w;                   // [T,k]
+  float* gate;                // [T]
+  float* post;                // [H]
+  float* pre;                 // [H]
+  float* partial;             // [block_bwd_groups][2][H], or nullptr without post and pre
+};
+
 // TMEM columns the router allocates: a power of two >= 32 covering E_pad.
 __host__ __device__ inline int route_tmem_cols(int E_pad) {
   int c = 32;
@@ -137,12 +168,17 @@ __host__ __device__ inline int route_tmem_cols(int E_pad) {
   return c;
 }
 
+// Epilogues of the grouped product (GemmArgs::gelu; the last one with U).
+enum { kEpiNone = 0, kEpiGelu = 1, kEpiGeluGrad = 2 };
+
 struct GemmArgs {
   const int32_t* offsets;  // [E+1] row segments of the expert-major buffer
   int E, K, N;             // reduction size, output columns
   int rows;                // rows of the A and D buffers (T*k)
   uint16_t* D;             // [rows, N] bf16
   int gelu;                // 1: act = gelu_tanh(acc), 0: plain
+  uint16_t* U = nullptr;   // training: [rows, N] values before the GELU, written by kEpiGelu
+                           // (where given), read by kEpiGeluGrad
   const float* a_scale;    // FP8 mode: per-row scales of A [rows]
   const float* b_scale;    // FP8 mode: per-column scales of B [E, N]
   uint32_t* row_amax;      // FP8 mode, optional: max |bf16 output| per row, fp32 bits,
@@ -152,6 +188,16 @@ struct GemmArgs {
   const int32_t* a_rows;   // optional: A row r is row a_rows[r] of the A tensor (a gather,
   int a_src_rows;          //   by TMA, from a tensor of a_src_rows rows); CTA-pair kernel
   int stages;              // CTA-pair kernel: pipeline depth (set by its launcher)
+  uint32_t* dev_status;
+  uint64_t timeout_ns;
+};
+
+// Gradient of the grouped product to the weights (csrc/moe_gemm_wgrad.cu).
+struct WgradArgs {
+  const int32_t* offsets;  // [E+1] row segments
+  int E, K, N, rows;
+  int bf16_out;            // dW [E,K,N] is bf16, otherwise fp32
+  int accumulate;          // fp32: add to dW
   uint32_t* dev_status;
   uint64_t timeout_ns;
 };
@@ -254,6 +300,15 @@ cudaError_t launch_grouped_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b
                                 const GemmArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_grouped_gemm_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                                      const GemmArgs& a, int num_sms, cudaStream_t st);
+// The product alone, with W [E][K][N] or (transposed) [E][N][K] and the
+// epilogues above; CTA-pair kernel at every size.
+cudaError_t launch_expert_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
+                               const GemmArgs& a, bool transposed, int num_sms, cudaStream_t st);
+cudaError_t launch_wgrad(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
+                         const WgradArgs& a, int num_sms, cudaStream_t st);
+int block_bwd_groups(int64_t T, int H);
+cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, cudaStream_t st);
 size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage);
 // FP8 operands; writes D (bf16), or Dq + d_scale when a.Dq is set
 cudaError_t launch_grouped_gemm_pair_fp8(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
