@@ -13,15 +13,16 @@
 // a box always has 128 rows: those behind the segment belong to the next expert
 // or to nothing, and may hold infinities or NaN. Only ceil(n / 16) of a stage's
 // eight K steps are issued, and where the last one has rows of both kinds the
-// stage takes a longer way: its loads count on barriers of their own CTA, two
-// warps (one per operand) wait for them, write zeros over the rows behind the
-// segment in both operands, and hand the stage to the issuer.
+// stage takes a longer way: its loads count on barriers of their own CTA, a
+// warp waits for them, writes zeros over the rows behind the segment in both
+// operands, and hands the stage to the issuer.
 //
-// Roles per CTA (384 threads): warp 0 TMA producer; warp 1 UMMA issuer (leader)
-// and TMEM allocation; warps 2, 3 the zeros behind a segment; warps 4-11 the
-// epilogue, each 32 rows x 128 columns of the CTA's 128 x 256: TMEM to registers,
-// through 4 KB of swizzled shared memory, and out by TMA (which cuts the tile at
-// K and N, and with `accumulate` adds in the fp32 gradient's place).
+// Roles per CTA (352 threads): warp 0 TMA producer; warp 1 UMMA issuer (leader)
+// and TMEM allocation; warp 2 the zeros behind a segment; warps 3-10 the
+// epilogue, each 32 rows x 128 columns of the CTA's 128 x 256: TMEM is added to
+// registers piece by piece, and a finished tile goes through 4 KB of swizzled
+// shared memory a warp and out by TMA (which cuts the tile at K and N, and with
+// `accumulate` adds in the fp32 gradient's place).
 //
 // Tiles of one expert cost as many stages as its segment has; experts are taken
 // from the longest segment down, so that the round-robin over pairs ends with
@@ -37,7 +38,7 @@ constexpr int kTile = 256;          // rows and columns of dW per pair
 constexpr int kDepth = 128;         // rows of x and g per stage
 constexpr int kStages = 3;
 constexpr int kEpiWarps = 8;
-constexpr int kFirstEpi = 4;
+constexpr int kFirstEpi = 3;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr uint32_t kOpBytes = kDepth * 128 * 2;      // 32 KB: 128 rows x 128 columns
 constexpr uint32_t kBlockBytes = kDepth * 128;       // 16 KB: one block of 64 columns
@@ -45,6 +46,11 @@ constexpr uint32_t kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kOutBytes = 32 * 128;             // one warp's 32 rows x 128 bytes
 constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr int kGroup = 8;           // m-tiles per raster group
+// Stages summed in TMEM before the sum moves to registers. The tensor core's
+// fp32 additions cut towards zero, a bias of about 2^-25 of the sum each, which
+// adds up over a long segment: 9e-6 of the result after 8192 rows. The epilogue
+// adds the pieces with rounding.
+constexpr int kPiece = 4;
 
 struct WgTile {
   int lo, len, m0, n0, e;
@@ -107,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&tail_ld[s], 1);
-      mbar_init(&tail_ok[s], 4);  // two warps of each CTA
+      mbar_init(&tail_ok[s], 2);  // a warp of each CTA
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0u;
     fence_barrier_init();
   }
-  if (warp == 3 && lane == 0) {
+  if (warp == kFirstEpi && lane == 0) {
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_g);
     tma_prefetch_desc(&tm_d);
@@ -253,13 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int L = cluster; L < total && !aborted; L += n_clusters) {
         const WgTile c = decode_wg(L, offs, order, mt, nt);
         if (c.len == 0) continue;
-        if (!pair_wait(&tempty[acc], acc_phase ^ 1u)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
         const uint32_t idesc = idesc_bf16_f32(kTile, p.N - c.n0 <= kTile / 2 ? kTile / 2 : kTile,
                                               true, true);
         const int nk = (c.len + kDepth - 1) / kDepth;
         for (int kb = 0; kb < nk; ++kb) {
+          const int in_piece = kb % kPiece;
+          if (in_piece == 0) {
+            if (!pair_wait(&tempty[acc], acc_phase ^ 1u)) {
+              aborted = true;
+              break;
+            }
+            tc_fence_after();
+          }
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
           const uint32_t bit = 1u << stage;
           bool ok;
           if (is_tail(c.len, kb)) {
@@ -285,17 +297,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               // columns are 16 KB apart
               const uint64_t xd = smem_desc_sw128(x_addr + 2048u * kk, kBlockBytes, 1024u);
               const uint64_t gd = smem_desc_sw128(g_addr + 2048u * kk, kBlockBytes, 1024u);
-              umma_bf16_pair(d_tmem, xd, gd, idesc, (kb | kk) != 0 ? 1u : 0u);
+              umma_bf16_pair(d_tmem, xd, gd, idesc, (in_piece | kk) != 0 ? 1u : 0u);
             }
           }
           umma_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == kStages) stage = 0;
-        }
-        if (aborted) break;
-        umma_commit_pair_multicast(&tfull[acc], 0x3);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
+          if (in_piece == kPiece - 1 || kb == nk - 1) {
+            umma_commit_pair_multicast(&tfull[acc], 0x3);
+            if (++acc == 2) {
+              acc = 0;
+              acc_phase ^= 1u;
+            }
+          }
         }
       }
       // every UMMA issued must finish before TMEM is released
@@ -304,9 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kFirstEpi) {
     // ------------------------------------- zeros behind a segment's end ----
-    // this warp's operand of each tail stage: whole 128-byte rows, which the
-    // swizzle keeps together
-    const uint32_t op = smem_u32(smem) + (warp == 3 ? kOpBytes : 0u);
+    // whole 128-byte rows, which the swizzle keeps together, in the four
+    // 64-column blocks (two of each operand) of each tail stage
     int stage = 0;
     uint32_t tail_par = 0;
     bool aborted = false;
@@ -324,10 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tail_par ^= 1u << s;
       const int left = c.len - (nk - 1) * kDepth;
       const int words = (((left + 15) & ~15) - left) * 8;  // 16-byte words per block
-      const uint32_t at = op + s * kStageBytes + 128u * left;
-      for (int i = lane; i < 2 * words; i += 32)
-        st_shared_v4(at + (i >= words ? kBlockBytes + 16u * (i - words) : 16u * i),
-                     make_uint4(0, 0, 0, 0));
+      const uint32_t at = smem_u32(smem) + s * kStageBytes + 128u * left;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        for (int i = lane; i < words; i += 32)
+          st_shared_v4(at + b * kBlockBytes + 16u * i, make_uint4(0, 0, 0, 0));
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive_release_shared(mapa_shared(smem_u32(&tail_ok[s]), 0));
@@ -344,70 +357,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        mapa_shared(smem_u32(&tempty[1]), 0)};
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int L = cluster; L < total; L += n_clusters) {
+    bool aborted = false;
+    for (int L = cluster; L < total && !aborted; L += n_clusters) {
       const WgTile c = decode_wg(L, offs, order, mt, nt);
       if (c.len == 0 && p.accumulate) continue;
-      if (c.len > 0) {
-        if (!pair_wait(&tfull[acc], acc_phase)) break;
-        tc_fence_after();
-      }
       const int row = c.m0 + static_cast<int>(rank) * (kTile / 2) + 32 * q;
       const int col0 = c.n0 + half * (kTile / 2);
-      const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                              static_cast<uint32_t>(acc * kTile + half * (kTile / 2));
-#pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        const int col = col0 + 32 * cc;
-        if (col >= p.N || row >= p.K) break;  // N and K are multiples of 64
-        uint32_t r[32];
-        if (c.len > 0) {
-          tmem_ld_32x32b_x32(t_base + 32u * cc, r);
-          tmem_ld_wait();
-        } else {
+      // whole 32-column chunks: N and K are multiples of 64
+      const int n_chunks = col0 >= p.N || row >= p.K ? 0 : min(4, (p.N - col0) / 32);
+      float sum[128];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0u;
+      for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+      for (int left = c.len; left > 0; left -= kPiece * kDepth) {
+        if (!pair_wait(&tfull[acc], acc_phase)) {
+          aborted = true;
+          break;
         }
-        if (p.bf16_out) {
-          // two chunks share a buffer of 64 columns
-          if ((cc & 1) == 0) {
-            if (lane == 0) tma_store_wait_read();
-            __syncwarp();
-          }
+        tc_fence_after();
+        const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                static_cast<uint32_t>(acc * kTile + half * (kTile / 2));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
-            v.y = pack_bf16x2(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
-            v.z = pack_bf16x2(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
-            v.w = pack_bf16x2(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
-            st_shared_v4(my + 16u * ((4 * (cc & 1) + i) ^ (lane & 7)), v);
-          }
-          if ((cc & 1) == 1) {
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) tma_store_3d(&tm_d, buf, col - 32, row, c.e);
-          }
-        } else {
-          if (lane == 0) tma_store_wait_read();
-          __syncwarp();
+        for (int cc = 0; cc < 8; ++cc) {
+          if (cc < 2 * n_chunks) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_base + 16u * cc, r);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            st_shared_v4(my + 16u * (i ^ (lane & 7)),
-                         make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            if (p.accumulate) tma_reduce_add_3d(&tm_d, buf, col, row, c.e);
-            else tma_store_3d(&tm_d, buf, col, row, c.e);
+            for (int i = 0; i < 16; ++i) sum[16 * cc + i] += __uint_as_float(r[i]);
           }
         }
-      }
-      if (c.len > 0) {
         tc_fence_before();
         mbar_arrive_cluster(tempty_leader[acc]);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
+        }
+      }
+      if (aborted) break;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        if (cc < n_chunks) {
+          const int col = col0 + 32 * cc;
+          if (p.bf16_out) {
+            // two chunks share a buffer of 64 columns
+            if ((cc & 1) == 0) {
+              if (lane == 0) tma_store_wait_read();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* v = sum + 32 * cc + 8 * i;
+              st_shared_v4(my + 16u * ((4 * (cc & 1) + i) ^ (lane & 7)),
+                           make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+            }
+            if ((cc & 1) == 1) {
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) tma_store_3d(&tm_d, buf, col - 32, row, c.e);
+            }
+          } else {
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* v = sum + 32 * cc + 4 * i;
+              st_shared_v4(my + 16u * (i ^ (lane & 7)),
+                           make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                      __float_as_uint(v[2]), __float_as_uint(v[3])));
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (p.accumulate) tma_reduce_add_3d(&tm_d, buf, col, row, c.e);
+              else tma_store_3d(&tm_d, buf, col, row, c.e);
+            }
+          }
         }
       }
     }
