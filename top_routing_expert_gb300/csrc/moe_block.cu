@@ -108,6 +108,12 @@ __device__ __forceinline__ Slot load_slot(const BlockArgs& a, int64_t t, int lan
   return s;
 }
 
+// Asks L2 to fetch a row of H bf16 values.
+__device__ __forceinline__ void prefetch_row(const uint16_t* base, int64_t row, int H) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(base + row * H), "r"(2 * H)
+               : "memory");
+}
+
 // c[v][8] = sum over the slots, ascending, of w_j y_j.
 template <int G, int NV>
 __device__ __forceinline__ void combine_rows(const BlockArgs& a, const Slot& s, int gt, int nvec,
@@ -160,10 +166,12 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_kernel(BlockArgs a) {
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPer;
   int turn = 0;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / G;
-  Slot next{-1, 0.f};
-  if (a.y != nullptr) next = load_slot(a, t, lane);
-  for (; t < a.T; t += step) {
-    const Slot s = next;
+  Slot s{-1, 0.f}, next{-1, 0.f}, next2{-1, 0.f};
+  if (a.y != nullptr) {
+    s = load_slot(a, t, lane);
+    next = load_slot(a, t + step, lane);
+  }
+  for (; t < a.T; t += step, s = next, next = next2) {
     uint4 res[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -174,8 +182,12 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_kernel(BlockArgs a) {
     float gate = 1.f;
     if (a.gate != nullptr) gate = a.gate[t];
     float h[NV][8];
+    if (gt < 32 && t + step < a.T) {
+      if (next.row >= 0) prefetch_row(a.y, next.row, a.H);
+      if (lane == 8) prefetch_row(a.residual, t + step, a.H);
+    }
     if (a.y != nullptr) {
-      next = load_slot(a, t + step, lane);
+      next2 = load_slot(a, t + 2 * step, lane);
       combine_rows<G, NV>(a, s, gt, nvec, h);
       float r = gate;
       if (a.post_norm) {
@@ -257,11 +269,13 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_bwd_kernel(BlockArgs 
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int q = 0; q < 8; ++q) s_post[v][q] = s_pre[v][q] = 0.f;
-  Slot next{-1, 0.f};
-  if (a.y != nullptr) next = load_slot(a, t, lane);
+  Slot s{-1, 0.f}, next{-1, 0.f}, next2{-1, 0.f};
+  if (a.y != nullptr) {
+    s = load_slot(a, t, lane);
+    next = load_slot(a, t + step, lane);
+  }
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (; t < a.T; t += step) {
-    const Slot s = next;
+  for (; t < a.T; t += step, s = next, next = next2) {
     uint4 hv[NV], xv[NV], ov[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -275,8 +289,14 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_bwd_kernel(BlockArgs 
     if (a.gate != nullptr) gate = a.gate[t];
     float c[NV][8];
     float sums[3] = {0.f, 0.f, 0.f};  // h^2, pre g_xn h, c^2
+    if (gt < 32 && t + step < a.T) {
+      if (next.row >= 0) prefetch_row(a.y, next.row, a.H);
+      if (lane == 8 && g.out != nullptr) prefetch_row(g.out, t + step, a.H);
+      if (lane == 9 && g.xn != nullptr) prefetch_row(g.xn, t + step, a.H);
+      if (lane == 10 && g.xn != nullptr) prefetch_row(g.h, t + step, a.H);
+    }
     if (a.y != nullptr) {
-      next = load_slot(a, t + step, lane);
+      next2 = load_slot(a, t + 2 * step, lane);
       combine_rows<G, NV>(a, s, gt, nvec, c);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -420,8 +440,10 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   float* out = col < H ? post : pre;
   float s = 0.f;
-  if (out != nullptr)
+  if (out != nullptr) {
+#pragma unroll 8
     for (int i = slice; i < n; i += 8) s += partial[static_cast<size_t>(i) * 2 * H + col];
+  }
   part[slice][threadIdx.x & 31] = s;
   __syncthreads();
   if (slice == 0 && out != nullptr) {
