@@ -1768,7 +1768,7 @@ moe_status moe_block_norm_bwd(const moe_block* b, const moe_bf16* h, const moe_b
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     g.partial = static_cast<float*>(ws);
   }
-  MOE_CUDA(launch_block_bwd(a, g, st));
+  MOE_CUDA(launch_block_bwd(a, g, num_sms(), st));
   return MOE_OK;
 }
 

@@ -26,48 +26,68 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Values are worked on as pairs in 64-bit registers, one instruction for two.
+using F2 = uint64_t;
+
+__device__ __forceinline__ void unpack8(const uint4& v, F2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = f32x2(bf16_lo(w[i]), bf16_hi(w[i]));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint4 v;
-  v.x = pack_bf16x2(f[0], f[1]);
-  v.y = pack_bf16x2(f[2], f[3]);
-  v.z = pack_bf16x2(f[4], f[5]);
-  v.w = pack_bf16x2(f[6], f[7]);
-  return v;
+__device__ __forceinline__ uint32_t pack2(F2 v) {
+  float lo, hi;
+  f32x2_get(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+  return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+
+__device__ __forceinline__ float sum2(F2 v) {
+  float lo, hi;
+  f32x2_get(v, lo, hi);
+  return lo + hi;
 }
 
 // 8 fp32 weights from column 8 * i, or ones.
-__device__ __forceinline__ void weight8(const float* w, int i, float (&f)[8]) {
+__device__ __forceinline__ void weight8(const float* w, int i, F2 (&f)[4]) {
   if (w == nullptr) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[q] = 1.f;
+    for (int q = 0; q < 4; ++q) f[q] = f32x2(1.f, 1.f);
     return;
   }
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * i);
-  const float4 b = __ldg(reinterpret_cast<const float4*>(w) + 2 * i + 1);
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = a.z;
-  f[3] = a.w;
-  f[4] = b.x;
-  f[5] = b.y;
-  f[6] = b.z;
-  f[7] = b.w;
+  const float4 a = reinterpret_cast<const float4*>(w)[2 * i];
+  const float4 b = reinterpret_cast<const float4*>(w)[2 * i + 1];
+  f[0] = f32x2(a.x, a.y);
+  f[1] = f32x2(a.z, a.w);
+  f[2] = f32x2(b.x, b.y);
+  f[3] = f32x2(b.z, b.w);
 }
 
-// Sums of M values over the G threads of a token's group, in every thread.
-// G > 32: the group is the block; `red` holds M * G/32 values for each of two
-// alternating calls, so one barrier a call is enough.
+// A token's group is one warp (G = 32) or the whole block of G threads. Cross-warp
+// scratch of such a block: three areas of 8 values a warp, taken in turn. A call's
+// area is written again three calls later, after two barriers that every reader of
+// the first has reached.
+template <int G>
+struct Scratch {
+  static constexpr int W = G / 32;
+  float v[3][8 * W];
+  __device__ __forceinline__ static float warps(const float* r) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; w += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(r + w);
+      s += (q.x + q.y) + (q.z + q.w);
+    }
+    return s;
+  }
+};
+
+// Sums of M values over a token's group, in every thread.
 template <int G, int M>
-__device__ __forceinline__ void group_sum(float (&v)[M], float* red, int& turn) {
+__device__ __forceinline__ void group_sum(float (&v)[M], Scratch<G>& red, int& turn) {
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -75,20 +95,46 @@ __device__ __forceinline__ void group_sum(float (&v)[M], float* red, int& turn) 
   if constexpr (G > 32) {
     constexpr int W = G / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* r = red + turn * (8 * W);
-    turn ^= 1;
+    float* r = red.v[turn];
+    turn = turn == 2 ? 0 : turn + 1;
     if (lane == 0) {
 #pragma unroll
       for (int m = 0; m < M; ++m) r[m * W + warp] = v[m];
     }
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      float s = 0.f;
+    for (int m = 0; m < M; ++m) v[m] = red.warps(r + m * W);
+  }
+}
+
+// Sums of 8 values over the group, value j in thread j of it. A warp halves the
+// values it still holds with each of the first three exchanges.
+template <int G>
+__device__ __forceinline__ float group_sum8(float (&v)[8], Scratch<G>& red, int& turn) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += r[m * W + w];
-      v[m] = s;
+  for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
+  }
+  float s = v[0];
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  // lanes 4j .. 4j+3 hold value j
+  if constexpr (G > 32) {
+    constexpr int W = G / 32;
+    const int warp = threadIdx.x >> 5;
+    float* r = red.v[turn];
+    turn = turn == 2 ? 0 : turn + 1;
+    if ((lane & 3) == 0) r[(lane >> 2) * W + warp] = s;
+    __syncthreads();
+    return threadIdx.x < 8 ? red.warps(r + threadIdx.x * W) : 0.f;
+  } else {
+    return __shfl_sync(0xffffffffu, s, 4 * (lane & 7));
   }
 }
 
@@ -114,53 +160,70 @@ __device__ __forceinline__ void prefetch_row(const uint16_t* base, int64_t row, 
                : "memory");
 }
 
-// c[v][8] = sum over the slots, ascending, of w_j y_j.
-template <int G, int NV>
+// c[v][8] = sum over the slots, ascending, of w_j y_j; KU rows in flight together.
+template <int G, int NV, int KU>
 __device__ __forceinline__ void combine_rows(const BlockArgs& a, const Slot& s, int gt, int nvec,
-                                             float (&c)[NV][8]) {
-  constexpr int KU = NV <= 2 ? 4 : 2;  // rows in flight together
+                                             F2 (&c)[NV][4]) {
   const uint4* yv = reinterpret_cast<const uint4*>(a.y);
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) c[v][q] = 0.f;
+    for (int q = 0; q < 4; ++q) c[v][q] = 0;
   for (int j0 = 0; j0 < a.k; j0 += KU) {
     uint4 b[KU][NV];
-    float w[KU];
+    int row[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-      const int j = j0 + u;
-      const int row = __shfl_sync(0xffffffffu, s.row, j & 31);
-      w[u] = __shfl_sync(0xffffffffu, s.w, j & 31);
-      if (row < 0) w[u] = 0.f;  // lanes from k up hold no row
+      row[u] = __shfl_sync(0xffffffffu, s.row, j0 + u);  // lanes from k up hold no row
+      if (row[u] >= 0) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int i = gt + G * v;
-        b[u][v] = row >= 0 && i < nvec ? __ldg(yv + static_cast<size_t>(row) * nvec + i)
-                                       : make_uint4(0, 0, 0, 0);
+        for (int v = 0; v < NV; ++v) {
+          const int i = gt + G * v;
+          b[u][v] = i < nvec ? __ldg(yv + static_cast<size_t>(row[u]) * nvec + i)
+                             : make_uint4(0, 0, 0, 0);
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < KU; ++u)
+    for (int u = 0; u < KU; ++u) {
+      const float w = __shfl_sync(0xffffffffu, s.w, j0 + u);
+      if (row[u] >= 0) {
+        const F2 ww = f32x2(w, w);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float f[8];
-        unpack8(b[u][v], f);
+        for (int v = 0; v < NV; ++v) {
+          F2 f[4];
+          unpack8(b[u][v], f);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) c[v][q] = fmaf(w[u], f[q], c[v][q]);
+          for (int q = 0; q < 4; ++q) c[v][q] = f32x2_fma(ww, f[q], c[v][q]);
+        }
       }
+    }
   }
 }
 
+template <int NV>
+__device__ __forceinline__ float square_sum(const F2 (&h)[NV][4]) {
+  F2 ss = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) ss = f32x2_fma(h[v][q], h[v][q], ss);
+  return sum2(ss);
+}
+
 // G threads to a token, NV vectors of 8 columns to a thread (vector gt + G v):
-// G * 8 * NV >= H. Blocks hold max(1, 128 / G) tokens.
-template <int G, int NV>
-__global__ void __launch_bounds__(G > 128 ? G : 128) block_kernel(BlockArgs a) {
-  constexpr int kPer = G >= 128 ? 1 : 128 / G;
-  __shared__ float red[2 * 8 * (G / 32)];
+// G * 8 * NV >= H. Blocks hold max(1, 128 / G) tokens. While a token is worked
+// on, L2 is asked for the rows of the next one: without that a block's loads and
+// its sums took turns (306 us for 32768 tokens of 4096 with two rows each, 207
+// with it, 6.2 TB/s).
+template <int G, int NV, int KU, int MB>
+__global__ void __launch_bounds__(G == 32 ? 128 : G, MB) block_kernel(BlockArgs a) {
+  constexpr int kPer = G == 32 ? 4 : 1;
+  __shared__ __align__(16) Scratch<G> red;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, gt = threadIdx.x % G;
+  const int lane = threadIdx.x & 31;
+  const int gt = threadIdx.x % G;
   const int nvec = a.H >> 3;
   const float inv_h = 1.f / static_cast<float>(a.H);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPer;
@@ -181,42 +244,40 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_kernel(BlockArgs a) {
     }
     float gate = 1.f;
     if (a.gate != nullptr) gate = a.gate[t];
-    float h[NV][8];
+    F2 h[NV][4];
     if (gt < 32 && t + step < a.T) {
       if (next.row >= 0) prefetch_row(a.y, next.row, a.H);
       if (lane == 8) prefetch_row(a.residual, t + step, a.H);
     }
+    const F2 scale = f32x2(a.scale, a.scale);
     if (a.y != nullptr) {
       next2 = load_slot(a, t + 2 * step, lane);
-      combine_rows<G, NV>(a, s, gt, nvec, h);
+      combine_rows<G, NV, KU>(a, s, gt, nvec, h);
       float r = gate;
       if (a.post_norm) {
-        float ss[1] = {0.f};
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int q = 0; q < 8; ++q) ss[0] = fmaf(h[v][q], h[v][q], ss[0]);
+        float ss[1] = {square_sum<NV>(h)};
         group_sum<G, 1>(ss, red, turn);
         r *= rsqrtf(fmaf(ss[0], inv_h, a.eps));
       }
+      const F2 rr = f32x2(r, r);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int i = gt + G * v;
         if (i < nvec) {
-          float w[8], f[8];
+          F2 w[4], f[4];
           weight8(a.post_weight, i, w);
           unpack8(res[v], f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) h[v][q] = fmaf(a.scale, f[q], h[v][q] * r * w[q]);
+          for (int q = 0; q < 4; ++q)
+            h[v][q] = f32x2_fma(scale, f[q], f32x2_mul(f32x2_mul(h[v][q], rr), w[q]));
         }
       }
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float f[8];
-        unpack8(res[v], f);
+        unpack8(res[v], h[v]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) h[v][q] = a.scale * f[q];
+        for (int q = 0; q < 4; ++q) h[v][q] = f32x2_mul(scale, h[v][q]);
       }
     }
     if (a.out != nullptr) {
@@ -227,21 +288,18 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_kernel(BlockArgs a) {
       }
     }
     if (a.xn != nullptr) {
-      float ss[1] = {0.f};
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) ss[0] = fmaf(h[v][q], h[v][q], ss[0]);
+      float ss[1] = {square_sum<NV>(h)};
       group_sum<G, 1>(ss, red, turn);
       const float r = rsqrtf(fmaf(ss[0], inv_h, a.eps));
+      const F2 rr = f32x2(r, r);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int i = gt + G * v;
         if (i < nvec) {
-          float w[8], f[8];
+          F2 w[4], f[4];
           weight8(a.pre_weight, i, w);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] = h[v][q] * r * w[q];
+          for (int q = 0; q < 4; ++q) f[q] = f32x2_mul(f32x2_mul(h[v][q], rr), w[q]);
           reinterpret_cast<uint4*>(a.xn)[t * nvec + i] = pack8(f);
         }
       }
@@ -249,183 +307,297 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) block_kernel(BlockArgs a) {
   }
 }
 
-// As block_kernel's layout. Sums over tokens (g_post, g_pre) stay in registers,
-// one column of a thread's each, until the block's last token; the blocks'
-// partial sums [blocks][2][H] are added by column_sum_kernel.
-template <int G, int NV>
-__global__ void __launch_bounds__(G > 128 ? G : 128) block_bwd_kernel(BlockArgs a, BlockGrads g) {
-  constexpr int kPer = G >= 128 ? 1 : 128 / G;
-  __shared__ float red[2 * 8 * (G / 32)];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int lane = threadIdx.x & 31, gt = threadIdx.x % G;
-  const int nvec = a.H >> 3;
+__device__ __forceinline__ void cp_async_16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Layout as block_kernel's. A token's rows (g_out, g_xn, h and, kStageY, its y_j)
+// are copied to shared memory by the threads that will read them, each its own
+// columns: no barrier stands between a copy and its use, and with two stages the
+// next token's rows arrive while this one is worked on. What this needs less of
+// than loads into registers is registers, so that the three sums a token takes
+// (each a barrier) and the second look at y_j wait on shared memory alone.
+// Sums over tokens (g_post, g_pre) stay in registers, one column of a thread's
+// each, until the block's last token; the groups' partial sums [groups][2][H]
+// are added by column_sum_kernel.
+template <int G, int NV, int KMAX, bool kStaged, bool kFull, int MB>
+__global__ void __launch_bounds__(G == 32 ? 128 : G, MB)
+    block_bwd_kernel(BlockArgs a, BlockGrads g, int stages) {
+  constexpr int kPer = G == 32 ? 4 : 1;
+  __shared__ __align__(16) Scratch<G> red;
+  extern __shared__ uint4 dyn[];
+  const int lane = threadIdx.x & 31;
+  const int gt = threadIdx.x % G;
+  const int nvec = kFull ? G * NV : a.H >> 3;
+  const int stage_vecs = (3 + (kStaged ? a.k : 0)) * nvec;
   const float inv_h = 1.f / static_cast<float>(a.H);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPer;
-  int turn = 0;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / G;
-  float s_post[NV][8], s_pre[NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s_post[v][q] = s_pre[v][q] = 0.f;
-  Slot s{-1, 0.f}, next{-1, 0.f}, next2{-1, 0.f};
-  if (a.y != nullptr) {
-    s = load_slot(a, t, lane);
-    next = load_slot(a, t + step, lane);
+  uint4* const ring = dyn + (kStaged ? 4 * nvec : 0) +
+                      static_cast<size_t>(threadIdx.x / G) * stages * stage_vecs;
+  int turn = 0;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  auto weights = [&](bool pre, int i, F2 (&f)[4]) {
+    if constexpr (kStaged) {
+      const ulonglong2* w = reinterpret_cast<const ulonglong2*>(dyn) + (pre ? 2 * nvec : 0) + 2 * i;
+      const ulonglong2 x = w[0], y = w[1];
+      f[0] = x.x;
+      f[1] = x.y;
+      f[2] = y.x;
+      f[3] = y.y;
+    } else {
+      weight8(pre ? a.pre_weight : a.post_weight, i, f);
+    }
+  };
+  if (kStaged) {
+    float* w = reinterpret_cast<float*>(dyn);
+    for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
+      w[i] = a.post_weight != nullptr ? a.post_weight[i] : 1.f;
+      w[a.H + i] = a.pre_weight != nullptr ? a.pre_weight[i] : 1.f;
+    }
+    __syncthreads();
   }
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (; t < a.T; t += step, s = next, next = next2) {
-    uint4 hv[NV], xv[NV], ov[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = gt + G * v;
-      const bool in = i < nvec;
-      ov[v] = in && g.out != nullptr ? ld_global_cs_v4(reinterpret_cast<const uint4*>(g.out) + t * nvec + i) : zero;
-      xv[v] = in && g.xn != nullptr ? ld_global_cs_v4(reinterpret_cast<const uint4*>(g.xn) + t * nvec + i) : zero;
-      hv[v] = in && g.xn != nullptr ? ld_global_cs_v4(reinterpret_cast<const uint4*>(g.h) + t * nvec + i) : zero;
-    }
-    float gate = 1.f;
-    if (a.gate != nullptr) gate = a.gate[t];
-    float c[NV][8];
-    float sums[3] = {0.f, 0.f, 0.f};  // h^2, pre g_xn h, c^2
-    if (gt < 32 && t + step < a.T) {
-      if (next.row >= 0) prefetch_row(a.y, next.row, a.H);
-      if (lane == 8 && g.out != nullptr) prefetch_row(g.out, t + step, a.H);
-      if (lane == 9 && g.xn != nullptr) prefetch_row(g.xn, t + step, a.H);
-      if (lane == 10 && g.xn != nullptr) prefetch_row(g.h, t + step, a.H);
-    }
-    if (a.y != nullptr) {
-      next2 = load_slot(a, t + 2 * step, lane);
-      combine_rows<G, NV>(a, s, gt, nvec, c);
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) sums[2] = fmaf(c[v][q], c[v][q], sums[2]);
-    }
-    if (g.xn != nullptr) {
+  // this thread's columns of token t's rows into a stage, as one group
+  auto fetch = [&](int64_t tok, const Slot& sl, uint4* st) {
+    if (tok < a.T) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int i = gt + G * v;
-        if (i < nvec) {
-          float w[8], h[8], x[8];
-          weight8(a.pre_weight, i, w);
-          unpack8(hv[v], h);
-          unpack8(xv[v], x);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            sums[0] = fmaf(h[q], h[q], sums[0]);
-            sums[1] = fmaf(w[q] * x[q], h[q], sums[1]);
+        if (kFull || i < nvec) {
+          const int64_t at = tok * nvec + i;
+          if (g.out != nullptr) cp_async_16(st + i, reinterpret_cast<const uint4*>(g.out) + at);
+          if (g.xn != nullptr) {
+            cp_async_16(st + nvec + i, reinterpret_cast<const uint4*>(g.xn) + at);
+            cp_async_16(st + 2 * nvec + i, reinterpret_cast<const uint4*>(g.h) + at);
           }
         }
       }
-    }
-    group_sum<G, 3>(sums, red, turn);
-    const float rh = rsqrtf(fmaf(sums[0], inv_h, a.eps));
-    const float rc = a.post_norm ? rsqrtf(fmaf(sums[2], inv_h, a.eps)) : 1.f;
-    const float along = sums[1] * inv_h * rh * rh;  // mean(v h) r_h^2
-    float G8[NV][8];  // G, then g_c
-    float uc[1] = {0.f};  // sum of G post c
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = gt + G * v;
-      unpack8(ov[v], G8[v]);
-      if (i < nvec) {
-        if (g.xn != nullptr) {
-          float w[8], h[8], x[8];
-          weight8(a.pre_weight, i, w);
-          unpack8(hv[v], h);
-          unpack8(xv[v], x);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            G8[v][q] = fmaf(rh, fmaf(-h[q], along, w[q] * x[q]), G8[v][q]);
-            s_pre[v][q] = fmaf(x[q] * rh, h[q], s_pre[v][q]);
-          }
-        }
-        if (g.residual != nullptr) {
-          float f[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] = a.scale * G8[v][q];
-          st_global_cs_v4(reinterpret_cast<uint4*>(g.residual) + t * nvec + i, pack8(f));
-        }
+      if constexpr (kStaged) {
         if (a.y != nullptr) {
-          float w[8];
-          weight8(a.post_weight, i, w);
-          const float gr = gate * rc;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            s_post[v][q] = fmaf(gr * G8[v][q], c[v][q], s_post[v][q]);
-            G8[v][q] *= w[q];
-            uc[0] = fmaf(G8[v][q], c[v][q], uc[0]);
-          }
-        }
-      }
-    }
-    if (a.y == nullptr) continue;
-    const bool need_uc = a.post_norm || g.gate != nullptr;
-    if (need_uc) group_sum<G, 1>(uc, red, turn);
-    if (g.gate != nullptr && gt == 0) g.gate[t] = uc[0] * rc;
-    const float back = a.post_norm ? uc[0] * inv_h * rc * rc : 0.f;
-    const float gr = gate * rc;
+          for (int j = 0; j < KMAX; ++j) {
+            const int row = __shfl_sync(0xffffffffu, sl.row, j);  // lanes from k up hold none
+            if (row >= 0) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) G8[v][q] = gr * fmaf(-c[v][q], back, G8[v][q]);
-    float dots[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dots[j] = 0.f;
-      if (j < a.k) {
-        const int row = __shfl_sync(0xffffffffu, s.row, j);
-        const float w = __shfl_sync(0xffffffffu, s.w, j);
-        if (row >= 0) {
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int i = gt + G * v;
-            if (i < nvec) {
-              const size_t at = static_cast<size_t>(row) * nvec + i;
-              if (g.w != nullptr) {
-                float f[8];
-                unpack8(__ldg(reinterpret_cast<const uint4*>(a.y) + at), f);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) dots[j] = fmaf(G8[v][q], f[q], dots[j]);
-              }
-              if (g.y != nullptr) {
-                float f[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) f[q] = w * G8[v][q];
-                st_global_cs_v4(reinterpret_cast<uint4*>(g.y) + at, pack8(f));
+              for (int v = 0; v < NV; ++v) {
+                const int i = gt + G * v;
+                if (kFull || i < nvec)
+                  cp_async_16(st + (3 + j) * nvec + i, reinterpret_cast<const uint4*>(a.y) +
+                                                           static_cast<size_t>(row) * nvec + i);
               }
             }
           }
         }
       }
     }
-    if (g.w != nullptr) {
-      if (a.k <= 2) {
-        float d[2] = {dots[0], dots[1]};
-        group_sum<G, 2>(d, red, turn);
-        if (gt < a.k) g.w[t * a.k + gt] = gt == 0 ? d[0] : d[1];
-      } else {
-        group_sum<G, 8>(dots, red, turn);
+    cp_async_commit();
+  };
+  F2 s_post[NV][4], s_pre[NV][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < a.k && gt == j) g.w[t * a.k + j] = dots[j];
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s_post[v][q] = s_pre[v][q] = 0;
+  Slot s{-1, 0.f}, next{-1, 0.f}, next2{-1, 0.f};
+  if (a.y != nullptr) {
+    s = load_slot(a, t, lane);
+    next = load_slot(a, t + step, lane);
+  }
+  fetch(t, s, ring);
+  int cur = 0;
+  for (; t < a.T; t += step, s = next, next = next2, cur = stages - 1 - cur) {
+    const uint4* st = ring + cur * stage_vecs;
+    float gate = 1.f;
+    if (a.gate != nullptr) gate = a.gate[t];
+    if (a.y != nullptr) next2 = load_slot(a, t + 2 * step, lane);
+    if (stages == 2) {
+      fetch(t + step, next, ring + (1 - cur) * stage_vecs);
+      cp_async_wait<1>();
+    } else {
+      if (gt < 32 && t + step < a.T) {  // the next token's rows as far as L2
+        if (next.row >= 0) prefetch_row(a.y, next.row, a.H);
+        if (lane == 8 && g.out != nullptr) prefetch_row(g.out, t + step, a.H);
+        if (lane == 9 && g.xn != nullptr) prefetch_row(g.xn, t + step, a.H);
+        if (lane == 10 && g.xn != nullptr) prefetch_row(g.h, t + step, a.H);
+      }
+      cp_async_wait<0>();
+    }
+    // vector i of the token's row j of y
+    auto y_vec = [&](int j, int row, int i) {
+      return kStaged ? st[(3 + j) * nvec + i]
+                     : __ldg(reinterpret_cast<const uint4*>(a.y) + static_cast<size_t>(row) * nvec + i);
+    };
+    F2 c[NV][4];
+    float sums[3] = {0.f, 0.f, 0.f};  // h^2, pre g_xn h, c^2
+    if (a.y != nullptr) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[v][q] = 0;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        const int row = __shfl_sync(0xffffffffu, s.row, j);
+        const float w = __shfl_sync(0xffffffffu, s.w, j);
+        if (row >= 0) {
+          const F2 ww = f32x2(w, w);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int i = gt + G * v;
+            if (kFull || i < nvec) {
+              F2 f[4];
+              unpack8(y_vec(j, row, i), f);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) c[v][q] = f32x2_fma(ww, f[q], c[v][q]);
+            }
+          }
+        }
+      }
+      sums[2] = square_sum<NV>(c);
+    }
+    if (g.xn != nullptr) {
+      F2 hh = 0, vh = 0;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int i = gt + G * v;
+        if (kFull || i < nvec) {
+          F2 w[4], h[4], x[4];
+          weights(true, i, w);
+          unpack8(st[nvec + i], x);
+          unpack8(st[2 * nvec + i], h);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            hh = f32x2_fma(h[q], h[q], hh);
+            vh = f32x2_fma(f32x2_mul(w[q], x[q]), h[q], vh);
+          }
+        }
+      }
+      sums[0] = sum2(hh);
+      sums[1] = sum2(vh);
+    }
+    group_sum<G, 3>(sums, red, turn);
+    const float rh = rsqrtf(fmaf(sums[0], inv_h, a.eps));
+    const float rc = a.post_norm ? rsqrtf(fmaf(sums[2], inv_h, a.eps)) : 1.f;
+    const float along = -sums[1] * inv_h * rh * rh;  // -mean(v h) r_h^2
+    const float gr = gate * rc;
+    const F2 rh2 = f32x2(rh, rh), along2 = f32x2(along, along), gr2 = f32x2(gr, gr);
+    const F2 scale = f32x2(a.scale, a.scale);
+    F2 G8[NV][4];  // G, then G post, then g_c
+    F2 uc2 = 0;    // sum of G post c
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = gt + G * v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) G8[v][q] = 0;
+      if (kFull || i < nvec) {
+        if (g.out != nullptr) unpack8(st[i], G8[v]);
+        if (g.xn != nullptr) {
+          F2 w[4], h[4], x[4];
+          weights(true, i, w);
+          unpack8(st[nvec + i], x);
+          unpack8(st[2 * nvec + i], h);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const F2 d = f32x2_fma(h[q], along2, f32x2_mul(w[q], x[q]));
+            G8[v][q] = f32x2_fma(rh2, d, G8[v][q]);
+            s_pre[v][q] = f32x2_fma(f32x2_mul(x[q], rh2), h[q], s_pre[v][q]);
+          }
+        }
+        if (g.residual != nullptr) {
+          F2 f[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) f[q] = f32x2_mul(scale, G8[v][q]);
+          st_global_cs_v4(reinterpret_cast<uint4*>(g.residual) + t * nvec + i, pack8(f));
+        }
+        if (a.y != nullptr) {
+          F2 w[4];
+          weights(false, i, w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            s_post[v][q] = f32x2_fma(f32x2_mul(gr2, G8[v][q]), c[v][q], s_post[v][q]);
+            G8[v][q] = f32x2_mul(G8[v][q], w[q]);
+            uc2 = f32x2_fma(G8[v][q], c[v][q], uc2);
+          }
+        }
       }
     }
+    if (a.y != nullptr) {
+      float uc[1] = {sum2(uc2)};
+      if (a.post_norm || g.gate != nullptr) group_sum<G, 1>(uc, red, turn);
+      if (g.gate != nullptr && gt == 0) g.gate[t] = uc[0] * rc;
+      const float back = a.post_norm ? -uc[0] * inv_h * rc * rc : 0.f;
+      const F2 back2 = f32x2(back, back);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          G8[v][q] = f32x2_mul(gr2, f32x2_fma(c[v][q], back2, G8[v][q]));
+      float dots[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dots[j] = 0.f;
+        if (j < KMAX) {
+          const int row = __shfl_sync(0xffffffffu, s.row, j);
+          const float w = __shfl_sync(0xffffffffu, s.w, j);
+          if (row >= 0) {
+            const F2 ww = f32x2(w, w);
+            F2 d = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const int i = gt + G * v;
+              if (kFull || i < nvec) {
+                if (g.w != nullptr) {
+                  F2 f[4];
+                  unpack8(y_vec(j, row, i), f);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) d = f32x2_fma(G8[v][q], f[q], d);
+                }
+                if (g.y != nullptr) {
+                  F2 f[4];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) f[q] = f32x2_mul(ww, G8[v][q]);
+                  st_global_cs_v4(reinterpret_cast<uint4*>(g.y) + static_cast<size_t>(row) * nvec + i,
+                                  pack8(f));
+                }
+              }
+            }
+            dots[j] = sum2(d);
+          }
+        }
+      }
+      if (g.w != nullptr) {
+        float d;
+        if constexpr (KMAX <= 2) {
+          float two[2] = {dots[0], dots[1]};
+          group_sum<G, 2>(two, red, turn);
+          d = gt == 0 ? two[0] : two[1];
+        } else {
+          d = group_sum8<G>(dots, red, turn);
+        }
+        if (gt < a.k) g.w[t * a.k + gt] = d;
+      }
+    }
+    // one stage: this thread has read all its columns of it
+    if (stages == 1) fetch(t + step, next, ring);
   }
+  cp_async_wait<0>();
   if (g.partial == nullptr) return;
   float* mine = g.partial + (static_cast<size_t>(blockIdx.x) * kPer + threadIdx.x / G) * 2 * a.H;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int i = gt + G * v;
-    if (i < nvec) {
-      float4* d = reinterpret_cast<float4*>(mine) + 2 * i;
-      d[0] = make_float4(s_post[v][0], s_post[v][1], s_post[v][2], s_post[v][3]);
-      d[1] = make_float4(s_post[v][4], s_post[v][5], s_post[v][6], s_post[v][7]);
-      d = reinterpret_cast<float4*>(mine + a.H) + 2 * i;
-      d[0] = make_float4(s_pre[v][0], s_pre[v][1], s_pre[v][2], s_pre[v][3]);
-      d[1] = make_float4(s_pre[v][4], s_pre[v][5], s_pre[v][6], s_pre[v][7]);
+    if (kFull || i < nvec) {
+      ulonglong2* d = reinterpret_cast<ulonglong2*>(mine) + 2 * i;
+      d[0] = make_ulonglong2(s_post[v][0], s_post[v][1]);
+      d[1] = make_ulonglong2(s_post[v][2], s_post[v][3]);
+      d = reinterpret_cast<ulonglong2*>(mine + a.H) + 2 * i;
+      d[0] = make_ulonglong2(s_pre[v][0], s_pre[v][1]);
+      d[1] = make_ulonglong2(s_pre[v][2], s_pre[v][3]);
     }
   }
 }
@@ -452,54 +624,101 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
   }
 }
 
-template <int G, int NV>
+// Blocks: no more than stay resident (MB to an SM), so that every SM has its share
+// of the tokens in one round.
+template <int G, int NV, int KU, int MB>
 cudaError_t launch_fwd(const BlockArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int kPer = G >= 128 ? 1 : 128 / G;
+  constexpr int kPer = G == 32 ? 4 : 1;
   const int64_t need = (a.T + kPer - 1) / kPer;
-  const int cap = num_sms * (G > 128 ? 2048 / G : 16);
-  return launch_pdl(block_kernel<G, NV>, dim3(static_cast<unsigned>(need < cap ? need : cap)),
-                    dim3(G > 128 ? G : 128), 0, st, a);
+  const int64_t cap = static_cast<int64_t>(num_sms) * MB;
+  return launch_pdl(block_kernel<G, NV, KU, MB>, dim3(static_cast<unsigned>(need < cap ? need : cap)),
+                    dim3(G == 32 ? 128 : G), 0, st, a);
 }
 
-template <int G, int NV>
-cudaError_t launch_bwd(const BlockArgs& a, const BlockGrads& g, int blocks, cudaStream_t st) {
-  return launch_pdl(block_bwd_kernel<G, NV>, dim3(blocks), dim3(G > 128 ? G : 128), 0, st, a, g);
+constexpr int kSmSharedBytes = 228 * 1024;  // of an SM; 1 KB less for a block
+
+template <int G, int NV, int KMAX, bool kStaged, bool kFull, int MB>
+cudaError_t launch_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st,
+                       int* groups) {
+  constexpr int kPer = G == 32 ? 4 : 1;
+  constexpr int kFixed = sizeof(Scratch<G>) + 1024;  // and what the system keeps of a block
+  const int stage = (3 + (kStaged ? a.k : 0)) * a.H * 2 * kPer;
+  const int weights = kStaged ? 8 * a.H : 0;
+  const int stages = 2 * stage + weights + kFixed <= kSmSharedBytes ? 2 : 1;
+  const int dyn = stages * stage + weights;
+  int per_sm = MB;
+  if (kSmSharedBytes / (dyn + kFixed) < per_sm) per_sm = kSmSharedBytes / (dyn + kFixed);
+  const auto kernel = block_bwd_kernel<G, NV, KMAX, kStaged, kFull, MB>;
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+  if (err != cudaSuccess) return err;
+  const int64_t need = (a.T + kPer - 1) / kPer, cap = static_cast<int64_t>(num_sms) * per_sm;
+  int blocks = static_cast<int>(need < cap ? need : cap);
+  if (blocks * kPer > kBlockMaxGroups) blocks = kBlockMaxGroups / kPer;
+  *groups = blocks * kPer;
+  return launch_pdl(kernel, dim3(blocks), dim3(G == 32 ? 128 : G), dyn, st, a, g, stages);
 }
 
-// Threads of a token's group by width.
-int group_threads(int H) { return H <= 1024 ? 32 : H <= 2048 ? 128 : H <= 8192 ? 256 : 512; }
+// Whether a token's rows and the weights fit beside the block's other memory.
+bool bwd_fits(int H, int k) {
+  return (3 + k) * H * 2 + 8 * H + static_cast<int>(sizeof(Scratch<512>)) + 1024 <= kSmSharedBytes;
+}
+
+template <int G, int NV, int KMAX, int MB>
+cudaError_t launch_bwd_k(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st,
+                         int* groups) {
+  if constexpr (G == 32) {
+    return launch_bwd<G, NV, KMAX, true, false, MB>(a, g, num_sms, st, groups);
+  } else {
+    if (!bwd_fits(a.H, a.k)) return launch_bwd<G, NV, 8, false, false, MB>(a, g, num_sms, st, groups);
+    if (a.H == 8 * G * NV) return launch_bwd<G, NV, KMAX, true, true, MB>(a, g, num_sms, st, groups);
+    return launch_bwd<G, NV, KMAX, true, false, MB>(a, g, num_sms, st, groups);
+  }
+}
+
+template <int G, int NV, int MB>
+cudaError_t launch_bwd_any(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st,
+                           int* groups) {
+  if (a.k <= 2) return launch_bwd_k<G, NV, 2, MB>(a, g, num_sms, st, groups);
+  if (a.k <= 4) return launch_bwd_k<G, NV, 4, MB>(a, g, num_sms, st, groups);
+  return launch_bwd_k<G, NV, 8, MB>(a, g, num_sms, st, groups);
+}
 
 }  // namespace
 
-// Partial rows of the gradient: up to kBlockMaxGroups, a multiple of a block's
-// groups.
+// Partial rows of the gradient at most: one per token (or per four, rounded up
+// to four), and kBlockMaxGroups.
 int block_bwd_groups(int64_t T, int H) {
-  const int per = group_threads(H) == 32 ? 4 : 1;
-  const int64_t groups = (T + per - 1) / per * per;
+  const int64_t groups = H <= 512 ? (T + 3) / 4 * 4 : T;
   return static_cast<int>(groups < kBlockMaxGroups ? groups : kBlockMaxGroups);
 }
 
 cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st) {
-  if (a.H <= 256) return launch_fwd<32, 1>(a, num_sms, st);
-  if (a.H <= 512) return launch_fwd<32, 2>(a, num_sms, st);
-  if (a.H <= 1024) return launch_fwd<32, 4>(a, num_sms, st);
-  if (a.H <= 2048) return launch_fwd<128, 2>(a, num_sms, st);
-  if (a.H <= 4096) return launch_fwd<256, 2>(a, num_sms, st);
-  if (a.H <= 8192) return launch_fwd<256, 4>(a, num_sms, st);
-  return launch_fwd<512, 4>(a, num_sms, st);
+  const bool few = a.k <= 2;
+  if (a.H <= 256) return launch_fwd<32, 1, 4, 8>(a, num_sms, st);
+  if (a.H <= 512) return launch_fwd<32, 2, 4, 4>(a, num_sms, st);
+  if (a.H <= 1024)
+    return few ? launch_fwd<128, 1, 2, 8>(a, num_sms, st) : launch_fwd<128, 1, 4, 8>(a, num_sms, st);
+  if (a.H <= 2048)
+    return few ? launch_fwd<256, 1, 2, 4>(a, num_sms, st) : launch_fwd<256, 1, 4, 4>(a, num_sms, st);
+  if (a.H <= 4096)
+    return few ? launch_fwd<256, 2, 2, 3>(a, num_sms, st) : launch_fwd<256, 2, 4, 2>(a, num_sms, st);
+  if (a.H <= 8192)
+    return few ? launch_fwd<256, 4, 2, 2>(a, num_sms, st) : launch_fwd<512, 2, 4, 1>(a, num_sms, st);
+  return launch_fwd<512, 4, 2, 1>(a, num_sms, st);
 }
 
-cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, cudaStream_t st) {
-  const int groups = block_bwd_groups(a.T, a.H);
-  const int blocks = group_threads(a.H) == 32 ? groups / 4 : groups;
+cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st) {
+  int groups = 0;
   cudaError_t err;
-  if (a.H <= 256) err = launch_bwd<32, 1>(a, g, blocks, st);
-  else if (a.H <= 512) err = launch_bwd<32, 2>(a, g, blocks, st);
-  else if (a.H <= 1024) err = launch_bwd<32, 4>(a, g, blocks, st);
-  else if (a.H <= 2048) err = launch_bwd<128, 2>(a, g, blocks, st);
-  else if (a.H <= 4096) err = launch_bwd<256, 2>(a, g, blocks, st);
-  else if (a.H <= 8192) err = launch_bwd<256, 4>(a, g, blocks, st);
-  else err = launch_bwd<512, 4>(a, g, blocks, st);
+  if (a.H <= 256) err = launch_bwd_any<32, 1, 4>(a, g, num_sms, st, &groups);
+  else if (a.H <= 512) err = launch_bwd_any<32, 2, 3>(a, g, num_sms, st, &groups);
+  else if (a.H <= 1024) err = launch_bwd_any<128, 1, 6>(a, g, num_sms, st, &groups);
+  else if (a.H <= 2048) err = launch_bwd_any<256, 1, 3>(a, g, num_sms, st, &groups);
+  else if (a.H <= 4096) err = launch_bwd_any<256, 2, 2>(a, g, num_sms, st, &groups);
+  else if (a.H <= 6144) err = launch_bwd_any<384, 2, 1>(a, g, num_sms, st, &groups);
+  else if (a.H <= 8192) err = launch_bwd_any<512, 2, 1>(a, g, num_sms, st, &groups);
+  else err = launch_bwd<1024, 2, 8, false, false, 1>(a, g, num_sms, st, &groups);
   if (err != cudaSuccess || g.partial == nullptr) return err;
   return launch_pdl(column_sum_kernel, dim3(a.H / 16), dim3(256), 0, st,
                     static_cast<const float*>(g.partial), groups, a.H, g.post, g.pre);

@@ -132,7 +132,7 @@ struct GroupedBwdArgs {
 
 // The step between two blocks and its gradient (csrc/moe_block.cu).
 constexpr int kBlockMaxWidth = 16384;
-constexpr int kBlockMaxGroups = 1216;  // partial rows of the gradient's sums over tokens
+constexpr int kBlockMaxGroups = 2432;  // partial rows of the gradient's sums over tokens
 struct BlockArgs {
   int64_t T;
   int H, rows, k;             // width; rows of y; slots per token
@@ -308,7 +308,7 @@ cudaError_t launch_wgrad(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const
                          const WgradArgs& a, int num_sms, cudaStream_t st);
 int block_bwd_groups(int64_t T, int H);
 cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st);
-cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, cudaStream_t st);
+cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st);
 size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage);
 // FP8 operands; writes D (bf16), or Dq + d_scale when a.Dq is set
 cudaError_t launch_grouped_gemm_pair_fp8(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
