@@ -644,10 +644,13 @@ cudaError_t launch_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cud
   constexpr int kFixed = sizeof(Scratch<G>) + 1024;  // and what the system keeps of a block
   const int stage = (3 + (kStaged ? a.k : 0)) * a.H * 2 * kPer;
   const int weights = kStaged ? 8 * a.H : 0;
-  const int stages = 2 * stage + weights + kFixed <= kSmSharedBytes ? 2 : 1;
+  const auto resident = [&](int stages) {
+    const int n = kSmSharedBytes / (stages * stage + weights + kFixed);
+    return n < MB ? n : MB;
+  };
+  const int stages = resident(2) == 0 || 2 * resident(2) <= resident(1) ? 1 : 2;
   const int dyn = stages * stage + weights;
-  int per_sm = MB;
-  if (kSmSharedBytes / (dyn + kFixed) < per_sm) per_sm = kSmSharedBytes / (dyn + kFixed);
+  const int per_sm = resident(stages);
   const auto kernel = block_bwd_kernel<G, NV, KMAX, kStaged, kFull, MB>;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
