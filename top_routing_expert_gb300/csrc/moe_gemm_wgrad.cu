@@ -78,6 +78,31 @@ __device__ __forceinline__ bool is_tail(int len, int kb) {
   return left < kDepth && (left & 15) != 0;
 }
 
+// Issues a stage's K steps of 16 rows and releases it. One 128-byte row per k: a
+// step is 2 KB on in both operands (128 in a descriptor); the blocks of 64
+// columns are 16 KB apart, g's behind x's. Called by the whole warp, straight on
+// for a full stage, so that an elected lane keeps the tensor core's queue filled
+// (a lane that issued alone in a diverged warp, its descriptors built on the way,
+// took 185 clocks per UMMA of 128: 852 us instead of 689 for 128 experts).
+__device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint64_t xd, uint32_t idesc, bool add,
+                                            int steps, uint64_t* release, uint64_t* done) {
+  constexpr uint64_t kG = kOpBytes >> 4;
+  if (elect_one()) {
+    umma_bf16_pair(d_tmem, xd, xd + kG, idesc, add ? 1u : 0u);
+    if (steps == kDepth / 16) {
+#pragma unroll
+      for (uint32_t k = 1; k < kDepth / 16; ++k)
+        umma_bf16_pair(d_tmem, xd + 128u * k, xd + kG + 128u * k, idesc, 1u);
+    } else {
+      for (uint32_t k = 1; k < static_cast<uint32_t>(steps); ++k)
+        umma_bf16_pair(d_tmem, xd + 128u * k, xd + kG + 128u * k, idesc, 1u);
+    }
+    umma_commit_pair_multicast(release, 0x3);
+    if (done != nullptr) umma_commit_pair_multicast(done, 0x3);
+  }
+  __syncwarp();
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_g,
                  const __grid_constant__ CUtensorMap tm_d, WgradArgs p) {
@@ -249,70 +274,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------------------- UMMA issuer (leader) ----
+      // the whole warp walks, an elected lane issues
       int stage = 0;
       uint32_t full_par = 0, tail_par = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool aborted = false;
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), kBlockBytes, 1024u);
       for (int L = cluster; L < total && !aborted; L += n_clusters) {
         const WgTile c = decode_wg(L, offs, order, mt, nt);
-        if (c.len == 0) continue;
         const uint32_t idesc = idesc_bf16_f32(kTile, p.N - c.n0 <= kTile / 2 ? kTile / 2 : kTile,
                                               true, true);
         const int nk = (c.len + kDepth - 1) / kDepth;
         for (int kb = 0; kb < nk; ++kb) {
           const int in_piece = kb % kPiece;
-          if (in_piece == 0) {
-            if (!pair_wait(&tempty[acc], acc_phase ^ 1u)) {
-              aborted = true;
-              break;
+          bool ok = true;
+          if (in_piece == 0) ok = pair_wait(&tempty[acc], acc_phase ^ 1u);
+          if (ok) {
+            if (is_tail(c.len, kb)) {
+              ok = mbar_wait<true>(&tail_ok[stage], tail_par >> stage & 1u, wc);
+              if (!ok) st_u32_cluster(peer_abort, 1u);
+              tail_par ^= 1u << stage;
+            } else {
+              ok = pair_wait(&full[stage], full_par >> stage & 1u);
+              full_par ^= 1u << stage;
             }
-            tc_fence_after();
           }
-          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
-          const uint32_t bit = 1u << stage;
-          bool ok;
-          if (is_tail(c.len, kb)) {
-            ok = mbar_wait<true>(&tail_ok[stage], tail_par >> stage & 1u, wc);
-            if (!ok) st_u32_cluster(peer_abort, 1u);
-            tail_par ^= bit;
-          } else {
-            ok = pair_wait(&full[stage], full_par >> stage & 1u);
-            full_par ^= bit;
-          }
-          if (!ok) {
+          if (!__all_sync(0xffffffffu, ok)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t x_addr = smem_u32(smem + stage * kStageBytes);
-          const uint32_t g_addr = x_addr + kOpBytes;
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
+          const uint64_t xd = desc0 + ((stage * kStageBytes) >> 4);
           const int steps = min(kDepth / 16, (c.len - kb * kDepth + 15) / 16);
-#pragma unroll
-          for (int kk = 0; kk < kDepth / 16; ++kk) {
-            if (kk < steps) {
-              // one 128-byte row per k: a 16-row K step is 2 KB; blocks of 64
-              // columns are 16 KB apart
-              const uint64_t xd = smem_desc_sw128(x_addr + 2048u * kk, kBlockBytes, 1024u);
-              const uint64_t gd = smem_desc_sw128(g_addr + 2048u * kk, kBlockBytes, 1024u);
-              umma_bf16_pair(d_tmem, xd, gd, idesc, (in_piece | kk) != 0 ? 1u : 0u);
-            }
-          }
-          umma_commit_pair_multicast(&empty[stage], 0x3);
+          const bool piece_end = in_piece == kPiece - 1 || kb == nk - 1;
+          issue_stage(d_tmem, xd, idesc, in_piece != 0, steps, &empty[stage],
+                      piece_end ? &tfull[acc] : nullptr);
           if (++stage == kStages) stage = 0;
-          if (in_piece == kPiece - 1 || kb == nk - 1) {
-            umma_commit_pair_multicast(&tfull[acc], 0x3);
-            if (++acc == 2) {
-              acc = 0;
-              acc_phase ^= 1u;
-            }
+          if (piece_end && ++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
           }
         }
       }
       // every UMMA issued must finish before TMEM is released
-      umma_commit_pair(drain);
+      if (elect_one()) umma_commit_pair(drain);
+      __syncwarp();
       mbar_wait_drain(drain, 0, kDrainLimitNs);
     }
   } else if (warp < kFirstEpi) {
