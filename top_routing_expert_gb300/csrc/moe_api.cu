@@ -1627,8 +1627,8 @@ moe_status moe_expert_wgrad(int64_t E, int64_t rows, int64_t K, int64_t N, const
   MOE_REQUIRE(offsets);
   MOE_REQUIRE(dev_status);
   CUtensorMap tm_x, tm_g, tm_d;
-  if (!tmap_bf16_kblocks(&tm_x, x, K, rows, 128, 2)) return MOE_ERR_CUDA;
-  if (!tmap_bf16_kblocks(&tm_g, g, N, rows, 128, 2)) return MOE_ERR_CUDA;
+  if (!tmap_bf16_kblocks(&tm_x, x, K, rows, 64, 2)) return MOE_ERR_CUDA;
+  if (!tmap_bf16_kblocks(&tm_g, g, N, rows, 64, 2)) return MOE_ERR_CUDA;
   if (!tmap_wgrad_out(&tm_d, dW, N, K, E, dtype == MOE_DTYPE_BF16)) return MOE_ERR_CUDA;
   WgradArgs a;
   a.offsets = offsets;

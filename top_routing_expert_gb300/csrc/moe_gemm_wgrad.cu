@@ -35,8 +35,8 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 256;          // rows and columns of dW per pair
-constexpr int kDepth = 128;         // rows of x and g per stage
-constexpr int kStages = 3;
+constexpr int kDepth = 64;          // rows of x and g per stage
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpi = 3;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
@@ -50,7 +50,7 @@ constexpr int kGroup = 8;           // m-tiles per raster group
 // fp32 additions cut towards zero, a bias of about 2^-25 of the sum each, which
 // adds up over a long segment: 9e-6 of the result after 8192 rows. The epilogue
 // adds the pieces with rounding.
-constexpr int kPiece = 4;
+constexpr int kPiece = 8;
 
 struct WgTile {
   int lo, len, m0, n0, e;
