@@ -72,6 +72,37 @@ __device__ __forceinline__ WgTile decode_wg(int L, const int* offs, const uint8_
   return t;
 }
 
+// A warp's walk over its pair's tiles. Each lane decodes one of the next 32 (the
+// divisions would otherwise stand between every two tiles of the issuer); called
+// by the whole warp.
+struct TileWalk {
+  const int* offs;
+  const uint8_t* order;
+  int mt, nt, total, stride, L, at;
+  WgTile mine;
+
+  __device__ __forceinline__ TileWalk(const int* offs_, const uint8_t* order_, int mt_, int nt_,
+                                      int total_, int first, int stride_)
+      : offs(offs_), order(order_), mt(mt_), nt(nt_), total(total_), stride(stride_), L(first), at(32) {}
+
+  __device__ __forceinline__ bool next(WgTile& t) {
+    if (L >= total) return false;
+    if (at == 32) {
+      const int l = min(L + static_cast<int>(threadIdx.x & 31) * stride, total - 1);
+      mine = decode_wg(l, offs, order, mt, nt);
+      at = 0;
+    }
+    t.lo = __shfl_sync(0xffffffffu, mine.lo, at);
+    t.len = __shfl_sync(0xffffffffu, mine.len, at);
+    t.m0 = __shfl_sync(0xffffffffu, mine.m0, at);
+    t.n0 = __shfl_sync(0xffffffffu, mine.n0, at);
+    t.e = __shfl_sync(0xffffffffu, mine.e, at);
+    ++at;
+    L += stride;
+    return true;
+  }
+};
+
 // Whether stage kb of a segment of len rows has a K step with rows behind it.
 __device__ __forceinline__ bool is_tail(int len, int kb) {
   const int left = len - kb * kDepth;
@@ -83,7 +114,7 @@ __device__ __forceinline__ bool is_tail(int len, int kb) {
 // columns are 16 KB apart, g's behind x's. Called by the whole warp, straight on
 // for a full stage, so that an elected lane keeps the tensor core's queue filled
 // (a lane that issued alone in a diverged warp, its descriptors built on the way,
-// took 185 clocks per UMMA of 128: 852 us instead of 689 for 128 experts).
+// took 185 clocks per UMMA of 128: 852 us instead of 788 for 128 experts).
 __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint64_t xd, uint32_t idesc, bool add,
                                             int steps, uint64_t* release, uint64_t* done) {
   constexpr uint64_t kG = kOpBytes >> 4;
@@ -189,8 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
+  TileWalk tiles(offs, order, mt, nt, total, cluster, n_clusters);
+  WgTile c;
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------ TMA producer ----
       int stage = 0;
       uint32_t phase = 0;
@@ -199,34 +232,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t full_par = 0, tail_par = 0, was_tail = 0;
       int issued = 0;
       bool aborted = false;
-      for (int L = cluster; L < total && !aborted; L += n_clusters) {
-        const WgTile c = decode_wg(L, offs, order, mt, nt);
+      while (!aborted && tiles.next(c)) {
         const int nk = (c.len + kDepth - 1) / kDepth;
         const bool half_n = p.N - c.n0 <= kTile / 2;
         const int xb = (c.m0 + static_cast<int>(rank) * (kTile / 2)) / 64;
         const int gb = (c.n0 + static_cast<int>(rank) * (half_n ? kTile / 4 : kTile / 2)) / 64;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!pair_wait(&empty[stage], phase ^ 1u)) {
+          if (!__all_sync(0xffffffffu, pair_wait(&empty[stage], phase ^ 1u))) {
             aborted = true;
             break;
           }
           const uint32_t bit = 1u << stage;
-          uint32_t bar;
-          if (is_tail(c.len, kb)) {
-            mbar_arrive_expect_tx(&tail_ld[stage], kStageBytes);
-            bar = mapa_shared(smem_u32(&tail_ld[stage]), rank);
+          const bool tail = is_tail(c.len, kb);
+          if (tail) {
             tail_par ^= bit;
             was_tail |= bit;
           } else {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
-            bar = mapa_shared(smem_u32(&full[stage]), 0);
             full_par ^= bit;
             was_tail &= ~bit;
           }
-          uint8_t* sx = smem + stage * kStageBytes;
-          const int row = c.lo + kb * kDepth;
-          tma_load_3d_pair(sx, &tm_x, bar, 0, row, xb);
-          tma_load_3d_pair(sx + kOpBytes, &tm_g, bar, 0, row, gb);
+          if (elect_one()) {
+            uint32_t bar;
+            if (tail) {
+              mbar_arrive_expect_tx(&tail_ld[stage], kStageBytes);
+              bar = mapa_shared(smem_u32(&tail_ld[stage]), rank);
+            } else {
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+              bar = mapa_shared(smem_u32(&full[stage]), 0);
+            }
+            uint8_t* sx = smem + stage * kStageBytes;
+            const int row = c.lo + kb * kDepth;
+            tma_load_3d_pair(sx, &tm_x, bar, 0, row, xb);
+            tma_load_3d_pair(sx + kOpBytes, &tm_g, bar, 0, row, gb);
+          }
+          __syncwarp();
           ++issued;
           if (++stage == kStages) {
             stage = 0;
@@ -242,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // waits. (Both walk the same tiles, so stage i is of one kind in both;
       // where the leader never reached it, waiting for a tail as for another
       // stage only runs into the limit.)
-      if (!leader) {
+      if (lane != 0) {
+        // lane 0 does the rest
+      } else if (!leader) {
         st_async_u32_cluster(mapa_shared(smem_u32(peer_issued), 0), static_cast<uint32_t>(issued),
                              mapa_shared(smem_u32(xbar), 0));
         for (int i = max(0, issued - kStages); i < issued; ++i) {
@@ -283,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t acc_phase = 0;
       bool aborted = false;
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), kBlockBytes, 1024u);
-      for (int L = cluster; L < total && !aborted; L += n_clusters) {
-        const WgTile c = decode_wg(L, offs, order, mt, nt);
+      while (!aborted && tiles.next(c)) {
         const uint32_t idesc = idesc_bf16_f32(kTile, p.N - c.n0 <= kTile / 2 ? kTile / 2 : kTile,
                                               true, true);
         const int nk = (c.len + kDepth - 1) / kDepth;
@@ -332,14 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t tail_par = 0;
     bool aborted = false;
-    for (int L = cluster; L < total && !aborted; L += n_clusters) {
-      const WgTile c = decode_wg(L, offs, order, mt, nt);
+    while (!aborted && tiles.next(c)) {
       const int nk = (c.len + kDepth - 1) / kDepth;
       if (nk == 0) continue;
       const int s = (stage + nk - 1) % kStages;
       stage = (stage + nk) % kStages;
       if (!is_tail(c.len, nk - 1)) continue;
-      if (!pair_wait(&tail_ld[s], tail_par >> s & 1u)) {
+      if (!__all_sync(0xffffffffu, pair_wait(&tail_ld[s], tail_par >> s & 1u))) {
         aborted = true;
         break;
       }
@@ -368,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool aborted = false;
-    for (int L = cluster; L < total && !aborted; L += n_clusters) {
-      const WgTile c = decode_wg(L, offs, order, mt, nt);
+    while (!aborted && tiles.next(c)) {
       if (c.len == 0 && p.accumulate) continue;
       const int row = c.m0 + static_cast<int>(rank) * (kTile / 2) + 32 * q;
       const int col0 = c.n0 + half * (kTile / 2);
@@ -379,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
       for (int left = c.len; left > 0; left -= kPiece * kDepth) {
-        if (!pair_wait(&tfull[acc], acc_phase)) {
+        if (!__all_sync(0xffffffffu, pair_wait(&tfull[acc], acc_phase))) {
           aborted = true;
           break;
         }
