@@ -20,7 +20,9 @@
 //
 // Roles per CTA (320 threads): warp 0 = TMA producer (both CTAs, own halves,
 // transaction bytes counted on the leader's barrier); warp 1 = UMMA issuer
-// (leader only) and TMEM allocation (both, collectively); warps 2-9 =
+// (leader only: an elected lane of the converged warp, which issues a UMMA in 54
+// clocks; a lane alone in a diverged warp took longer than a UMMA's 128) and TMEM
+// allocation (both, collectively); warps 2-9 =
 // epilogue of the CTA's own 128 rows, two warps per TMEM lane quadrant, each
 // taking half of the 256 columns. Stage and accumulator barriers are
 // released to both CTAs by multicast commits; the leader waits for both
@@ -59,16 +61,6 @@ struct PairTile {
   int e, row0, row_end, n0;
 };
 
-// n-tile index of pair tile L (the raster arithmetic of decode_pair).
-__device__ __forceinline__ int pair_tile_nt(int L, int E, int total_pm, int n_tiles_n,
-                                            int a_row_bytes) {
-  const int group = raster_group(total_pm, E, a_row_bytes);
-  const int per_group = group * n_tiles_n;
-  const int g = L / per_group;
-  const int gsz = min(group, total_pm - g * group);
-  return (L - g * per_group) / gsz;
-}
-
 __device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, const int* offs,
                                                 int E, int total_pm, int n_tiles_n, int rank,
                                                 int a_row_bytes) {
@@ -92,6 +84,31 @@ __device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, con
   t.n0 = nt * kBN;
   return t;
 }
+
+// A warp's walk over its pair's tiles. Each lane decodes one of the next 32 (the
+// divisions and the search would otherwise stand between every two tiles of the
+// issuer); called by the whole warp.
+struct PairWalk {
+  const int *pm_prefix, *offs;
+  int E, total_pm, n_tiles_n, rank, a_row_bytes, total, stride, L, at;
+  PairTile mine;
+
+  __device__ __forceinline__ bool next(PairTile& t) {
+    if (L >= total) return false;
+    if (at == 32) {
+      const int l = min(L + static_cast<int>(threadIdx.x & 31) * stride, total - 1);
+      mine = decode_pair(l, pm_prefix, offs, E, total_pm, n_tiles_n, rank, a_row_bytes);
+      at = 0;
+    }
+    t.e = __shfl_sync(0xffffffffu, mine.e, at);
+    t.row0 = __shfl_sync(0xffffffffu, mine.row0, at);
+    t.row_end = __shfl_sync(0xffffffffu, mine.row_end, at);
+    t.n0 = __shfl_sync(0xffffffffu, mine.n0, at);
+    ++at;
+    L += stride;
+    return true;
+  }
+};
 
 __device__ __forceinline__ float gelu_tanh_f(float u) {
   // 0.5 u (1 + tanh(z)) = u / (1 + exp(-2 z)),  z = sqrt(2/pi) (u + 0.044715 u^3)
@@ -249,10 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
+  PairWalk tiles{pm_prefix, offs, E, total_pm, n_tiles_n, static_cast<int>(rank), a_row_bytes, total,
+                 n_clusters, cluster, 32, {}};
+  PairTile c;
   if (warp == 0) {
-    // lanes 1-31 leave at once unless they gather (they must not fall
-    // through to the epilogue branch below)
-    if (kGather || lane == 0) {
+    {
       // ------------------------------------------------------ TMA producer ----
       // lane 0 waits, arms the barrier and loads B (and A when not gathered);
       // with kGather every lane of the warp also gathers four A rows
@@ -261,8 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
       bool aborted = false;
       const uint64_t pol_a = l2_policy_evict_last();
-      for (int L = cluster; L < total && !aborted; L += n_clusters) {
-        const PairTile c = decode_pair(L, pm_prefix, offs, E, total_pm, n_tiles_n, rank, a_row_bytes);
+      while (!aborted && tiles.next(c)) {
         // A last n-tile of at most 128 columns runs as an N = 128 UMMA, each
         // CTA holding 64 of its columns (the loads stay the same size: the
         // extra columns are read and never used).
@@ -278,17 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         for (int kb = 0; kb < nk; ++kb) {
-          bool ok = true;
-          if (lane == 0) ok = pair_wait(&empty[stage], phase ^ 1u);
-          if constexpr (kGather) ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) {
+          if (!__all_sync(0xffffffffu, pair_wait(&empty[stage], phase ^ 1u))) {
             aborted = true;
             break;
           }
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
           uint8_t* sa = smem + stage * kSB;
           uint8_t* sb = sa + kKBS * kABytes;
-          if (lane == 0) {
+          if (elect_one()) {
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kSB);
             // A rows are reused by every n-tile of the group: keep them in L2
             if constexpr (kFp8) {
@@ -315,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d_pair(sb, &tm_b, bar, 0, kb * kKBS * kBlockK, b_col / 64, c.e);
             }
           }
+          __syncwarp();
           if constexpr (kGather)
             tma_gather4_pair(sa + 512 * lane, &tm_a, bar, kb * kKE, gr[0], gr[1], gr[2], gr[3]);
           ++issued;
@@ -361,71 +376,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------------------- UMMA issuer (leader) ----
+      // the whole warp walks, an elected lane issues
       const uint32_t idesc_full =
           kFp8 ? idesc_e4m3_f32(2 * kBM, kBN) : idesc_bf16_f32(2 * kBM, kBN, false, !kTrans);
       const uint32_t idesc_half = kFp8 ? idesc_e4m3_f32(2 * kBM, kBN / 2)
                                        : idesc_bf16_f32(2 * kBM, kBN / 2, false, !kTrans);
+      // A (and B where it is K-major): 128-byte rows along K. B MN-major: one
+      // 128-byte row per k, this CTA's two 64-column blocks kKBS * 8 KB apart.
+      const uint64_t a_desc0 = smem_desc_sw128(smem_u32(smem), 16u, 1024u);
+      const uint64_t b_desc0 =
+          kFp8 || kTrans ? a_desc0 + ((kKBS * kABytes) >> 4)
+                         : smem_desc_sw128(smem_u32(smem) + kKBS * kABytes, kKBS * 64u * kBlockK * 2, 1024u);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool aborted = false;
-      for (int L = cluster; L < total && !aborted; L += n_clusters) {
-        if (!pair_wait(&tempty[acc], acc_phase ^ 1u)) break;
-        tc_fence_after();
+      while (!aborted && tiles.next(c)) {
+        if (!__all_sync(0xffffffffu, pair_wait(&tempty[acc], acc_phase ^ 1u))) break;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
-        const int nt = pair_tile_nt(L, E, total_pm, n_tiles_n, a_row_bytes);
-        const uint32_t idesc = p.N - nt * kBN <= kBN / 2 ? idesc_half : idesc_full;
+        const uint32_t idesc = p.N - c.n0 <= kBN / 2 ? idesc_half : idesc_full;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!pair_wait(&full[stage], phase)) {
+          if (!__all_sync(0xffffffffu, pair_wait(&full[stage], phase))) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stage * kSB);
-          const uint32_t b_addr = a_addr + kKBS * kABytes;
+          const uint64_t ad = a_desc0 + ((stage * kSB) >> 4), bd = b_desc0 + ((stage * kSB) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int r = 0; r < kKBS; ++r) {
+            for (uint32_t r = 0; r < kKBS; ++r) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              // A: K-major 128-byte rows, k-block r at r * 16 KB; one UMMA K
-              // step (16 bf16 or 32 e4m3) is 32 bytes.
-              const uint64_t ad = smem_desc_sw128(a_addr + kABytes * r + 32u * kk, 16u, 1024u);
-              const uint32_t acc_in = (kb | r | kk) != 0 ? 1u : 0u;
-              if constexpr (kFp8) {
-                // B: K-major like A
-                const uint64_t bd = smem_desc_sw128(b_addr + kBBytes * r + 32u * kk, 16u, 1024u);
-                umma_f8_pair(d_tmem, ad, bd, idesc, acc_in);
-              } else if constexpr (kTrans) {
-                const uint64_t bd = smem_desc_sw128(b_addr + kBBytes * r + 32u * kk, 16u, 1024u);
-                umma_bf16_pair(d_tmem, ad, bd, idesc, acc_in);
-              } else {
-                // B: MN-major, one 128-byte row per k (16-row K step = 2 KB,
-                // k-block r at r * 8 KB), this CTA's two 64-column blocks
-                // kKBS * 8 KB apart.
-                const uint64_t bd = smem_desc_sw128(b_addr + 8192u * r + 2048u * kk,
-                                                    kKBS * 64u * kBlockK * 2, 1024u);
-                umma_bf16_pair(d_tmem, ad, bd, idesc, acc_in);
+              for (uint32_t kk = 0; kk < 4; ++kk) {
+                // one UMMA K step is 16 bf16 or 32 e4m3: 32 bytes of a K-major
+                // operand (k-block r at r * 16 KB), 2 KB of an MN-major one (k-block
+                // r at r * 8 KB)
+                const uint64_t a = ad + (kABytes >> 4) * r + 2u * kk;
+                const uint64_t b = kFp8 || kTrans ? bd + (kBBytes >> 4) * r + 2u * kk
+                                                  : bd + 512u * r + 128u * kk;
+                const uint32_t acc_in = (r | kk) != 0 || kb != 0 ? 1u : 0u;
+                if constexpr (kFp8) umma_f8_pair(d_tmem, a, b, idesc, acc_in);
+                else umma_bf16_pair(d_tmem, a, b, idesc, acc_in);
               }
             }
+            umma_commit_pair_multicast(&empty[stage], 0x3);
+            if (kb == nk - 1) umma_commit_pair_multicast(&tfull[acc], 0x3);
           }
-          umma_commit_pair_multicast(&empty[stage], 0x3);
+          __syncwarp();
           if (++stage == nst) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (aborted) break;
-        umma_commit_pair_multicast(&tfull[acc], 0x3);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       // every UMMA issued must finish before TMEM is released
-      umma_commit_pair(drain);
+      if (elect_one()) umma_commit_pair(drain);
+      __syncwarp();
       mbar_wait_drain(drain, 0, kDrainLimitNs);
     }
   } else {
@@ -439,8 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        mapa_shared(smem_u32(&tempty[1]), 0)};
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int L = cluster; L < total; L += n_clusters) {
-      const PairTile c = decode_pair(L, pm_prefix, offs, E, total_pm, n_tiles_n, rank, a_row_bytes);
+    while (tiles.next(c)) {
       const int row = c.row0 + 32 * q + lane;
       const bool valid = row < c.row_end;
       const int col0 = c.n0 + half * (kBN / 2);
@@ -469,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) uv[i] = ld_global_cs_v4(urow + 8 * i);
         }
       }
-      if (!pair_wait(&tfull[acc], acc_phase)) break;
+      if (!__all_sync(0xffffffffu, pair_wait(&tfull[acc], acc_phase))) break;
       tc_fence_after();
       uint16_t* drow = p.D + static_cast<size_t>(valid ? row : 0) * p.N;
       float row_max = 0.f;  // FP8 mode: max |output| of this row in these columns
