@@ -1603,7 +1603,11 @@ moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N, const 
   g.U = pre;
   g.dev_status = dev_status;
   g.timeout_ns = wait_timeout_ns();
-  MOE_CUDA(launch_expert_gemm(tm_a, tm_b, g, transposed != 0, num_sms(),
+  CUtensorMap tm_d, tm_u = {};
+  if (!tmap_bf16_2d(&tm_d, D, N, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return MOE_ERR_CUDA;
+  if (pre != nullptr && !tmap_bf16_2d(&tm_u, pre, N, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return MOE_ERR_CUDA;
+  MOE_CUDA(launch_expert_gemm(tm_a, tm_b, tm_d, tm_u, g, transposed != 0, num_sms(),
                               static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }

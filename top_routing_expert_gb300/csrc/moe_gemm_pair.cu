@@ -46,6 +46,7 @@ constexpr uint32_t kBBytes = (kBN / 2) * kBlockK * 2;    // 16 KB
 constexpr uint32_t kStageBytes = kABytes + kBBytes;      // 32 KB per k-block
 constexpr int kWideKB = 2;  // k-blocks per stage of the bf16 tile-loaded kernel
 constexpr uint32_t kTmemCols = 2 * kBN;                  // two accumulators
+constexpr uint32_t kOutBytes = 32 * 64;  // training: one warp's 32 rows x 32 bf16 columns
 // Pair m-tiles per raster group: 16 when the experts average at least 16
 // pair m-tiles (4096 rows) and A's rows are short, so that a group stays
 // within one expert's weights (1.7 % faster on the power-capped large-expert
@@ -63,7 +64,7 @@ struct PairTile {
 
 __device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, const int* offs,
                                                 int E, int total_pm, int n_tiles_n, int rank,
-                                                int a_row_bytes) {
+                                                int a_row_bytes, int width) {
   const int group = raster_group(total_pm, E, a_row_bytes);
   const int per_group = group * n_tiles_n;
   const int g = L / per_group;
@@ -81,7 +82,7 @@ __device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, con
   t.e = lo;
   t.row0 = offs[lo] + (2 * (pm - pm_prefix[lo]) + rank) * kBM;
   t.row_end = offs[lo + 1];
-  t.n0 = nt * kBN;
+  t.n0 = nt * width;
   return t;
 }
 
@@ -90,14 +91,14 @@ __device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, con
 // issuer); called by the whole warp.
 struct PairWalk {
   const int *pm_prefix, *offs;
-  int E, total_pm, n_tiles_n, rank, a_row_bytes, total, stride, L, at;
+  int E, total_pm, n_tiles_n, rank, a_row_bytes, width, total, stride, L, at;
   PairTile mine;
 
   __device__ __forceinline__ bool next(PairTile& t) {
     if (L >= total) return false;
     if (at == 32) {
       const int l = min(L + static_cast<int>(threadIdx.x & 31) * stride, total - 1);
-      mine = decode_pair(l, pm_prefix, offs, E, total_pm, n_tiles_n, rank, a_row_bytes);
+      mine = decode_pair(l, pm_prefix, offs, E, total_pm, n_tiles_n, rank, a_row_bytes, width);
       at = 0;
     }
     t.e = __shfl_sync(0xffffffffu, mine.e, at);
@@ -131,19 +132,11 @@ __device__ __forceinline__ float gelu_slope(float u) {
   return fmaf(x * (e * s), s * fmaf(0.2140644488f, x2, 1.5957691216057308f), s);
 }
 
-// 32 fp32 accumulator words to bf16, 64 bytes of one output row. Outputs are
-// read once, by the next kernel: streamed past L2.
-__device__ __forceinline__ void store_row_chunk(uint16_t* dst, const uint32_t (&r)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 v;
-    v.x = pack_bf16x2(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1]));
-    v.y = pack_bf16x2(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3]));
-    v.z = pack_bf16x2(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5]));
-    v.w = pack_bf16x2(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7]));
-    st_global_cs_v4(reinterpret_cast<uint4*>(dst) + i, v);
-  }
-}
+// Tensor maps of the training epilogues' outputs, D and the values before the
+// GELU: 32 rows x 32 columns, 64-byte swizzle.
+struct OutMaps {
+  CUtensorMap d, u;
+};
 
 // kFp8: A and B are e4m3 (both K-major, 128 elements = 128 bytes per
 // stage row), the UMMA is kind::f8f6f4 and the epilogue multiplies by the
@@ -164,7 +157,8 @@ __device__ __forceinline__ void store_row_chunk(uint16_t* dst, const uint32_t (&
 template <bool kFp8, bool kQOut, bool kGather, bool kTrans, bool kTrain>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
-                             const __grid_constant__ CUtensorMap tm_b, GemmArgs p) {
+                             const __grid_constant__ CUtensorMap tm_b,
+                             const __grid_constant__ OutMaps tm_out, GemmArgs p) {
   constexpr int kKE = kFp8 ? 128 : kBlockK;  // K elements per k-block
   constexpr int kKBS = kGather ? 1 : kWideKB;  // k-blocks per stage
   constexpr uint32_t kSB = kKBS * kStageBytes;             // bytes per stage
@@ -173,7 +167,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nst = p.stages;  // pipeline depth, chosen by the launcher to fit shared memory
   // FP8 column scales of the current tile, 128 per epilogue warp
   float* col_scale = reinterpret_cast<float*>(smem + nst * kSB);
-  uint64_t* full = reinterpret_cast<uint64_t*>(col_scale + (kFp8 ? kEpiWarps * (kBN / 2) : 0));
+  // training: kOutBufs buffers of 32 rows x 64 bytes per epilogue warp (in place
+  // of the scales)
+  uint64_t* full = reinterpret_cast<uint64_t*>(col_scale + (kFp8 ? kEpiWarps * (kBN / 2) : 0) +
+                                               (kTrain ? kEpiWarps * p.out_bufs * kOutBytes / 4 : 0));
   uint64_t* empty = full + nst;
   uint64_t* tfull = empty + nst;
   uint64_t* tempty = tfull + 2;
@@ -250,7 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem_base = *tmem_slot;
   const int total_pm = pm_prefix[E];
-  const int n_tiles_n = (p.N + kBN - 1) / kBN;
+  // Training: tiles of 128 columns where those of 256 would leave half the pairs
+  // without one (a tile then takes half as long in its epilogue)
+  const int width = kTrain && 2 * total_pm * ((p.N + kBN - 1) / kBN) <= n_clusters ? kBN / 2 : kBN;
+  const int n_tiles_n = (p.N + width - 1) / width;
   const int a_row_bytes = p.K * (kFp8 ? 1 : 2);
   const int total = total_pm * n_tiles_n;
   // stages per tile; a partial last stage reads zeros past K (A and B are
@@ -266,8 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  PairWalk tiles{pm_prefix, offs, E, total_pm, n_tiles_n, static_cast<int>(rank), a_row_bytes, total,
-                 n_clusters, cluster, 32, {}};
+  PairWalk tiles{pm_prefix, offs, E, total_pm, n_tiles_n, static_cast<int>(rank), a_row_bytes, width,
+                 total, n_clusters, cluster, 32, {}};
+  // a tile of at most 128 columns runs as an N = 128 UMMA
+  auto is_narrow = [&](const PairTile& t) { return width < kBN || p.N - t.n0 <= kBN / 2; };
   PairTile c;
   if (warp == 0) {
     {
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A last n-tile of at most 128 columns runs as an N = 128 UMMA, each
         // CTA holding 64 of its columns (the loads stay the same size: the
         // extra columns are read and never used).
-        const bool half_n = p.N - c.n0 <= kBN / 2;
+        const bool half_n = is_narrow(c);
         const int b_col = c.n0 + static_cast<int>(rank) * (half_n ? kBN / 4 : kBN / 2);
         int gr[4] = {0, 0, 0, 0};
         if constexpr (kGather) {
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (!aborted && tiles.next(c)) {
         if (!__all_sync(0xffffffffu, pair_wait(&tempty[acc], acc_phase ^ 1u))) break;
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
-        const uint32_t idesc = p.N - c.n0 <= kBN / 2 ? idesc_half : idesc_full;
+        const uint32_t idesc = is_narrow(c) ? idesc_half : idesc_full;
         for (int kb = 0; kb < nk; ++kb) {
           if (!__all_sync(0xffffffffu, pair_wait(&full[stage], phase))) {
             aborted = true;
@@ -450,14 +452,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* wscale = col_scale + (warp - 2) * (kBN / 2);
     const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
                                        mapa_shared(smem_u32(&tempty[1]), 0)};
+    const uint32_t out_buf = smem_u32(col_scale) + static_cast<uint32_t>(warp - 2) * p.out_bufs * kOutBytes;
+    int out_at = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     while (tiles.next(c)) {
       const int row = c.row0 + 32 * q + lane;
       const bool valid = row < c.row_end;
-      const int col0 = c.n0 + half * (kBN / 2);
+      // (training: a narrow tile's columns are shared by both warps of a quadrant)
+      const int part = kTrain && is_narrow(c) ? kBN / 4 : kBN / 2;
+      const int col0 = c.n0 + half * part;
       // whole 32-column chunks: N is a multiple of 64
-      const int n_chunks = col0 >= p.N ? 0 : min(4, (p.N - col0) / 32);
+      const int n_chunks = col0 >= p.N ? 0 : min(part / 32, (p.N - col0) / 32);
       float rs = 1.f;
       if constexpr (kFp8) {
         // scales are fetched before the accumulator wait, hiding their latency
@@ -470,6 +476,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid) rs = p.a_scale[row];
         __syncwarp();
       }
+      // Training: 32 columns of the warp's rows as bf16. Through shared memory and
+      // out by TMA where all 32 rows are the segment's (a lane storing its own 64
+      // bytes touches 32 lines with each instruction, a clock each: 4096 clocks a
+      // tile and output); by the lanes that have a row at a segment's end.
+      auto emit = [&](const uint32_t(&r)[32], const CUtensorMap& map, uint16_t* out, int col) {
+        if constexpr (kTrain) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* w = r + 8 * i;
+            auto two = [](uint32_t a, uint32_t b) {
+              return pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
+            };
+            v[i] = make_uint4(two(w[0], w[1]), two(w[2], w[3]), two(w[4], w[5]), two(w[6], w[7]));
+          }
+          if (row - lane + 32 <= c.row_end) {
+            if (lane == 0) {
+              if (p.out_bufs == 2) tma_store_wait_read<1>();
+              else tma_store_wait_read<0>();
+            }
+            __syncwarp();
+            const uint32_t buf = out_buf + out_at * kOutBytes;
+            // 16-byte word i of row r lies at i ^ (r / 2 & 3)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              st_shared_v4(buf + 64u * lane + 16u * (i ^ (lane >> 1 & 3)), v[i]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&map, buf, col, row);
+            out_at = p.out_bufs - 1 - out_at;
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * p.N + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_cs_v4(dst + i, v[i]);
+          }
+        }
+      };
       // the first kept values are fetched before the accumulator wait, each
       // later chunk's while the one before it is worked on
       const uint16_t* urow = nullptr;
@@ -486,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* drow = p.D + static_cast<size_t>(valid ? row : 0) * p.N;
       float row_max = 0.f;  // FP8 mode: max |output| of this row in these columns
       const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                              static_cast<uint32_t>(acc * kBN + half * (kBN / 2));
+                              static_cast<uint32_t>(acc * kBN + half * part);
       // two register sets: the next chunk's TMEM load overlaps this chunk's math
       uint32_t ra[32], rb[32];
       if constexpr (kQOut) {
@@ -551,35 +594,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t(&nx)[32] = (cc & 1) ? ra : rb;
             if (cc + 1 < n_chunks) tmem_ld_32x32b_x32(t_base + 32u * (cc + 1), nx);
             if constexpr (kTrain) {
-              if (valid) {
-                if (p.gelu == kEpiGeluGrad) {
-                  uint32_t u[16];
+              const int col = col0 + 32 * cc;
+              if (p.gelu == kEpiGeluGrad) {
+                uint32_t u[16];
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    u[4 * i] = uv[i].x;
-                    u[4 * i + 1] = uv[i].y;
-                    u[4 * i + 2] = uv[i].z;
-                    u[4 * i + 3] = uv[i].w;
-                  }
-                  if (cc + 1 < n_chunks) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                      uv[i] = ld_global_cs_v4(urow + 32 * (cc + 1) + 8 * i);
-                  }
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) * gelu_slope(bf16_lo(u[i])));
-                    r[2 * i + 1] =
-                        __float_as_uint(__uint_as_float(r[2 * i + 1]) * gelu_slope(bf16_hi(u[i])));
-                  }
-                } else if (p.gelu == kEpiGelu) {
-                  if (p.U != nullptr) store_row_chunk(p.U + static_cast<size_t>(row) * p.N + col0 + 32 * cc, r);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    r[i] = __float_as_uint(gelu_tanh_f(__uint_as_float(r[i])));
+                for (int i = 0; i < 4; ++i) {
+                  u[4 * i] = uv[i].x;
+                  u[4 * i + 1] = uv[i].y;
+                  u[4 * i + 2] = uv[i].z;
+                  u[4 * i + 3] = uv[i].w;
                 }
-                store_row_chunk(drow + col0 + 32 * cc, r);
+                if (valid && cc + 1 < n_chunks) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    uv[i] = ld_global_cs_v4(urow + 32 * (cc + 1) + 8 * i);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) * gelu_slope(bf16_lo(u[i])));
+                  r[2 * i + 1] =
+                      __float_as_uint(__uint_as_float(r[2 * i + 1]) * gelu_slope(bf16_hi(u[i])));
+                }
+              } else if (p.gelu == kEpiGelu) {
+                if (p.U != nullptr) emit(r, tm_out.u, p.U, col);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  r[i] = __float_as_uint(gelu_tanh_f(__uint_as_float(r[i])));
               }
+              emit(r, tm_out.d, p.D, col);
             } else if (valid) {
               uint32_t packed[16];
 #pragma unroll
@@ -621,6 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1u;
       }
     }
+    if constexpr (kTrain) {
+      if (lane == 0) tma_store_wait();
+    }
   }
 
   __syncwarp();
@@ -633,15 +678,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage) {
+static size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage, int out_bufs) {
   return 1024 + static_cast<size_t>(stages) * kStageBytes * kb_per_stage +
-         (fp8 ? 4 * kEpiWarps * (kBN / 2) : 0) +
+         (fp8 ? 4 * kEpiWarps * (kBN / 2) : 0) + kEpiWarps * out_bufs * kOutBytes +
          8 * (2 * stages + 6) + 16 + 8 * static_cast<size_t>(E + 1);
 }
 
 template <bool kFp8, bool kQOut, bool kGather, bool kTrans = false, bool kTrain = false>
 cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const GemmArgs& a,
-                        int num_sms, cudaStream_t st) {
+                        int num_sms, cudaStream_t st, const OutMaps& tm_out = OutMaps{}) {
   // the deepest ring that fits: every stage in flight hides TMA latency
   int dev = 0, optin = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -651,10 +696,15 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
   GemmArgs args = a;
   constexpr int kbs = kGather ? 1 : kWideKB;
   args.stages = kMaxStages;
-  while (args.stages > 2 &&
-         gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs) > static_cast<size_t>(optin))
-    --args.stages;
-  const size_t smem = gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs);
+  args.out_bufs = kTrain ? 2 : 0;
+  const auto bytes = [&] { return gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, args.out_bufs); };
+  while (args.stages > 2 && bytes() > static_cast<size_t>(optin)) {
+    // with the offsets of more than 241 experts, one output buffer a warp fits
+    // beside three stages of two k-blocks
+    if (kTrain && args.out_bufs == 2 && args.stages == 3) args.out_bufs = 1;
+    else --args.stages;
+  }
+  const size_t smem = bytes();
   err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
@@ -676,7 +726,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>, tm_a, tm_b,
-                           args);
+                           tm_out, args);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
 }
@@ -688,10 +738,12 @@ cudaError_t launch_grouped_gemm_pair(const CUtensorMap& tm_a, const CUtensorMap&
 }
 
 cudaError_t launch_expert_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
-                               const GemmArgs& a, bool transposed, int num_sms, cudaStream_t st) {
+                               const CUtensorMap& tm_d, const CUtensorMap& tm_u, const GemmArgs& a,
+                               bool transposed, int num_sms, cudaStream_t st) {
+  const OutMaps out{tm_d, tm_u};
   if (transposed)
-    return launch_pair<false, false, false, true, true>(tm_a, tm_b, a, num_sms, st);
-  return launch_pair<false, false, false, false, true>(tm_a, tm_b, a, num_sms, st);
+    return launch_pair<false, false, false, true, true>(tm_a, tm_b, a, num_sms, st, out);
+  return launch_pair<false, false, false, false, true>(tm_a, tm_b, a, num_sms, st, out);
 }
 
 cudaError_t launch_grouped_gemm_pair_fp8(const CUtensorMap& tm_a, const CUtensorMap& tm_b,

@@ -188,6 +188,7 @@ struct GemmArgs {
   const int32_t* a_rows;   // optional: A row r is row a_rows[r] of the A tensor (a gather,
   int a_src_rows;          //   by TMA, from a tensor of a_src_rows rows); CTA-pair kernel
   int stages;              // CTA-pair kernel: pipeline depth (set by its launcher)
+  int out_bufs = 0;        // training: output buffers per epilogue warp (set by its launcher)
   uint32_t* dev_status;
   uint64_t timeout_ns;
 };
@@ -301,15 +302,16 @@ cudaError_t launch_grouped_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b
 cudaError_t launch_grouped_gemm_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                                      const GemmArgs& a, int num_sms, cudaStream_t st);
 // The product alone, with W [E][K][N] or (transposed) [E][N][K] and the
-// epilogues above; CTA-pair kernel at every size.
+// epilogues above; CTA-pair kernel at every size. tm_d, tm_u: D and U in boxes of
+// 32 rows x 32 columns, 64-byte swizzle (tm_u unused without U).
 cudaError_t launch_expert_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
-                               const GemmArgs& a, bool transposed, int num_sms, cudaStream_t st);
+                               const CUtensorMap& tm_d, const CUtensorMap& tm_u, const GemmArgs& a,
+                               bool transposed, int num_sms, cudaStream_t st);
 cudaError_t launch_wgrad(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
                          const WgradArgs& a, int num_sms, cudaStream_t st);
 int block_bwd_groups(int64_t T, int H);
 cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st);
-size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage);
 // FP8 operands; writes D (bf16), or Dq + d_scale when a.Dq is set
 cudaError_t launch_grouped_gemm_pair_fp8(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                                          const GemmArgs& a, int num_sms, cudaStream_t st);

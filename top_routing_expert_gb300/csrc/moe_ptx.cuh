@@ -647,8 +647,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sa
       : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+template <int kLeft = 0>  // all but the last kLeft groups
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
 }
 __device__ __forceinline__ void tma_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
