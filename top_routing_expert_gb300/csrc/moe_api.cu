@@ -1587,7 +1587,8 @@ moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N, const 
   MOE_OPTIONAL(pre);
   MOE_REQUIRE(dev_status);
   CUtensorMap tm_a, tm_b;
-  if (!tmap_bf16_kblocks(&tm_a, x, K, rows, 128, 2)) return MOE_ERR_CUDA;
+  const int a_box = rows < 128 ? static_cast<int>(rows + 7) / 8 * 8 : 128;
+  if (!tmap_bf16_kblocks(&tm_a, x, K, rows, a_box, 2)) return MOE_ERR_CUDA;
   if (transposed ? !tmap_bf16_kblocks(&tm_b, W, K, static_cast<uint64_t>(E) * N, 128, 2)
                  : !tmap_bf16_experts(&tm_b, W, N, K, E, 2 * kBlockK))
     return MOE_ERR_CUDA;
@@ -1601,6 +1602,7 @@ moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N, const 
   g.gelu = epilogue == MOE_EPILOGUE_GELU ? kEpiGelu
            : epilogue == MOE_EPILOGUE_GELU_GRAD ? kEpiGeluGrad : kEpiNone;
   g.U = pre;
+  g.a_box = a_box;
   g.dev_status = dev_status;
   g.timeout_ns = wait_timeout_ns();
   CUtensorMap tm_d, tm_u = {};

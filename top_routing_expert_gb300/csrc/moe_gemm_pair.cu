@@ -40,13 +40,17 @@ constexpr int kBM = 128;           // rows per CTA; the pair computes 256
 constexpr int kBN = 256;           // columns per pair tile (128 held by each CTA)
 constexpr int kMaxStages = 7;  // bf16 with E <= 234; FP8 (scale area) and larger E: 6
 constexpr int kEpiWarps = 8;                             // 2 per TMEM lane quadrant
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kABytes = kBM * kBlockK * 2;          // 16 KB
 constexpr uint32_t kBBytes = (kBN / 2) * kBlockK * 2;    // 16 KB
 constexpr uint32_t kStageBytes = kABytes + kBBytes;      // 32 KB per k-block
 constexpr int kWideKB = 2;  // k-blocks per stage of the bf16 tile-loaded kernel
 constexpr uint32_t kTmemCols = 2 * kBN;                  // two accumulators
-constexpr uint32_t kOutBytes = 32 * 64;  // training: one warp's 32 rows x 32 bf16 columns
+// Training: 16 epilogue warps, four per TMEM lane quadrant with 64 columns each (8
+// warps of 128: GELU over K = 128 took 75 us where 16 take 49), and a buffer of 32
+// rows x 32 bf16 columns for each.
+constexpr int kTrainEpiWarps = 16;
+constexpr uint32_t kOutBytes = 32 * 64;
+__host__ __device__ constexpr int epi_warps(bool train) { return train ? kTrainEpiWarps : kEpiWarps; }
 // Pair m-tiles per raster group: 16 when the experts average at least 16
 // pair m-tiles (4096 rows) and A's rows are short, so that a group stays
 // within one expert's weights (1.7 % faster on the power-capped large-expert
@@ -62,7 +66,17 @@ struct PairTile {
   int e, row0, row_end, n0;
 };
 
-__device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, const int* offs,
+// Pair m-tiles before expert e: one for every 256 rows before its segment, and
+// what the segments' ends add to that (at most one each, so 16 bits hold it).
+struct PmPrefix {
+  const int* offs;
+  const uint16_t* extra;
+  __device__ __forceinline__ int operator[](int e) const {
+    return (offs[e] - offs[0]) / (2 * kBM) + extra[e];
+  }
+};
+
+__device__ __forceinline__ PairTile decode_pair(int L, const PmPrefix& pm_prefix, const int* offs,
                                                 int E, int total_pm, int n_tiles_n, int rank,
                                                 int a_row_bytes, int width) {
   const int group = raster_group(total_pm, E, a_row_bytes);
@@ -90,7 +104,8 @@ __device__ __forceinline__ PairTile decode_pair(int L, const int* pm_prefix, con
 // divisions and the search would otherwise stand between every two tiles of the
 // issuer); called by the whole warp.
 struct PairWalk {
-  const int *pm_prefix, *offs;
+  PmPrefix pm_prefix;
+  const int* offs;
   int E, total_pm, n_tiles_n, rank, a_row_bytes, width, total, stride, L, at;
   PairTile mine;
 
@@ -117,21 +132,6 @@ __device__ __forceinline__ float gelu_tanh_f(float u) {
   return __fdividef(u, 1.0f + __expf(-z2));
 }
 
-// Slope of gelu_tanh_f: with s = 1 / (1 + e), e = exp(-2 z),
-//   d/du u s(u) = s + u e s^2 2 dz/du,  2 dz/du = 2 sqrt(2/pi) (1 + 3 * 0.044715 u^2).
-// e s^2 is s (1 - s) without the difference next to 1. Beyond +-8 the slope is
-// 0 or 1 to fp32's last place and the cube would run out of range, so u is
-// held there (a NaN stays one).
-__device__ __forceinline__ float gelu_slope(float u) {
-  float x;
-  asm("min.NaN.f32 %0, %1, 0f41000000;" : "=f"(x) : "f"(u));
-  asm("max.NaN.f32 %0, %0, 0fC1000000;" : "+f"(x));
-  const float x2 = x * x;
-  const float e = __expf(-1.5957691216057308f * fmaf(0.044715f * x2, x, x));
-  const float s = __fdividef(1.0f, 1.0f + e);
-  return fmaf(x * (e * s), s * fmaf(0.2140644488f, x2, 1.5957691216057308f), s);
-}
-
 // Tensor maps of the training epilogues' outputs, D and the values before the
 // GELU: 32 rows x 32 columns, 64-byte swizzle.
 struct OutMaps {
@@ -155,10 +155,11 @@ struct OutMaps {
 // kTrain (bf16): the epilogues of training (GemmArgs::gelu and U): GELU with
 // the value before it kept, or the product times GELU's slope at kept values.
 template <bool kFp8, bool kQOut, bool kGather, bool kTrans, bool kTrain>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(64 + 32 * epi_warps(kTrain), 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                              const __grid_constant__ CUtensorMap tm_b,
                              const __grid_constant__ OutMaps tm_out, GemmArgs p) {
+  constexpr int kThreads = 64 + 32 * epi_warps(kTrain);
   constexpr int kKE = kFp8 ? 128 : kBlockK;  // K elements per k-block
   constexpr int kKBS = kGather ? 1 : kWideKB;  // k-blocks per stage
   constexpr uint32_t kSB = kKBS * kStageBytes;             // bytes per stage
@@ -167,10 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nst = p.stages;  // pipeline depth, chosen by the launcher to fit shared memory
   // FP8 column scales of the current tile, 128 per epilogue warp
   float* col_scale = reinterpret_cast<float*>(smem + nst * kSB);
-  // training: kOutBufs buffers of 32 rows x 64 bytes per epilogue warp (in place
-  // of the scales)
+  // (training: the epilogue warps' output buffers in their place)
   uint64_t* full = reinterpret_cast<uint64_t*>(col_scale + (kFp8 ? kEpiWarps * (kBN / 2) : 0) +
-                                               (kTrain ? kEpiWarps * p.out_bufs * kOutBytes / 4 : 0));
+                                               (kTrain ? kTrainEpiWarps * kOutBytes / 4 : 0));
   uint64_t* empty = full + nst;
   uint64_t* tfull = empty + nst;
   uint64_t* tempty = tfull + 2;
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* abort_flag = tmem_slot + 1;
   uint32_t* peer_issued = abort_flag + 1;              // leader: stages the peer loaded
   int* offs = reinterpret_cast<int*>(peer_issued + 1);  // [E+1]
-  int* pm_prefix = offs + (p.E + 1);                    // [E+1]
+  uint16_t* pm_extra = reinterpret_cast<uint16_t*>(offs + (p.E + 1));  // [E+1]
+  const PmPrefix pm_prefix{offs, pm_extra};
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.E;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps * 32);  // both CTAs' epilogue threads
+      mbar_init(&tempty[a], 2 * epi_warps(kTrain) * 32);  // both CTAs' epilogue threads
     }
     mbar_init(drain, 1);
     mbar_init(xbar, 1);
@@ -235,10 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += n;
       }
-      if (e < E) pm_prefix[e] = carry + incl - pm;
+      if (e < E)
+        pm_extra[e] = static_cast<uint16_t>(carry + incl - pm - (offs[e] - offs[0]) / (2 * kBM));
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) pm_prefix[E] = carry;
+    if (lane == 0)
+      pm_extra[E] = static_cast<uint16_t>(carry - (offs[E] - offs[0]) / (2 * kBM));
   }
   tc_fence_before();
   __syncthreads();
@@ -280,6 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int issued = 0;
       bool aborted = false;
+      // Bytes of a CTA's A in a stage. Training: A's box has no more rows than the
+      // buffer, and a CTA whose rows lie past the segment loads none (what is then
+      // in its place only reaches rows that are never stored).
+      const uint32_t a_bytes = kTrain ? kKBS * 128u * p.a_box : kKBS * kABytes;
+      const uint32_t b_bytes = kKBS * kBBytes;
+      uint32_t peer_has_a = 0;  // by stage, the leader's record of its last loads
       const uint64_t pol_a = l2_policy_evict_last();
       while (!aborted && tiles.next(c)) {
         // A last n-tile of at most 128 columns runs as an N = 128 UMMA, each
@@ -302,10 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          const bool has_a = !kTrain || c.row0 < c.row_end;
+          const bool peer_a = !kTrain || c.row0 + kBM < c.row_end;  // as the leader sees it
+          peer_has_a = (peer_has_a & ~(1u << stage)) | (peer_a ? 1u : 0u) << stage;
           uint8_t* sa = smem + stage * kSB;
           uint8_t* sb = sa + kKBS * kABytes;
           if (elect_one()) {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kSB);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * b_bytes + (peer_a ? 2 : 1) * a_bytes);
             // A rows are reused by every n-tile of the group: keep them in L2
             if constexpr (kFp8) {
               // A e4m3 [rows, K] and B^T [E*N, K] (this CTA's 128 output
@@ -317,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_2d_pair(sb + r * kBBytes, &tm_b, bar, k0, c.e * p.N + b_col);
               }
             } else if constexpr (!kGather) {
-              // A: {64 k, 128 rows, kKBS k-blocks}
-              tma_load_3d_pair_hint(sa, &tm_a, bar, 0, c.row0, kb * kKBS, pol_a);
+              // A: {64 k, 128 rows (training: a_box), kKBS k-blocks}
+              if (has_a) tma_load_3d_pair_hint(sa, &tm_a, bar, 0, c.row0, kb * kKBS, pol_a);
             }
             if constexpr (kTrans) {
               // B [E*N, K]: this CTA's 128 output columns as K-major rows
@@ -368,10 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int hi = max(issued, theirs);
           for (int i = max(0, hi - nst); i < hi; ++i) {
             uint64_t* b = &full[i % nst];
+            // (of a stage the leader never reached, it does not know whether the
+            // peer loaded A: if not, this wait runs into its limit)
             if (i >= issued)
-              mbar_arrive_expect_tx(b, kSB);  // armed here for the peer's half alone
-            else if (i >= theirs)
-              mbar_complete_tx(b, kSB);       // the peer's half will never come
+              mbar_arrive_expect_tx(b, a_bytes + b_bytes);  // armed here for the peer's half alone
+            else if (i >= theirs)  // the peer's half will never come
+              mbar_complete_tx(b, b_bytes + (peer_has_a >> (i % nst) & 1u) * a_bytes);
             mbar_wait_drain(b, static_cast<uint32_t>(i / nst) & 1u, kDrainLimitNs);
           }
         }
@@ -415,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // one UMMA K step is 16 bf16 or 32 e4m3: 32 bytes of a K-major
                 // operand (k-block r at r * 16 KB), 2 KB of an MN-major one (k-block
                 // r at r * 8 KB)
-                const uint64_t a = ad + (kABytes >> 4) * r + 2u * kk;
+                const uint64_t a = ad + (kTrain ? 8u * p.a_box : kABytes >> 4) * r + 2u * kk;
                 const uint64_t b = kFp8 || kTrans ? bd + (kBBytes >> 4) * r + 2u * kk
                                                   : bd + 512u * r + 128u * kk;
                 const uint32_t acc_in = (r | kk) != 0 || kb != 0 ? 1u : 0u;
@@ -443,6 +457,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait_drain(drain, 0, kDrainLimitNs);
     }
+  } else if constexpr (kTrain) {
+    // --------------------------------------------- epilogue, training ----
+    // warp w reads TMEM lane quadrant w % 4 (the only one it may access) and a
+    // quarter of the tile's columns, 32 at a time
+    const int q = warp & 3;
+    const int quarter = (warp - 2) >> 2;
+    const uint32_t buf = smem_u32(col_scale) + static_cast<uint32_t>(warp - 2) * kOutBytes;
+    // 16-byte word i of row r of the buffer lies at i ^ (r / 2 & 3), as the 64-byte
+    // swizzle of the copies has it; this lane's row, and its place in the first of
+    // the four passes over 8 rows of the values before the GELU
+    const uint32_t mine = buf + 64u * lane;
+    const uint32_t swz = lane >> 1 & 3;
+    const uint32_t pass0 = buf + 64u * (lane >> 2) + 16u * ((lane & 3) ^ (lane >> 3 & 3));
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
+                                       mapa_shared(smem_u32(&tempty[1]), 0)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    while (tiles.next(c)) {
+      const int part = is_narrow(c) ? kBN / 8 : kBN / 4;
+      const int col0 = c.n0 + quarter * part;
+      // whole 32-column chunks: N is a multiple of 64
+      const int n_chunks = col0 >= p.N ? 0 : min(part / 32, (p.N - col0) / 32);
+      const int row0 = c.row0 + 32 * q;
+      const bool any = row0 < c.row_end && n_chunks > 0;
+      const bool whole = row0 + 32 <= c.row_end;
+      // Values before the GELU, 8 rows x 64 bytes with each load (a lane reading its
+      // own row would touch 32 lines with each, a clock each), a chunk ahead.
+      uint4 uv[4];
+      auto fetch_u = [&](int col) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = row0 + 8 * i + (lane >> 2);
+          uv[i] = r < c.row_end ? ld_global_cs_v4(p.U + static_cast<size_t>(r) * p.N + col + 8 * (lane & 3))
+                                : make_uint4(0, 0, 0, 0);
+        }
+      };
+      if (p.gelu == kEpiGeluGrad && any) fetch_u(col0);
+      if (!__all_sync(0xffffffffu, pair_wait(&tfull[acc], acc_phase))) break;
+      tc_fence_after();
+      const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                              static_cast<uint32_t>(acc * kBN + quarter * part);
+      // 32 columns of the warp's rows as bf16: through shared memory and out by TMA
+      // where all 32 rows are the segment's, by the lanes that have a row at its end
+      auto emit = [&](const uint32_t(&r)[32], const CUtensorMap& map, uint16_t* out, int col,
+                      bool buffer_free) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          auto two = [&](int j) {
+            return pack_bf16x2(__uint_as_float(r[8 * i + j]), __uint_as_float(r[8 * i + j + 1]));
+          };
+          v[i] = make_uint4(two(0), two(2), two(4), two(6));
+        }
+        if (whole) {
+          if (!buffer_free) {
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared_v4(mine + 16u * (i ^ swz), v[i]);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&map, buf, col, row0);
+        } else if (row0 + lane < c.row_end) {
+          uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(row0 + lane) * p.N + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_global_cs_v4(dst + i, v[i]);
+        }
+      };
+#pragma unroll 1
+      for (int cc = 0; cc < n_chunks && any; ++cc) {
+        const int col = col0 + 32 * cc;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t_base + 32u * cc, r);
+        if (p.gelu == kEpiGeluGrad) {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared_v4(pass0 + 512u * i, uv[i]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) uv[i] = ld_shared_v4(mine + 16u * (i ^ swz));
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            gelu_slope_x2(uv[i].x, r[8 * i], r[8 * i + 1]);
+            gelu_slope_x2(uv[i].y, r[8 * i + 2], r[8 * i + 3]);
+            gelu_slope_x2(uv[i].z, r[8 * i + 4], r[8 * i + 5]);
+            gelu_slope_x2(uv[i].w, r[8 * i + 6], r[8 * i + 7]);
+          }
+          if (cc + 1 < n_chunks) fetch_u(col + 32);
+          // its own row of the buffer is all that a lane read: it is free
+          emit(r, tm_out.d, p.D, col, true);
+        } else {
+          tmem_ld_wait();
+          if (p.gelu == kEpiGelu) {
+            if (p.U != nullptr) emit(r, tm_out.u, p.U, col, false);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) gelu_tanh_x2(r[i], r[i + 1]);
+          }
+          emit(r, tm_out.d, p.D, col, false);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_cluster(tempty_leader[acc]);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (lane == 0) tma_store_wait();
   } else {
     // ------------------------------------------------------ epilogue ----
     // warp w reads TMEM lane quadrant w % 4 (the only one it may access) and
@@ -452,18 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* wscale = col_scale + (warp - 2) * (kBN / 2);
     const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
                                        mapa_shared(smem_u32(&tempty[1]), 0)};
-    const uint32_t out_buf = smem_u32(col_scale) + static_cast<uint32_t>(warp - 2) * p.out_bufs * kOutBytes;
-    int out_at = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     while (tiles.next(c)) {
       const int row = c.row0 + 32 * q + lane;
       const bool valid = row < c.row_end;
-      // (training: a narrow tile's columns are shared by both warps of a quadrant)
-      const int part = kTrain && is_narrow(c) ? kBN / 4 : kBN / 2;
-      const int col0 = c.n0 + half * part;
+      const int col0 = c.n0 + half * (kBN / 2);
       // whole 32-column chunks: N is a multiple of 64
-      const int n_chunks = col0 >= p.N ? 0 : min(part / 32, (p.N - col0) / 32);
+      const int n_chunks = col0 >= p.N ? 0 : min(4, (p.N - col0) / 32);
       float rs = 1.f;
       if constexpr (kFp8) {
         // scales are fetched before the accumulator wait, hiding their latency
@@ -476,60 +597,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid) rs = p.a_scale[row];
         __syncwarp();
       }
-      // Training: 32 columns of the warp's rows as bf16. Through shared memory and
-      // out by TMA where all 32 rows are the segment's (a lane storing its own 64
-      // bytes touches 32 lines with each instruction, a clock each: 4096 clocks a
-      // tile and output); by the lanes that have a row at a segment's end.
-      auto emit = [&](const uint32_t(&r)[32], const CUtensorMap& map, uint16_t* out, int col) {
-        if constexpr (kTrain) {
-          uint4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t* w = r + 8 * i;
-            auto two = [](uint32_t a, uint32_t b) {
-              return pack_bf16x2(__uint_as_float(a), __uint_as_float(b));
-            };
-            v[i] = make_uint4(two(w[0], w[1]), two(w[2], w[3]), two(w[4], w[5]), two(w[6], w[7]));
-          }
-          if (row - lane + 32 <= c.row_end) {
-            if (lane == 0) {
-              if (p.out_bufs == 2) tma_store_wait_read<1>();
-              else tma_store_wait_read<0>();
-            }
-            __syncwarp();
-            const uint32_t buf = out_buf + out_at * kOutBytes;
-            // 16-byte word i of row r lies at i ^ (r / 2 & 3)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              st_shared_v4(buf + 64u * lane + 16u * (i ^ (lane >> 1 & 3)), v[i]);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) tma_store_2d(&map, buf, col, row);
-            out_at = p.out_bufs - 1 - out_at;
-          } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * p.N + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st_global_cs_v4(dst + i, v[i]);
-          }
-        }
-      };
-      // the first kept values are fetched before the accumulator wait, each
-      // later chunk's while the one before it is worked on
-      const uint16_t* urow = nullptr;
-      uint4 uv[4];
-      if constexpr (kTrain) {
-        if (p.gelu == kEpiGeluGrad && valid && n_chunks > 0) {
-          urow = p.U + static_cast<size_t>(row) * p.N + col0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) uv[i] = ld_global_cs_v4(urow + 8 * i);
-        }
-      }
       if (!__all_sync(0xffffffffu, pair_wait(&tfull[acc], acc_phase))) break;
       tc_fence_after();
       uint16_t* drow = p.D + static_cast<size_t>(valid ? row : 0) * p.N;
       float row_max = 0.f;  // FP8 mode: max |output| of this row in these columns
       const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                              static_cast<uint32_t>(acc * kBN + half * part);
+                              static_cast<uint32_t>(acc * kBN + half * (kBN / 2));
       // two register sets: the next chunk's TMEM load overlaps this chunk's math
       uint32_t ra[32], rb[32];
       if constexpr (kQOut) {
@@ -593,36 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t(&r)[32] = (cc & 1) ? rb : ra;
             uint32_t(&nx)[32] = (cc & 1) ? ra : rb;
             if (cc + 1 < n_chunks) tmem_ld_32x32b_x32(t_base + 32u * (cc + 1), nx);
-            if constexpr (kTrain) {
-              const int col = col0 + 32 * cc;
-              if (p.gelu == kEpiGeluGrad) {
-                uint32_t u[16];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  u[4 * i] = uv[i].x;
-                  u[4 * i + 1] = uv[i].y;
-                  u[4 * i + 2] = uv[i].z;
-                  u[4 * i + 3] = uv[i].w;
-                }
-                if (valid && cc + 1 < n_chunks) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    uv[i] = ld_global_cs_v4(urow + 32 * (cc + 1) + 8 * i);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  r[2 * i] = __float_as_uint(__uint_as_float(r[2 * i]) * gelu_slope(bf16_lo(u[i])));
-                  r[2 * i + 1] =
-                      __float_as_uint(__uint_as_float(r[2 * i + 1]) * gelu_slope(bf16_hi(u[i])));
-                }
-              } else if (p.gelu == kEpiGelu) {
-                if (p.U != nullptr) emit(r, tm_out.u, p.U, col);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  r[i] = __float_as_uint(gelu_tanh_f(__uint_as_float(r[i])));
-              }
-              emit(r, tm_out.d, p.D, col);
-            } else if (valid) {
+            if (valid) {
               uint32_t packed[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -663,9 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1u;
       }
     }
-    if constexpr (kTrain) {
-      if (lane == 0) tma_store_wait();
-    }
   }
 
   __syncwarp();
@@ -678,10 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-static size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage, int out_bufs) {
+static size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage, bool train) {
   return 1024 + static_cast<size_t>(stages) * kStageBytes * kb_per_stage +
-         (fp8 ? 4 * kEpiWarps * (kBN / 2) : 0) + kEpiWarps * out_bufs * kOutBytes +
-         8 * (2 * stages + 6) + 16 + 8 * static_cast<size_t>(E + 1);
+         (fp8 ? 4 * kEpiWarps * (kBN / 2) : 0) + (train ? kTrainEpiWarps * kOutBytes : 0) +
+         8 * (2 * stages + 6) + 16 + 6 * static_cast<size_t>(E + 1);
 }
 
 template <bool kFp8, bool kQOut, bool kGather, bool kTrans = false, bool kTrain = false>
@@ -696,22 +737,17 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
   GemmArgs args = a;
   constexpr int kbs = kGather ? 1 : kWideKB;
   args.stages = kMaxStages;
-  args.out_bufs = kTrain ? 2 : 0;
-  const auto bytes = [&] { return gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, args.out_bufs); };
-  while (args.stages > 2 && bytes() > static_cast<size_t>(optin)) {
-    // with the offsets of more than 241 experts, one output buffer a warp fits
-    // beside three stages of two k-blocks
-    if (kTrain && args.out_bufs == 2 && args.stages == 3) args.out_bufs = 1;
-    else --args.stages;
-  }
-  const size_t smem = bytes();
+  while (args.stages > 2 &&
+         gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, kTrain) > static_cast<size_t>(optin))
+    --args.stages;
+  const size_t smem = gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, kTrain);
   err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (num_sms / 2)), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(64 + 32 * epi_warps(kTrain), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];

@@ -188,7 +188,7 @@ struct GemmArgs {
   const int32_t* a_rows;   // optional: A row r is row a_rows[r] of the A tensor (a gather,
   int a_src_rows;          //   by TMA, from a tensor of a_src_rows rows); CTA-pair kernel
   int stages;              // CTA-pair kernel: pipeline depth (set by its launcher)
-  int out_bufs = 0;        // training: output buffers per epilogue warp (set by its launcher)
+  int a_box = 128;         // training: rows of the boxes A is loaded in, a multiple of 8
   uint32_t* dev_status;
   uint64_t timeout_ns;
 };

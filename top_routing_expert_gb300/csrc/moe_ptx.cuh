@@ -707,6 +707,76 @@ __device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c
   return r;
 }
 
+// ---------------------------------------------------------------- GELU ----
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN where one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// GELU-tanh of two values: 0.5 u (1 + tanh z) = u / (1 + 2^(-2 log2(e) z)), z =
+// sqrt(2/pi) (u + 0.044715 u^3). The two quotients share one reciprocal, so a
+// value takes 1.5 special-function operations (4 a clock and SM sub-partition),
+// which bound the epilogues that use it. The exponent is held at 60, so that the product of
+// the denominators stays finite, and the numerator at -7.5, from where on it is:
+// the result there is -7.5 x 2^-60 for values between that and -0, -inf's too.
+// (Choosing 0 instead: 30.1 us for the ragged 4-bit product with GELU, this 28.7.) A NaN
+// stays one, and its neighbour a value.
+__device__ __forceinline__ void gelu_tanh_x2(uint32_t& x, uint32_t& y) {
+  const float u = __uint_as_float(x), v = __uint_as_float(y);
+  const uint64_t uv = f32x2(u, v);
+  // -2 log2(e) sqrt(2/pi) (0.044715 u^2 + 1) u
+  const uint64_t e2 = f32x2_mul(uv, f32x2_fma(f32x2_mul(uv, uv), f32x2(-0.10294324f, -0.10294324f),
+                                              f32x2(-2.3022082f, -2.3022082f)));
+  float pu, pv, a, b;
+  f32x2_get(e2, pu, pv);
+  const uint64_t ab = f32x2_add(f32x2(exp2_approx(fminf(pu, 60.0f)), exp2_approx(fminf(pv, 60.0f))),
+                                f32x2(1.0f, 1.0f));
+  f32x2_get(ab, a, b);
+  const float r = rcp_approx(a * b);
+  f32x2_get(f32x2_mul(f32x2(max_nan(u, -7.5f), max_nan(v, -7.5f)), f32x2_mul(f32x2(r, r), f32x2(b, a))), a, b);
+  x = __float_as_uint(a);
+  y = __float_as_uint(b);
+}
+
+// Two accumulators times the slope of GELU-tanh at the bf16 values of uv: with s =
+// 1 / (1 + e), e = 2^(-2 log2(e) z), the slope of u s is s + u (e s) s 2 dz/du; e s^2
+// is s (1 - s) without the difference next to 1. One reciprocal for both, as above.
+// Beyond +-7 the slope is 0 or 1 to 2^-44 and u is held there; a NaN stays one, and
+// its neighbour a value.
+__device__ __forceinline__ void gelu_slope_x2(uint32_t uv, uint32_t& x, uint32_t& y) {
+  asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(uv) : "r"(0x40E040E0u));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(uv) : "r"(0xC0E0C0E0u));
+  const uint64_t u = f32x2(__uint_as_float(uv << 16), __uint_as_float(uv & 0xFFFF0000u));
+  const uint64_t sq = f32x2_mul(u, u);
+  const uint64_t e2 = f32x2_mul(u, f32x2_fma(sq, f32x2(-0.10294324f, -0.10294324f),
+                                             f32x2(-2.3022082f, -2.3022082f)));
+  float pu, pv, a, b;
+  f32x2_get(e2, pu, pv);
+  const uint64_t e = f32x2(exp2_approx(fminf(pu, 60.0f)), exp2_approx(fminf(pv, 60.0f)));
+  f32x2_get(f32x2_add(e, f32x2(1.0f, 1.0f)), a, b);
+  const float r = rcp_approx(a * b);
+  const uint64_t s = f32x2_mul(f32x2(r, r), f32x2(b, a));
+  const uint64_t dz = f32x2_fma(sq, f32x2(0.21406445f, 0.21406445f), f32x2(1.5957691f, 1.5957691f));
+  const uint64_t slope = f32x2_fma(f32x2_mul(u, f32x2_mul(e, s)), f32x2_mul(s, dz), s);
+  f32x2_get(f32x2_mul(f32x2(__uint_as_float(x), __uint_as_float(y)), slope), a, b);
+  x = __float_as_uint(a);
+  y = __float_as_uint(b);
+}
+
 // ---------------------------------------------------------------- misc ----
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
