@@ -1607,7 +1607,10 @@ moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N, const 
   g.timeout_ns = wait_timeout_ns();
   CUtensorMap tm_d, tm_u = {};
   if (!tmap_bf16_2d(&tm_d, D, N, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return MOE_ERR_CUDA;
-  if (pre != nullptr && !tmap_bf16_2d(&tm_u, pre, N, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+  const bool read_pre = epilogue == MOE_EPILOGUE_GELU_GRAD;
+  if (pre != nullptr &&
+      !tmap_bf16_2d(&tm_u, pre, N, rows, read_pre ? 64 : 32, read_pre ? 128 : 32,
+                    read_pre ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B))
     return MOE_ERR_CUDA;
   MOE_CUDA(launch_expert_gemm(tm_a, tm_b, tm_d, tm_u, g, transposed != 0, num_sms(),
                               static_cast<cudaStream_t>(stream)));

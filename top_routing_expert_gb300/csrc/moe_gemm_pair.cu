@@ -29,6 +29,8 @@
 // epilogues before reusing an accumulator.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -50,6 +52,7 @@ constexpr uint32_t kTmemCols = 2 * kBN;                  // two accumulators
 // rows x 32 bf16 columns for each.
 constexpr int kTrainEpiWarps = 16;
 constexpr uint32_t kOutBytes = 32 * 64;
+constexpr int kInference = -1;
 __host__ __device__ constexpr int epi_warps(bool train) { return train ? kTrainEpiWarps : kEpiWarps; }
 // Pair m-tiles per raster group: 16 when the experts average at least 16
 // pair m-tiles (4096 rows) and A's rows are short, so that a group stays
@@ -132,8 +135,9 @@ __device__ __forceinline__ float gelu_tanh_f(float u) {
   return __fdividef(u, 1.0f + __expf(-z2));
 }
 
-// Tensor maps of the training epilogues' outputs, D and the values before the
-// GELU: 32 rows x 32 columns, 64-byte swizzle.
+// Tensor maps of the training epilogues: D, and the values before the GELU where
+// they are written, 32 rows x 32 columns with 64-byte swizzle; where they are read
+// (prefetched to L2), 128 rows x 64 columns.
 struct OutMaps {
   CUtensorMap d, u;
 };
@@ -152,13 +156,15 @@ struct OutMaps {
 // block maximum, a second one converts and stores.
 // kTrans (bf16): B is [E][N][K], K-major like A: the product with the
 // transposed weights, as a gradient to the rows takes them.
-// kTrain (bf16): the epilogues of training (GemmArgs::gelu and U): GELU with
-// the value before it kept, or the product times GELU's slope at kept values.
-template <bool kFp8, bool kQOut, bool kGather, bool kTrans, bool kTrain>
-__global__ void __launch_bounds__(64 + 32 * epi_warps(kTrain), 1)
+// kEpi (bf16): kEpiNone, kEpiGelu (the value before it kept in U) and kEpiGeluGrad
+// (the product times GELU's slope at U) are the epilogues of training, a kernel
+// each: in one kernel their registers spilled. kInference: as GemmArgs::gelu says.
+template <bool kFp8, bool kQOut, bool kGather, bool kTrans, int kEpi>
+__global__ void __launch_bounds__(64 + 32 * epi_warps(kEpi != kInference), 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                              const __grid_constant__ CUtensorMap tm_b,
                              const __grid_constant__ OutMaps tm_out, GemmArgs p) {
+  constexpr bool kTrain = kEpi != kInference;
   constexpr int kThreads = 64 + 32 * epi_warps(kTrain);
   constexpr int kKE = kFp8 ? 128 : kBlockK;  // K elements per k-block
   constexpr int kKBS = kGather ? 1 : kWideKB;  // k-blocks per stage
@@ -296,6 +302,15 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(kTrain), 1)
         // extra columns are read and never used).
         const bool half_n = is_narrow(c);
         const int b_col = c.n0 + static_cast<int>(rank) * (half_n ? kBN / 4 : kBN / 2);
+        if constexpr (kTrain) {
+          // the values before the GELU, as far as L2: the epilogue comes to them
+          // while this warp is some tiles ahead
+          if (kEpi == kEpiGeluGrad && c.row0 < c.row_end && elect_one()) {
+            const int end = min(p.N, c.n0 + (half_n ? kBN / 2 : kBN));
+            for (int col = c.n0; col < end; col += 64) tma_prefetch_l2_2d(&tm_out.u, col, c.row0);
+          }
+          __syncwarp();
+        }
         int gr[4] = {0, 0, 0, 0};
         if constexpr (kGather) {
 #pragma unroll
@@ -483,17 +498,21 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(kTrain), 1)
       const bool any = row0 < c.row_end && n_chunks > 0;
       const bool whole = row0 + 32 <= c.row_end;
       // Values before the GELU, 8 rows x 64 bytes with each load (a lane reading its
-      // own row would touch 32 lines with each, a clock each), a chunk ahead.
-      uint4 uv[4];
-      auto fetch_u = [&](int col) {
+      // own row would touch 32 lines with each, a clock each): both chunks' on their
+      // way before the accumulator is waited for.
+      uint4 u0[4], u1[4];
+      auto fetch_u = [&](uint4(&u)[4], int col) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = row0 + 8 * i + (lane >> 2);
-          uv[i] = r < c.row_end ? ld_global_cs_v4(p.U + static_cast<size_t>(r) * p.N + col + 8 * (lane & 3))
+          u[i] = r < c.row_end ? ld_global_cs_v4(p.U + static_cast<size_t>(r) * p.N + col + 8 * (lane & 3))
                                 : make_uint4(0, 0, 0, 0);
         }
       };
-      if (p.gelu == kEpiGeluGrad && any) fetch_u(col0);
+      if (kEpi == kEpiGeluGrad && any) {
+        fetch_u(u0, col0);
+        if (n_chunks > 1) fetch_u(u1, col0 + 32);
+      }
       if (!__all_sync(0xffffffffu, pair_wait(&tfull[acc], acc_phase))) break;
       tc_fence_after();
       const uint32_t t_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
@@ -526,33 +545,34 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(kTrain), 1)
           for (int i = 0; i < 4; ++i) st_global_cs_v4(dst + i, v[i]);
         }
       };
-#pragma unroll 1
-      for (int cc = 0; cc < n_chunks && any; ++cc) {
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        if (cc >= n_chunks || !any) continue;
         const int col = col0 + 32 * cc;
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_base + 32u * cc, r);
-        if (p.gelu == kEpiGeluGrad) {
+        if constexpr (kEpi == kEpiGeluGrad) {
+          uint4(&u)[4] = cc == 0 ? u0 : u1;
           if (lane == 0) tma_store_wait_read();
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st_shared_v4(pass0 + 512u * i, uv[i]);
+          for (int i = 0; i < 4; ++i) st_shared_v4(pass0 + 512u * i, u[i]);
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) uv[i] = ld_shared_v4(mine + 16u * (i ^ swz));
+          for (int i = 0; i < 4; ++i) u[i] = ld_shared_v4(mine + 16u * (i ^ swz));
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            gelu_slope_x2(uv[i].x, r[8 * i], r[8 * i + 1]);
-            gelu_slope_x2(uv[i].y, r[8 * i + 2], r[8 * i + 3]);
-            gelu_slope_x2(uv[i].z, r[8 * i + 4], r[8 * i + 5]);
-            gelu_slope_x2(uv[i].w, r[8 * i + 6], r[8 * i + 7]);
+            gelu_slope_x2(u[i].x, r[8 * i], r[8 * i + 1]);
+            gelu_slope_x2(u[i].y, r[8 * i + 2], r[8 * i + 3]);
+            gelu_slope_x2(u[i].z, r[8 * i + 4], r[8 * i + 5]);
+            gelu_slope_x2(u[i].w, r[8 * i + 6], r[8 * i + 7]);
           }
-          if (cc + 1 < n_chunks) fetch_u(col + 32);
           // its own row of the buffer is all that a lane read: it is free
           emit(r, tm_out.d, p.D, col, true);
         } else {
           tmem_ld_wait();
-          if (p.gelu == kEpiGelu) {
+          if constexpr (kEpi == kEpiGelu) {
             if (p.U != nullptr) emit(r, tm_out.u, p.U, col, false);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) gelu_tanh_x2(r[i], r[i + 1]);
@@ -725,7 +745,7 @@ static size_t gemm_pair_smem_bytes(int E, int stages, bool fp8, int kb_per_stage
          8 * (2 * stages + 6) + 16 + 6 * static_cast<size_t>(E + 1);
 }
 
-template <bool kFp8, bool kQOut, bool kGather, bool kTrans = false, bool kTrain = false>
+template <bool kFp8, bool kQOut, bool kGather, bool kTrans = false, int kEpi = kInference>
 cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const GemmArgs& a,
                         int num_sms, cudaStream_t st, const OutMaps& tm_out = OutMaps{}) {
   // the deepest ring that fits: every stage in flight hides TMA latency
@@ -735,13 +755,14 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
   err = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (err != cudaSuccess) return err;
   GemmArgs args = a;
+  constexpr bool kTrain = kEpi != kInference;
   constexpr int kbs = kGather ? 1 : kWideKB;
   args.stages = kMaxStages;
   while (args.stages > 2 &&
          gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, kTrain) > static_cast<size_t>(optin))
     --args.stages;
   const size_t smem = gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, kTrain);
-  err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>,
+  err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kEpi>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
@@ -761,7 +782,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kTrain>, tm_a, tm_b,
+  err = cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kEpi>, tm_a, tm_b,
                            tm_out, args);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
@@ -777,9 +798,15 @@ cudaError_t launch_expert_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                                const CUtensorMap& tm_d, const CUtensorMap& tm_u, const GemmArgs& a,
                                bool transposed, int num_sms, cudaStream_t st) {
   const OutMaps out{tm_d, tm_u};
-  if (transposed)
-    return launch_pair<false, false, false, true, true>(tm_a, tm_b, a, num_sms, st, out);
-  return launch_pair<false, false, false, false, true>(tm_a, tm_b, a, num_sms, st, out);
+  const auto run = [&](auto trans) {
+    constexpr bool kT = decltype(trans)::value;
+    if (a.gelu == kEpiGelu)
+      return launch_pair<false, false, false, kT, kEpiGelu>(tm_a, tm_b, a, num_sms, st, out);
+    if (a.gelu == kEpiGeluGrad)
+      return launch_pair<false, false, false, kT, kEpiGeluGrad>(tm_a, tm_b, a, num_sms, st, out);
+    return launch_pair<false, false, false, kT, kEpiNone>(tm_a, tm_b, a, num_sms, st, out);
+  };
+  return transposed ? run(std::true_type{}) : run(std::false_type{});
 }
 
 cudaError_t launch_grouped_gemm_pair_fp8(const CUtensorMap& tm_a, const CUtensorMap& tm_b,

@@ -303,7 +303,8 @@ cudaError_t launch_grouped_gemm_pair(const CUtensorMap& tm_a, const CUtensorMap&
                                      const GemmArgs& a, int num_sms, cudaStream_t st);
 // The product alone, with W [E][K][N] or (transposed) [E][N][K] and the
 // epilogues above; CTA-pair kernel at every size. tm_d, tm_u: D and U in boxes of
-// 32 rows x 32 columns, 64-byte swizzle (tm_u unused without U).
+// 32 rows x 32 columns, 64-byte swizzle (U where it is read: 128 rows x 64 columns,
+// no swizzle; unused without U).
 cudaError_t launch_expert_gemm(const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                                const CUtensorMap& tm_d, const CUtensorMap& tm_u, const GemmArgs& a,
                                bool transposed, int num_sms, cudaStream_t st);
