@@ -167,6 +167,38 @@ def test_weight_gradient(segments, K, N, dtype, accumulate):
                 assert torch.equal(dW[e].cpu(), before[e])
 
 
+@pytest.mark.parametrize("lengths,first,behind", [([5000], 0, 0), ([2049], 3, 9), ([6300, 0, 7], 0, 5),
+                                                  ([2100, 2050], 1, 0), ([64 * 40 + 1], 0, 100),
+                                                  ([2130, 2000, 2120, 2115], 0, 0), ([10, 8200], 0, 0)])
+@pytest.mark.parametrize("K,N", [(64, 64), (256, 128), (512, 704), (1024, 192)])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.float32, False), (torch.bfloat16, False),
+                                              (torch.float32, True)])
+def test_weight_gradient_of_few_tiles(lengths, first, behind, K, N, dtype, accumulate):
+    """Long segments of few tiles, whose rows several pairs share."""
+    off = _offsets(lengths, first)
+    rows, E = off[-1] + behind, len(lengths)
+    g = torch.Generator().manual_seed(12)
+    x, y = _draw(g, rows, K), _draw(g, rows, N)
+    for t in (x, y):
+        t[:first] = float("nan")
+        t[off[-1]:] = float("inf")
+    before = torch.randn(E, K, N, generator=g).to(dtype)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    runs = []
+    for _ in range(2):
+        dW = before.to(DEV)
+        moe.moe_expert_wgrad(x.to(DEV), y.to(DEV), torch.tensor(off, dtype=torch.int32, device=DEV), dW,
+                             accumulate=accumulate, dev_status=status)
+        runs.append(dW)
+    assert int(status.item()) == 0 and torch.equal(runs[0], runs[1])
+    for e in range(E):
+        a, b = _f64(x[off[e]:off[e + 1]]), _f64(y[off[e]:off[e + 1]])
+        ref, S = a.T @ b, np.abs(a).T @ np.abs(b)
+        if accumulate:
+            S, ref = S + np.abs(_f64(before[e])), ref + _f64(before[e])
+        _check(_f64(runs[0][e]), ref, S, len(a), dtype, what=e)
+
+
 def test_nan_of_one_expert_stays_there():
     g, off, offsets, rows, x, y = _case("steps", 5, 128, 128)
     x[off[2], 3] = float("nan")

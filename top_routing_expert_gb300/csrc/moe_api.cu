@@ -1645,6 +1645,7 @@ moe_status moe_expert_wgrad(int64_t E, int64_t rows, int64_t K, int64_t N, const
   a.K = static_cast<int>(K);
   a.N = static_cast<int>(N);
   a.rows = static_cast<int>(rows);
+  a.dW = dW;
   a.bf16_out = dtype == MOE_DTYPE_BF16;
   a.accumulate = accumulate;
   a.dev_status = dev_status;

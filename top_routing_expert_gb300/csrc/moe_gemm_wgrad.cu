@@ -51,9 +51,17 @@ constexpr int kGroup = 8;           // m-tiles per raster group
 // adds up over a long segment: 9e-6 of the result after 8192 rows. The epilogue
 // adds the pieces with rounding.
 constexpr int kPiece = 8;
+// Segments of this many rows on average are split over pairs where their tiles are
+// too few for all: over four where there is one tile for eight pairs, over two where
+// there is one for two (clusters of eight CTAs do not pack as well: 16 tiles of 2048
+// rows took 22.7 us in them, two rounds). Unsplit and split: 1 tile of 1024 rows
+// 10.9, 11.8 us, of 2048 15.1, 12.8, of 8192 40.8, 19.5; 30 tiles of 8192 rows 42.4,
+// 30.5; 16 of 32768 (a router's gradient, 4096 x 64) 138, 75.
+constexpr int kSplitRows = 2048;
 
 struct WgTile {
   int lo, len, m0, n0, e;
+  int empty;  // the whole segment is
 };
 
 __device__ __forceinline__ WgTile decode_wg(int L, const int* offs, const uint8_t* order, int mt,
@@ -63,6 +71,7 @@ __device__ __forceinline__ WgTile decode_wg(int L, const int* offs, const uint8_
   t.e = order[L / per_e];
   t.lo = offs[t.e];
   t.len = offs[t.e + 1] - t.lo;
+  t.empty = t.len == 0;
   const int r = L % per_e;
   const int g = r / (kGroup * nt);
   const int gsz = min(kGroup, mt - g * kGroup);
@@ -79,17 +88,26 @@ struct TileWalk {
   const int* offs;
   const uint8_t* order;
   int mt, nt, total, stride, L, at;
+  int part, parts;  // which of how many pieces of a segment's stages
   WgTile mine;
 
   __device__ __forceinline__ TileWalk(const int* offs_, const uint8_t* order_, int mt_, int nt_,
-                                      int total_, int first, int stride_)
-      : offs(offs_), order(order_), mt(mt_), nt(nt_), total(total_), stride(stride_), L(first), at(32) {}
+                                      int total_, int first, int stride_, int part_, int parts_)
+      : offs(offs_), order(order_), mt(mt_), nt(nt_), total(total_), stride(stride_), L(first), at(32),
+        part(part_), parts(parts_) {}
 
   __device__ __forceinline__ bool next(WgTile& t) {
     if (L >= total) return false;
     if (at == 32) {
       const int l = min(L + static_cast<int>(threadIdx.x & 31) * stride, total - 1);
       mine = decode_wg(l, offs, order, mt, nt);
+      if (parts > 1) {
+        const int nk = (mine.len + kDepth - 1) / kDepth;
+        const int first = static_cast<int>(static_cast<int64_t>(nk) * part / parts) * kDepth;
+        const int last = static_cast<int>(static_cast<int64_t>(nk) * (part + 1) / parts) * kDepth;
+        mine.lo += first;
+        mine.len = min(mine.len, last) - first;
+      }
       at = 0;
     }
     t.lo = __shfl_sync(0xffffffffu, mine.lo, at);
@@ -97,6 +115,7 @@ struct TileWalk {
     t.m0 = __shfl_sync(0xffffffffu, mine.m0, at);
     t.n0 = __shfl_sync(0xffffffffu, mine.n0, at);
     t.e = __shfl_sync(0xffffffffu, mine.e, at);
+    t.empty = __shfl_sync(0xffffffffu, mine.empty, at);
     ++at;
     L += stride;
     return true;
@@ -116,7 +135,8 @@ __device__ __forceinline__ bool is_tail(int len, int kb) {
 // (a lane that issued alone in a diverged warp, its descriptors built on the way,
 // took 185 clocks per UMMA of 128: 852 us instead of 788 for 128 experts).
 __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint64_t xd, uint32_t idesc, bool add,
-                                            int steps, uint64_t* release, uint64_t* done) {
+                                            int steps, uint64_t* release, uint64_t* done,
+                                            uint16_t pair_mask) {
   constexpr uint64_t kG = kOpBytes >> 4;
   if (elect_one()) {
     umma_bf16_pair(d_tmem, xd, xd + kG, idesc, add ? 1u : 0u);
@@ -128,12 +148,17 @@ __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint64_t xd, uint32
       for (uint32_t k = 1; k < static_cast<uint32_t>(steps); ++k)
         umma_bf16_pair(d_tmem, xd + 128u * k, xd + kG + 128u * k, idesc, 1u);
     }
-    umma_commit_pair_multicast(release, 0x3);
-    if (done != nullptr) umma_commit_pair_multicast(done, 0x3);
+    umma_commit_pair_multicast(release, pair_mask);
+    if (done != nullptr) umma_commit_pair_multicast(done, pair_mask);
   }
   __syncwarp();
 }
 
+// kSplit: a cluster of kSplit pairs works on one tile, each on a part of the
+// segment's stages. The parts' sums then lie in shared memory (the ring's, by then
+// idle) as [column / 4][row] of four, and each pair adds up, in the pairs' order,
+// the columns that it stores. One tile to a cluster at most.
+template <int kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_g,
                  const __grid_constant__ CUtensorMap tm_d, WgradArgs p) {
@@ -156,9 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.E;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t cta = cluster_ctarank();
+  const uint32_t rank = cta & 1u, lead = cta & ~1u;  // in the pair; the pair's leader
   const bool leader = rank == 0;
-  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
+  const int part = static_cast<int>(cta >> 1);
+  const int cluster = blockIdx.x / (2 * kSplit), n_clusters = gridDim.x / (2 * kSplit);
 
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -213,14 +241,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mt = (p.K + kTile - 1) / kTile, nt = (p.N + kTile - 1) / kTile;
   const int total = E * mt * nt;
   const WaitCtl wc{abort_flag, p.dev_status, p.timeout_ns};
-  const uint32_t peer_abort = mapa_shared(smem_u32(abort_flag), rank ^ 1u);
+  const uint32_t peer_abort = mapa_shared(smem_u32(abort_flag), cta ^ 1u);
   auto pair_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (mbar_wait(bar, parity, wc)) return true;
     st_u32_cluster(peer_abort, 1u);
     return false;
   };
 
-  TileWalk tiles(offs, order, mt, nt, total, cluster, n_clusters);
+  TileWalk tiles(offs, order, mt, nt, total, cluster, n_clusters, part, kSplit);
   WgTile c;
   if (warp == 0) {
     {
@@ -255,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t bar;
             if (tail) {
               mbar_arrive_expect_tx(&tail_ld[stage], kStageBytes);
-              bar = mapa_shared(smem_u32(&tail_ld[stage]), rank);
+              bar = mapa_shared(smem_u32(&tail_ld[stage]), cta);
             } else {
               if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
-              bar = mapa_shared(smem_u32(&full[stage]), 0);
+              bar = mapa_shared(smem_u32(&full[stage]), lead);
             }
             uint8_t* sx = smem + stage * kStageBytes;
             const int row = c.lo + kb * kDepth;
@@ -284,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane != 0) {
         // lane 0 does the rest
       } else if (!leader) {
-        st_async_u32_cluster(mapa_shared(smem_u32(peer_issued), 0), static_cast<uint32_t>(issued),
-                             mapa_shared(smem_u32(xbar), 0));
+        st_async_u32_cluster(mapa_shared(smem_u32(peer_issued), lead), static_cast<uint32_t>(issued),
+                             mapa_shared(smem_u32(xbar), lead));
         for (int i = max(0, issued - kStages); i < issued; ++i) {
           const int s = i % kStages;
           if (was_tail >> s & 1u) mbar_wait_drain(&tail_ld[s], (tail_par >> s & 1u) ^ 1u, kDrainLimitNs);
@@ -352,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int steps = min(kDepth / 16, (c.len - kb * kDepth + 15) / 16);
           const bool piece_end = in_piece == kPiece - 1 || kb == nk - 1;
           issue_stage(d_tmem, xd, idesc, in_piece != 0, steps, &empty[stage],
-                      piece_end ? &tfull[acc] : nullptr);
+                      piece_end ? &tfull[acc] : nullptr, pair_mask);
           if (++stage == kStages) stage = 0;
           if (piece_end && ++acc == 2) {
             acc = 0;
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           st_shared_v4(at + b * kBlockBytes + 16u * i, make_uint4(0, 0, 0, 0));
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive_release_shared(mapa_shared(smem_u32(&tail_ok[s]), 0));
+      if (lane == 0) mbar_arrive_release_shared(mapa_shared(smem_u32(&tail_ok[s]), lead));
     }
   } else {
     // ------------------------------------------------------ epilogue ----
@@ -402,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this lane's row of the buffer: 128 bytes in eight 16-byte words, word w at
     // w ^ (row & 7) as the 128-byte swizzle of the store has it
     const uint32_t my = buf + 128u * lane;
-    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
-                                       mapa_shared(smem_u32(&tempty[1]), 0)};
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), lead),
+                                       mapa_shared(smem_u32(&tempty[1]), lead)};
     int acc = 0;
     uint32_t acc_phase = 0;
     bool aborted = false;
     while (!aborted && tiles.next(c)) {
-      if (c.len == 0 && p.accumulate) continue;
+      if (c.empty && p.accumulate) continue;
       const int row = c.m0 + static_cast<int>(rank) * (kTile / 2) + 32 * q;
       const int col0 = c.n0 + half * (kTile / 2);
       // whole 32-column chunks: N and K are multiples of 64
@@ -442,6 +470,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (aborted) break;
+      if constexpr (kSplit > 1) {
+        const uint32_t at = smem_u32(smem) + 16u * (128 * 32 * half + 32 * q + lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          st_shared_v4(at + 16u * 128 * i,
+                       make_uint4(__float_as_uint(sum[4 * i]), __float_as_uint(sum[4 * i + 1]),
+                                  __float_as_uint(sum[4 * i + 2]), __float_as_uint(sum[4 * i + 3])));
+        continue;
+      }
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
         if (cc < n_chunks) {
@@ -487,6 +524,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) tma_store_wait();
   }
 
+  if constexpr (kSplit > 1) {
+    __syncwarp();
+    cluster_sync();  // every pair's sums are in place
+    TileWalk again(offs, order, mt, nt, total, cluster, n_clusters, part, kSplit);
+    if (warp >= kFirstEpi && again.next(c) && !(c.empty && p.accumulate)) {
+      constexpr int kCols = kTile / kSplit / 2;  // of each warp
+      const int local = 32 * (warp & 3) + lane;
+      const int row = c.m0 + static_cast<int>(rank) * (kTile / 2) + local;
+      const int first = part * (kTile / kSplit) + ((warp - kFirstEpi) >> 2) * kCols;
+#pragma unroll 1
+      for (int cc = 0; cc < kCols && c.n0 + first + cc < p.N && row < p.K; cc += 32) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        for (uint32_t pair = 0; pair < kSplit; ++pair) {
+          const uint32_t at = mapa_shared(
+              smem_u32(smem) + 16u * (128 * ((first + cc) / 4) + local), 2 * pair + rank);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 f = ld_shared_cluster_v4(at + 16u * 128 * i);
+            v[4 * i] += f.x;
+            v[4 * i + 1] += f.y;
+            v[4 * i + 2] += f.z;
+            v[4 * i + 3] += f.w;
+          }
+        }
+        const size_t at = (static_cast<size_t>(c.e) * p.K + row) * p.N + c.n0 + first + cc;
+        if (p.bf16_out) {
+          uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dW) + at);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            d[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                              pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                              pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+        } else {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.dW) + at);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (p.accumulate) {
+              const float4 o = d[i];
+              f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
+            }
+            d[i] = f;
+          }
+        }
+      }
+    }
+  }
+
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -502,28 +589,44 @@ size_t wgrad_smem_bytes(int E) {
 
 }  // namespace
 
-cudaError_t launch_wgrad(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
+namespace {
+
+template <int kSplit>
+cudaError_t launch_split(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
                          const WgradArgs& a, int num_sms, cudaStream_t st) {
   const size_t smem = wgrad_smem_bytes(a.E);
-  cudaError_t err = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t err = cudaFuncSetAttribute(wgrad_kernel<kSplit>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (num_sms / 2)), 1, 1);
+  constexpr int kCluster = 2 * kSplit;
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / kCluster * kCluster), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, wgrad_kernel, tm_x, tm_g, tm_d, a);
+  err = cudaLaunchKernelEx(&cfg, wgrad_kernel<kSplit>, tm_x, tm_g, tm_d, a);
   return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_wgrad(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
+                         const WgradArgs& a, int num_sms, cudaStream_t st) {
+  const int64_t tiles = static_cast<int64_t>(a.E) * ((a.K + kTile - 1) / kTile) * ((a.N + kTile - 1) / kTile);
+  const int64_t rows = a.rows / a.E;
+  if (rows >= kSplitRows && tiles <= num_sms / 16) return launch_split<4>(tm_x, tm_g, tm_d, a, num_sms, st);
+  if (rows >= kSplitRows && tiles <= num_sms / 4) return launch_split<2>(tm_x, tm_g, tm_d, a, num_sms, st);
+  return launch_split<1>(tm_x, tm_g, tm_d, a, num_sms, st);
 }
 
 }  // namespace moe

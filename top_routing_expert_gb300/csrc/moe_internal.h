@@ -197,7 +197,8 @@ struct GemmArgs {
 struct WgradArgs {
   const int32_t* offsets;  // [E+1] row segments
   int E, K, N, rows;
-  int bf16_out;            // dW [E,K,N] is bf16, otherwise fp32
+  void* dW;                // [E,K,N] (the split kernels; otherwise by tensor map)
+  int bf16_out;            // dW is bf16, otherwise fp32
   int accumulate;          // fp32: add to dW
   uint32_t* dev_status;
   uint64_t timeout_ns;

@@ -635,6 +635,16 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
   return v;
 }
 
+// 16 bytes of shared memory of a CTA of the cluster.
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
 // 2-D tiled TMA store from shared memory, a bulk group of the issuing thread.
 // `wait_read` returns when its groups no longer read shared memory, `wait` when
 // they are complete.
