@@ -854,6 +854,17 @@ def moe_expert_gemm_mx4(x_q, x_scale, offsets, Wq, w_scale, out, gelu=False, dev
 _EPILOGUES = {None: 0, "gelu": 1, "gelu_grad": 2}
 
 
+def _sized(t: Optional[torch.Tensor], dtype, name: str, dev: int, shape) -> Optional[int]:
+    """As _ptr, for a tensor that has to be of this shape (or None)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        return _ptr(t, dtype, name)   # raises with the reason
+    return t.data_ptr()
+
+
 def moe_expert_gemm(x, offsets, W, out, transposed=False, epilogue=None, pre=None, dev_status=None,
                     stream=None):
     """out [rows, N] bf16 = each row of x [rows, K] times its expert's weights W
@@ -866,18 +877,16 @@ def moe_expert_gemm(x, offsets, W, out, transposed=False, epilogue=None, pre=Non
     if x.dim() != 2 or W.dim() != 3:
         raise ValueError("x must be [rows, K] and W [E, K, N] or, transposed, [E, N, K]")
     rows, K = x.shape
-    E, Kw, N = (W.shape[0], W.shape[2], W.shape[1]) if transposed else W.shape
+    E, Kw, N = W.shape
+    if transposed:
+        Kw, N = N, Kw
     if K != Kw:
         raise ValueError(f"x has K = {K}, W has K = {Kw}")
-    for t, name in ((out, "out"), (pre, "pre")):
-        if t is not None and t.shape != (rows, N):
-            raise ValueError(f"{name} must be [rows, N] = [{rows}, {N}], got {list(t.shape)}")
-    dev = _device_of(x, "x")
-    bf16 = torch.bfloat16
+    dev, bf16, shape = _device_of(x, "x"), torch.bfloat16, (rows, N)
     _check("moe_expert_gemm", load_library().moe_expert_gemm(
         E, rows, K, N, _address(x, bf16, "x", dev), _ptr(offsets, torch.int32, "offsets", E + 1),
         _address(W, bf16, "W", dev), 1 if transposed else 0, _EPILOGUES[epilogue],
-        None if pre is None else _address(pre, bf16, "pre", dev), _address(out, bf16, "out", dev),
+        _sized(pre, bf16, "pre", dev, shape), _sized(out, bf16, "out", dev, shape),
         _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
 
 
@@ -898,7 +907,7 @@ def moe_expert_wgrad(x, grad, offsets, dW, accumulate=False, dev_status=None, st
     _check("moe_expert_wgrad", load_library().moe_expert_wgrad(
         E, rows, K, N, _address(x, torch.bfloat16, "x", dev),
         _address(grad, torch.bfloat16, "grad", dev), _ptr(offsets, torch.int32, "offsets", E + 1),
-        _address(dW, dW.dtype, "dW", dev), 1 if dW.dtype == torch.bfloat16 else 0,
+        _address(dW, dW.dtype, "dW", dev), 1 if dW.dtype is torch.bfloat16 else 0,
         1 if accumulate else 0, _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
 
 
@@ -920,12 +929,12 @@ class BlockWorkspace:
         self.buf = torch.empty(max(self.nbytes, 16), dtype=torch.uint8, device=device)
 
 
-def _block(cfg: BlockConfig, stream_t, name, y, dest_row, topk_w, post_weight, gate, pre_weight):
-    """The moe_block of a call and the addresses of the arguments that both
-    directions share; stream_t [T, H] gives the sizes."""
-    if stream_t.dim() != 2:
+def _block(cfg: BlockConfig, like, name, y, dest_row, topk_w, post_weight, gate, pre_weight):
+    """The moe_block of a call, the addresses of the arguments that both
+    directions share, and the device; like [T, H] gives the sizes."""
+    if like.dim() != 2:
         raise ValueError(f"{name} must be [T, H]")
-    T, H = stream_t.shape
+    T, H = like.shape
     rows, k = 0, 1
     if y is not None:
         if y.dim() != 2 or y.shape[1] != H:
@@ -935,22 +944,12 @@ def _block(cfg: BlockConfig, stream_t, name, y, dest_row, topk_w, post_weight, g
         if dest_row.dim() != 2 or dest_row.shape[0] != T:
             raise ValueError(f"dest_row must be [{T}, k], got {list(dest_row.shape)}")
         k = dest_row.shape[1]
-    if topk_w is not None and topk_w.shape != (T, k):
-        raise ValueError(f"topk_w must be [T, k] = [{T}, {k}], got {list(topk_w.shape)}")
-    f32 = torch.float32
-    for t, n, want in ((post_weight, "post_weight", (H,)), (pre_weight, "pre_weight", (H,)),
-                       (gate, "gate", (T,))):
-        if t is not None and t.shape != want:
-            raise ValueError(f"{n} must be {list(want)}, got {list(t.shape)}")
-    b = _Block(T, H, rows, k, cfg.post_norm, cfg.residual_scale, cfg.eps)
-    return b, (_ptr(y, torch.bfloat16, "y"), _ptr(dest_row, torch.int32, "dest_row"),
-               _ptr(topk_w, f32, "topk_w"), _ptr(post_weight, f32, "post_weight"),
-               _ptr(gate, f32, "gate"), _ptr(pre_weight, f32, "pre_weight"))
-
-
-def _same_shape(t, like, name):
-    if t is not None and t.shape != like.shape:
-        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+    f32, dev = torch.float32, _device_of(like, name)
+    return _Block(T, H, rows, k, cfg.post_norm, cfg.residual_scale, cfg.eps), (
+        None if y is None else _address(y, torch.bfloat16, "y", dev),
+        None if dest_row is None else _address(dest_row, torch.int32, "dest_row", dev),
+        _sized(topk_w, f32, "topk_w", dev, (T, k)), _sized(post_weight, f32, "post_weight", dev, (H,)),
+        _sized(gate, f32, "gate", dev, (T,)), _sized(pre_weight, f32, "pre_weight", dev, (H,))), dev
 
 
 def moe_block_norm(cfg: BlockConfig, residual, y, out, xn=None, dest_row=None, topk_w=None,
@@ -958,13 +957,12 @@ def moe_block_norm(cfg: BlockConfig, residual, y, out, xn=None, dest_row=None, t
     """out [T, H] = residual_scale * residual + gate * norm(sum_j topk_w_j
     y[dest_row_j]) * post_weight, xn [T, H] = norm(out) * pre_weight (bf16; see
     moe_block_norm in the header for what may be None)."""
-    b, shared = _block(cfg, residual, "residual", y, dest_row, topk_w, post_weight, gate, pre_weight)
-    bf16 = torch.bfloat16
-    _same_shape(out, residual, "out")
-    _same_shape(xn, residual, "xn")
+    b, shared, dev = _block(cfg, residual, "residual", y, dest_row, topk_w, post_weight, gate,
+                            pre_weight)
+    bf16, shape = torch.bfloat16, residual.shape
     _check("moe_block_norm", load_library().moe_block_norm(
-        ctypes.byref(b), _ptr(residual, bf16, "residual"), *shared, _ptr(out, bf16, "out"),
-        _ptr(xn, bf16, "xn"), _stream(stream)))
+        ctypes.byref(b), _address(residual, bf16, "residual", dev), *shared,
+        _sized(out, bf16, "out", dev, shape), _sized(xn, bf16, "xn", dev, shape), _stream(stream)))
 
 
 def moe_block_norm_bwd(cfg: BlockConfig, h, y, grad_out, grad_residual, grad_y, grad_xn=None,
@@ -974,23 +972,20 @@ def moe_block_norm_bwd(cfg: BlockConfig, h, y, grad_out, grad_residual, grad_y, 
     """Gradient of moe_block_norm from grad_out and grad_xn [T, H] (bf16, either
     may be None), h [T, H] being what the forward wrote as out. Gradients that
     are None are not formed; ws is needed for grad_post and grad_pre."""
-    b, shared = _block(cfg, h, "h", y, dest_row, topk_w, post_weight, gate, pre_weight)
-    bf16, f32 = torch.bfloat16, torch.float32
-    for t, n in ((grad_out, "grad_out"), (grad_xn, "grad_xn"), (grad_residual, "grad_residual")):
-        _same_shape(t, h, n)
-    if grad_y is not None and (y is None or grad_y.shape != y.shape):
-        raise ValueError("grad_y must have the shape of y")
-    for t, n, want in ((grad_topk_w, "grad_topk_w", (b.T, b.top_k)), (grad_post, "grad_post", (b.H,)),
-                       (grad_pre, "grad_pre", (b.H,)), (grad_gate, "grad_gate", (b.T,))):
-        if t is not None and t.shape != want:
-            raise ValueError(f"{n} must be {list(want)}, got {list(t.shape)}")
-    wp, wn = (None, 0) if ws is None else (_ptr(ws.buf, torch.uint8, "ws"), ws.nbytes)
+    b, shared, dev = _block(cfg, h, "h", y, dest_row, topk_w, post_weight, gate, pre_weight)
+    bf16, f32, shape = torch.bfloat16, torch.float32, h.shape
+    T, H, k = b.T, b.H, b.top_k
+    if grad_y is not None and y is None:
+        raise ValueError("grad_y without y")
+    wp, wn = (None, 0) if ws is None else (_ptr(ws.buf, torch.uint8, "ws", ws.nbytes), ws.nbytes)
     _check("moe_block_norm_bwd", load_library().moe_block_norm_bwd(
-        ctypes.byref(b), _ptr(h, bf16, "h"), *shared, _ptr(grad_out, bf16, "grad_out"),
-        _ptr(grad_xn, bf16, "grad_xn"), _ptr(grad_residual, bf16, "grad_residual"),
-        _ptr(grad_y, bf16, "grad_y"), _ptr(grad_topk_w, f32, "grad_topk_w"),
-        _ptr(grad_post, f32, "grad_post"), _ptr(grad_gate, f32, "grad_gate"),
-        _ptr(grad_pre, f32, "grad_pre"), wp, wn, _stream(stream)))
+        ctypes.byref(b), _address(h, bf16, "h", dev), *shared,
+        _sized(grad_out, bf16, "grad_out", dev, shape), _sized(grad_xn, bf16, "grad_xn", dev, shape),
+        _sized(grad_residual, bf16, "grad_residual", dev, shape),
+        _sized(grad_y, bf16, "grad_y", dev, y.shape if y is not None else None),
+        _sized(grad_topk_w, f32, "grad_topk_w", dev, (T, k)),
+        _sized(grad_post, f32, "grad_post", dev, (H,)), _sized(grad_gate, f32, "grad_gate", dev, (T,)),
+        _sized(grad_pre, f32, "grad_pre", dev, (H,)), wp, wn, _stream(stream)))
 
 
 # ------------------------------------------------- expert parallelism ----

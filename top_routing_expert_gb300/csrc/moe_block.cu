@@ -652,9 +652,11 @@ cudaError_t launch_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cud
   const int dyn = stages * stage + weights;
   const int per_sm = resident(stages);
   const auto kernel = block_bwd_kernel<G, NV, KMAX, kStaged, kFull, MB>;
-  const cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
-  if (err != cudaSuccess) return err;
+  if (dyn > 48 * 1024) {  // more than a kernel may have without asking
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
+    if (err != cudaSuccess) return err;
+  }
   const int64_t need = (a.T + kPer - 1) / kPer, cap = static_cast<int64_t>(num_sms) * per_sm;
   int blocks = static_cast<int>(need < cap ? need : cap);
   if (blocks * kPer > kBlockMaxGroups) blocks = kBlockMaxGroups / kPer;
