@@ -10,7 +10,8 @@ Outputs are held to twice that, 2^-8 sqrt(32 / 3) of the 2-norm. A factor or a
 term that is missing shows as much more. The router's gradient comes from g_w_tj =
 <g_c, y_j>, a sum over H products that cancel: its error goes by m_tj, the 2-norm
 of the products, whatever is left of their sum, and the logits' by w_j (m_tj +
-sum_i w_i m_ti), which the token's xn multiplies."""
+sum_i w_i m_ti), which the token's xn multiplies (the gate's gradient) or not (its
+bias')."""
 import numpy as np
 import pytest
 import torch
@@ -36,7 +37,7 @@ def _make(T, H, E, k, h, cf, score, post_norm, scale, seed):
     bf = lambda *n, std=1.0: (std * torch.randn(n, generator=g)).to(torch.bfloat16).to(DEV)
     f32 = lambda *n: torch.randn(n, generator=g).to(DEV)
     w = BlockWeights(bf(E, H, h, std=H ** -0.5), bf(E, h, H, std=h ** -0.5), bf(H, E, std=H ** -0.5),
-                     1 + 0.2 * f32(H), 1 + 0.2 * f32(H))
+                     1 + 0.2 * f32(H), 1 + 0.2 * f32(H), 0.5 * f32(E) if T % 2 else None)
     block = TrainBlock(moe.MoeShape.make(T, H, E, k, h, cf), moe.RouteConfig.make(score),
                        moe.BlockConfig.make(post_norm=post_norm, residual_scale=scale, eps=1e-5))
     data = {"h": bf(T, H), "xn": bf(T, H), "gate": torch.rand(T, generator=g).to(DEV),
@@ -53,8 +54,9 @@ def _step(block, w, d, grads=None, accumulate=False):
     block.forward(d["h"], d["xn"], w, out, xn, token_gate=d["gate"])
     block.backward(d["g_out"], d["g_xn"], gh, gx, grads, grad_token_gate=g_gate,
                    grad_aux=d["g_aux"], accumulate=accumulate)
-    return {"out": out, "xn_next": xn, "h": gh, "xn": gx, "token_gate": g_gate, "W1": grads.W1,
-            "W2": grads.W2, "gate": grads.gate, "post": grads.post, "pre": grads.pre}
+    res = {"out": out, "xn_next": xn, "h": gh, "xn": gx, "token_gate": g_gate, "W1": grads.W1,
+           "W2": grads.W2, "gate": grads.gate, "post": grads.post, "pre": grads.pre}
+    return res if w.gate_bias is None else res | {"gate_bias": grads.gate_bias}
 
 
 def _reference(block, w, d, score, post_norm, scale):
@@ -64,6 +66,9 @@ def _reference(block, w, d, score, post_norm, scale):
     s, eps = block.shape, 1e-5
     idx, dest = block.topk_idx.long(), block.dest_row
     logits = v["xn"] @ v["gate"]
+    if w.gate_bias is not None:
+        v["gate_bias"] = f64(w.gate_bias)
+        logits = logits + v["gate_bias"]
     p = torch.softmax(logits, 1) if score == "softmax" else torch.sigmoid(logits)
     chosen = p.gather(1, idx)
     weights = chosen / chosen.sum(1, keepdim=True)
@@ -87,7 +92,8 @@ def _reference(block, w, d, score, post_norm, scale):
     m = (g_c[:, None] * y).norm(dim=2)
     wt = weights.detach()
     per_logit = wt * (m + (wt * m).sum(1, keepdim=True))
-    router = (d["xn"].double().norm(dim=1) * per_logit.norm(dim=1)).norm().item()
+    router = {"gate": (d["xn"].double().norm(dim=1) * per_logit.norm(dim=1)).norm().item(),
+              "gate_bias": per_logit.norm().item()}
     return {"out": out, "xn_next": xn} | dict(zip(names, found)), router
 
 
@@ -112,7 +118,7 @@ def test_step(case):
     want, router = _reference(block, w, d, score, post_norm, scale)
     for n, ref in want.items():
         err, size = (got[n].double() - ref).norm().item(), ref.norm().item()
-        assert err <= TOL * (size + (router if n == "gate" else 0.0)) + 1e-6, (n, err / size)
+        assert err <= TOL * (size + router.get(n, 0.0)) + 1e-6, (n, err / size)
 
 
 def test_accumulation_graph_and_streams():

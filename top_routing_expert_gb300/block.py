@@ -14,7 +14,7 @@ and of the balance loss:
   gradients, weights 1; 1. moe_route_grouped_bwd, and the router's own two
   products as those of a single expert.
 Every step runs in the library's kernels on the current stream but for the sum
-of the two gradients that reach xn; nothing synchronises with the host, so both
+of the two gradients that reach xn and that of the gate's bias; nothing synchronises with the host, so both
 directions can be captured in a CUDA graph. A small run of it all:
 python -m top_routing_expert_gb300.block
 """
@@ -32,15 +32,18 @@ from . import (BlockConfig, BlockWorkspace, MoeShape, RouteConfig, Workspace, _s
 class BlockWeights:
     """Weights of a block, or (zeros) their gradients: W1 [E, H, h], W2 [E, h, H]
     and gate [H, E] (bf16; gradients fp32), post and pre [H] fp32 (the norm of
-    the block's output, and the one that the next block begins with)."""
+    the block's output, and the one that the next block begins with), gate_bias
+    [E] fp32 or None."""
 
-    def __init__(self, W1, W2, gate, post, pre):
+    def __init__(self, W1, W2, gate, post, pre, gate_bias=None):
         self.W1, self.W2, self.gate, self.post, self.pre = W1, W2, gate, post, pre
+        self.gate_bias = gate_bias
 
     @classmethod
     def zeros_like(cls, w: "BlockWeights") -> "BlockWeights":
         z = lambda t: torch.zeros(t.shape, dtype=torch.float32, device=t.device)
-        return cls(z(w.W1), z(w.W2), z(w.gate), z(w.post), z(w.pre))
+        return cls(z(w.W1), z(w.W2), z(w.gate), z(w.post), z(w.pre),
+                   None if w.gate_bias is None else z(w.gate_bias))
 
 
 class TrainBlock:
@@ -89,7 +92,7 @@ class TrainBlock:
             for t in (self.routed_counts, self.P, self.aux, self.kept_counts, self.offsets):
                 t.zero_()
             return out
-        moe_route(s, xn, w.gate, None, self.topk_idx, self.topk_w, logits_out=self.logits,
+        moe_route(s, xn, w.gate, w.gate_bias, self.topk_idx, self.topk_w, logits_out=self.logits,
                   dev_status=st, ws=ws)
         moe_route_grouped(s, self.route, self.logits, select_bias, self.topk_idx, self.topk_w,
                           routed_counts=self.routed_counts, P=self.P, aux=self.aux,
@@ -115,8 +118,10 @@ class TrainBlock:
         s, st = self.shape, self.dev_status
         xn, w, out, token_gate = self._kept
         if s.T == 0:
-            for t in (grads.post, grads.pre, grads.gate) + (() if accumulate else (grads.W1, grads.W2)):
-                t.zero_()
+            for t in (grads.post, grads.pre, grads.gate, grads.gate_bias,
+                      None if accumulate else grads.W1, None if accumulate else grads.W2):
+                if t is not None:
+                    t.zero_()
             return
         if grad_xn_next is None:
             grads.pre.zero_()
@@ -138,7 +143,10 @@ class TrainBlock:
         moe_route_grouped_bwd(s, self.route, self.logits, self.topk_idx, self.g_topk_w,
                               self.g_logits, grad_aux=grad_aux,
                               routed_counts=self.routed_counts if grad_aux is not None else None)
-        # the router is a product with a single expert: logits = xn . gate
+        if w.gate_bias is not None:
+            torch.sum(self.g_logits, 0, out=grads.gate_bias)
+        # the router is a product with a single expert, logits = xn . gate, and its
+        # gradient enters the two products in bf16 like every other operand
         self.g_scores[:, :s.E].copy_(self.g_logits)
         self.gate_wide[:, :s.E].copy_(w.gate)
         moe_expert_gemm(self.g_scores, self.one_segment, self.gate_wide[None], self.g_router,

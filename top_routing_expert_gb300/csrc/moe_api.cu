@@ -1576,8 +1576,6 @@ moe_status moe_expert_gemm(int64_t E, int64_t rows, int64_t K, int64_t N, const 
       epilogue != MOE_EPILOGUE_GELU_GRAD)
     return MOE_ERR_SHAPE;
   if (epilogue == MOE_EPILOGUE_NONE && pre != nullptr) return MOE_ERR_SHAPE;
-  // W [E][N][K] is read as one matrix of E * N rows
-  if (transposed && E * N >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   MOE_REQUIRE(x);
   MOE_REQUIRE(offsets);
