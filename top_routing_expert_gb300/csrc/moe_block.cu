@@ -16,9 +16,12 @@
 //   g_y[dest_j] = w_j g_c,  g_w_j = <g_c, y_j>
 //
 // All sums are fp32 in a fixed order; every value is rounded once, when it is
-// stored. Both kernels are bound by their bytes: a token's rows are read once
-// from HBM, the statistics come from registers, and the gradient's second look
-// at y_j (for g_w) finds it in L1 or L2.
+// stored. Both kernels read a token's rows once from HBM and are bound by their
+// bytes, the gradient nearly so: 32768 tokens of 4096 with two rows each, a tenth of
+// them dropped, take 197 us (6.3 TB/s of DRAM traffic; a copy has 6.7) and 362 us (5.5
+// TB/s); 16383 of 2048 with six rows 98 and 200 us; one token 3.5 us. In
+// the gradient 16 warps to an SM issue in half of the clocks; the rest is the
+// latency of shared memory and of three sums over the block.
 #include "moe_internal.h"
 #include "moe_ptx.cuh"
 
@@ -648,6 +651,8 @@ cudaError_t launch_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cud
     const int n = kSmSharedBytes / (stages * stage + weights + kFixed);
     return n < MB ? n : MB;
   };
+  // two stages, unless one lets twice as many blocks share an SM (5957 tokens of 2816
+  // with eight rows: 206 us with two stages, 143 with one and two blocks)
   const int stages = resident(2) == 0 || 2 * resident(2) <= resident(1) ? 1 : 2;
   const int dyn = stages * stage + weights;
   const int per_sm = resident(stages);
@@ -675,7 +680,9 @@ cudaError_t launch_bwd_k(const BlockArgs& a, const BlockGrads& g, int num_sms, c
   if constexpr (G == 32) {
     return launch_bwd<G, NV, KMAX, true, false, MB>(a, g, num_sms, st, groups);
   } else {
-    if (!bwd_fits(a.H, a.k)) return launch_bwd<G, NV, 8, false, false, MB>(a, g, num_sms, st, groups);
+    if constexpr (G == 512) {  // narrower rows fit with eight slots too
+      if (!bwd_fits(a.H, a.k)) return launch_bwd<G, NV, 8, false, false, MB>(a, g, num_sms, st, groups);
+    }
     if (a.H == 8 * G * NV) return launch_bwd<G, NV, KMAX, true, true, MB>(a, g, num_sms, st, groups);
     return launch_bwd<G, NV, KMAX, true, false, MB>(a, g, num_sms, st, groups);
   }
@@ -698,6 +705,11 @@ int block_bwd_groups(int64_t T, int H) {
   return static_cast<int>(groups < kBlockMaxGroups ? groups : kBlockMaxGroups);
 }
 
+// Threads, vectors to a thread, rows in flight and blocks to an SM by width. Few
+// tokens at work at a time keep HBM's pages open: 4096 wide with 256 x 2, three blocks
+// 197 us, four 224, five 364; 512 x 1, two blocks 271; 128 x 4, four blocks 229. 2048
+// wide, six rows: 256 x 1, four blocks 98, six with two rows in flight 114; 128 x 2,
+// five blocks 108.
 cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st) {
   const bool few = a.k <= 2;
   if (a.H <= 256) return launch_fwd<32, 1, 4, 8>(a, num_sms, st);
@@ -713,6 +725,12 @@ cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st) {
   return launch_fwd<512, 4, 2, 1>(a, num_sms, st);
 }
 
+// As above, for the gradient. 4096 wide, two rows: 256 x 2, two blocks 362 us (a loop
+// over k that is not unrolled 391, three blocks' registers 483); 512 x 1, one block
+// 643; 128 x 2 with rows in registers instead of shared memory 480. 2048 wide, six
+// rows: 256 x 1, up to three blocks' registers 200, four 215; 128 x 2 218. 1024 wide,
+// eight rows: 128 x 1 118, a warp with four vectors to a thread 204. Rows beyond 8192
+// are left in L2 (40 % of the copy's rate; a block holds 1024 threads' sums).
 cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st) {
   int groups = 0;
   cudaError_t err;

