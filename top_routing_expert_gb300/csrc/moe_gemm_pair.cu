@@ -766,9 +766,10 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const 
          gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, kTrain) > static_cast<size_t>(optin))
     --args.stages;
   const size_t smem = gemm_pair_smem_bytes(a.E, args.stages, kFp8, kbs, kTrain);
+  // the most a block may have, whatever this call needs: calls with other expert
+  // counts on other threads do not lower it before the launch
   err = cudaFuncSetAttribute(grouped_gemm_pair_kernel<kFp8, kQOut, kGather, kTrans, kEpi>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (num_sms / 2)), 1, 1);

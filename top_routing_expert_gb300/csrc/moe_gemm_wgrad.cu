@@ -601,9 +601,10 @@ template <int kSplit>
 cudaError_t launch_split(const CUtensorMap& tm_x, const CUtensorMap& tm_g, const CUtensorMap& tm_d,
                          const WgradArgs& a, int num_sms, cudaStream_t st) {
   const size_t smem = wgrad_smem_bytes(a.E);
+  // for every expert count: calls on other threads do not lower it before the launch
   cudaError_t err = cudaFuncSetAttribute(wgrad_kernel<kSplit>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(wgrad_smem_bytes(kMaxExperts)));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   constexpr int kCluster = 2 * kSplit;
