@@ -96,13 +96,25 @@ class _Block(ctypes.Structure):
 class BlockConfig:
     """How moe_block_norm ends a block: whether the block's output is normalised
     (post_norm), the factor of the residual, and eps of both norms."""
-    __slots__ = ("post_norm", "residual_scale", "eps")
+    __slots__ = ("post_norm", "residual_scale", "eps", "_blocks")
 
     @classmethod
     def make(cls, post_norm=True, residual_scale=1.0, eps=1e-6) -> "BlockConfig":
         c = cls()
         c.post_norm, c.residual_scale, c.eps = int(bool(post_norm)), float(residual_scale), float(eps)
+        c._blocks = {}
         return c
+
+    def block(self, T: int, H: int, rows: int, k: int):
+        """The moe_block of these sizes, by reference (one of 64 that are kept:
+        making it takes as long as three tensors' checks)."""
+        key = (T, H, rows, k, self.post_norm, self.residual_scale, self.eps)
+        b = self._blocks.get(key)
+        if b is None:
+            if len(self._blocks) == 64:
+                self._blocks.clear()
+            b = self._blocks[key] = ctypes.byref(_Block(*key))
+        return b
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -865,6 +877,11 @@ def _sized(t: Optional[torch.Tensor], dtype, name: str, dev: int, shape) -> Opti
     return t.data_ptr()
 
 
+def _stream_on(stream, dev: int) -> int:
+    """As _stream, the current device being known."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 def moe_expert_gemm(x, offsets, W, out, transposed=False, epilogue=None, pre=None, dev_status=None,
                     stream=None):
     """out [rows, N] bf16 = each row of x [rows, K] times its expert's weights W
@@ -887,7 +904,7 @@ def moe_expert_gemm(x, offsets, W, out, transposed=False, epilogue=None, pre=Non
         E, rows, K, N, _address(x, bf16, "x", dev), _ptr(offsets, torch.int32, "offsets", E + 1),
         _address(W, bf16, "W", dev), 1 if transposed else 0, _EPILOGUES[epilogue],
         _sized(pre, bf16, "pre", dev, shape), _sized(out, bf16, "out", dev, shape),
-        _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+        _ptr(dev_status, torch.int32, "dev_status", 1), _stream_on(stream, dev)))
 
 
 def moe_expert_wgrad(x, grad, offsets, dW, accumulate=False, dev_status=None, stream=None):
@@ -908,7 +925,7 @@ def moe_expert_wgrad(x, grad, offsets, dW, accumulate=False, dev_status=None, st
         E, rows, K, N, _address(x, torch.bfloat16, "x", dev),
         _address(grad, torch.bfloat16, "grad", dev), _ptr(offsets, torch.int32, "offsets", E + 1),
         _address(dW, dW.dtype, "dW", dev), 1 if dW.dtype is torch.bfloat16 else 0,
-        1 if accumulate else 0, _ptr(dev_status, torch.int32, "dev_status", 1), _stream(stream)))
+        1 if accumulate else 0, _ptr(dev_status, torch.int32, "dev_status", 1), _stream_on(stream, dev)))
 
 
 # ------------------------------------------------- between two blocks ----
@@ -930,8 +947,8 @@ class BlockWorkspace:
 
 
 def _block(cfg: BlockConfig, like, name, y, dest_row, topk_w, post_weight, gate, pre_weight):
-    """The moe_block of a call, the addresses of the arguments that both
-    directions share, and the device; like [T, H] gives the sizes."""
+    """The sizes T, H and k of a call, the device, and the arguments that both
+    directions begin with; like [T, H] gives the sizes."""
     if like.dim() != 2:
         raise ValueError(f"{name} must be [T, H]")
     T, H = like.shape
@@ -945,11 +962,12 @@ def _block(cfg: BlockConfig, like, name, y, dest_row, topk_w, post_weight, gate,
             raise ValueError(f"dest_row must be [{T}, k], got {list(dest_row.shape)}")
         k = dest_row.shape[1]
     f32, dev = torch.float32, _device_of(like, name)
-    return _Block(T, H, rows, k, cfg.post_norm, cfg.residual_scale, cfg.eps), (
+    return (T, H, k), dev, (
+        cfg.block(T, H, rows, k), _address(like, torch.bfloat16, name, dev),
         None if y is None else _address(y, torch.bfloat16, "y", dev),
         None if dest_row is None else _address(dest_row, torch.int32, "dest_row", dev),
         _sized(topk_w, f32, "topk_w", dev, (T, k)), _sized(post_weight, f32, "post_weight", dev, (H,)),
-        _sized(gate, f32, "gate", dev, (T,)), _sized(pre_weight, f32, "pre_weight", dev, (H,))), dev
+        _sized(gate, f32, "gate", dev, (T,)), _sized(pre_weight, f32, "pre_weight", dev, (H,)))
 
 
 def moe_block_norm(cfg: BlockConfig, residual, y, out, xn=None, dest_row=None, topk_w=None,
@@ -957,12 +975,12 @@ def moe_block_norm(cfg: BlockConfig, residual, y, out, xn=None, dest_row=None, t
     """out [T, H] = residual_scale * residual + gate * norm(sum_j topk_w_j
     y[dest_row_j]) * post_weight, xn [T, H] = norm(out) * pre_weight (bf16; see
     moe_block_norm in the header for what may be None)."""
-    b, shared, dev = _block(cfg, residual, "residual", y, dest_row, topk_w, post_weight, gate,
-                            pre_weight)
-    bf16, shape = torch.bfloat16, residual.shape
+    (T, H, _), dev, args = _block(cfg, residual, "residual", y, dest_row, topk_w, post_weight, gate,
+                                  pre_weight)
+    bf16, shape = torch.bfloat16, (T, H)
     _check("moe_block_norm", load_library().moe_block_norm(
-        ctypes.byref(b), _address(residual, bf16, "residual", dev), *shared,
-        _sized(out, bf16, "out", dev, shape), _sized(xn, bf16, "xn", dev, shape), _stream(stream)))
+        *args, _sized(out, bf16, "out", dev, shape), _sized(xn, bf16, "xn", dev, shape),
+        _stream_on(stream, dev)))
 
 
 def moe_block_norm_bwd(cfg: BlockConfig, h, y, grad_out, grad_residual, grad_y, grad_xn=None,
@@ -972,20 +990,18 @@ def moe_block_norm_bwd(cfg: BlockConfig, h, y, grad_out, grad_residual, grad_y, 
     """Gradient of moe_block_norm from grad_out and grad_xn [T, H] (bf16, either
     may be None), h [T, H] being what the forward wrote as out. Gradients that
     are None are not formed; ws is needed for grad_post and grad_pre."""
-    b, shared, dev = _block(cfg, h, "h", y, dest_row, topk_w, post_weight, gate, pre_weight)
-    bf16, f32, shape = torch.bfloat16, torch.float32, h.shape
-    T, H, k = b.T, b.H, b.top_k
+    (T, H, k), dev, args = _block(cfg, h, "h", y, dest_row, topk_w, post_weight, gate, pre_weight)
+    bf16, f32, shape = torch.bfloat16, torch.float32, (T, H)
     if grad_y is not None and y is None:
         raise ValueError("grad_y without y")
-    wp, wn = (None, 0) if ws is None else (_ptr(ws.buf, torch.uint8, "ws", ws.nbytes), ws.nbytes)
+    wp, wn = (None, 0) if ws is None else (_address(ws.buf, torch.uint8, "ws", dev), ws.nbytes)
     _check("moe_block_norm_bwd", load_library().moe_block_norm_bwd(
-        ctypes.byref(b), _address(h, bf16, "h", dev), *shared,
-        _sized(grad_out, bf16, "grad_out", dev, shape), _sized(grad_xn, bf16, "grad_xn", dev, shape),
+        *args, _sized(grad_out, bf16, "grad_out", dev, shape), _sized(grad_xn, bf16, "grad_xn", dev, shape),
         _sized(grad_residual, bf16, "grad_residual", dev, shape),
         _sized(grad_y, bf16, "grad_y", dev, y.shape if y is not None else None),
         _sized(grad_topk_w, f32, "grad_topk_w", dev, (T, k)),
         _sized(grad_post, f32, "grad_post", dev, (H,)), _sized(grad_gate, f32, "grad_gate", dev, (T,)),
-        _sized(grad_pre, f32, "grad_pre", dev, (H,)), wp, wn, _stream(stream)))
+        _sized(grad_pre, f32, "grad_pre", dev, (H,)), wp, wn, _stream_on(stream, dev)))
 
 
 # ------------------------------------------------- expert parallelism ----
