@@ -80,6 +80,7 @@ def _close(got, ref, A, factor, dtype, what):
 
 WIDTHS = [64, 192, 256, 448, 960, 1024, 1408, 2048, 2816, 4096, 7168, 8192, 8256, 14336, 16384]
 SHAPES = [(T, H, k) for H in WIDTHS for T, k in ((1, 2), (5, 1), (37, 8))] + [
+    (3, 2048, 1), (9, 512, 3),                 # 48 KB of staged rows and weights, and next to it
     (700, 256, 2), (1500, 64, 4), (333, 4096, 2), (1300, 2048, 6), (2501, 192, 3)]
 
 

@@ -657,14 +657,12 @@ cudaError_t launch_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cud
   const int dyn = stages * stage + weights;
   const int per_sm = resident(stages);
   const auto kernel = block_bwd_kernel<G, NV, KMAX, kStaged, kFull, MB>;
-  if (dyn > 48 * 1024) {
-    // more than a kernel may have without asking; the same for every call, so that
-    // calls of other sizes on other threads do not lower it before the launch
-    const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmSharedBytes - 1024 - static_cast<int>(sizeof(Scratch<G>)));
-    if (err != cudaSuccess) return err;
-  }
+  // the most a block may have, the same for every call: calls of other sizes on other
+  // threads do not lower it before the launch
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmSharedBytes - 1024 - static_cast<int>(sizeof(Scratch<G>)));
+  if (err != cudaSuccess) return err;
   const int64_t need = (a.T + kPer - 1) / kPer, cap = static_cast<int64_t>(num_sms) * per_sm;
   int blocks = static_cast<int>(need < cap ? need : cap);
   if (blocks * kPer > kBlockMaxGroups) blocks = kBlockMaxGroups / kPer;
