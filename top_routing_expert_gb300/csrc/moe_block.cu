@@ -18,7 +18,7 @@
 // All sums are fp32 in a fixed order; every value is rounded once, when it is
 // stored. Both kernels read a token's rows once from HBM and are bound by their
 // bytes, the gradient nearly so: 32768 tokens of 4096 with two rows each, a tenth of
-// them dropped, take 197 us (6.3 TB/s of DRAM traffic; a copy has 6.7) and 362 us (5.5
+// them dropped, take 197 us (6.3 TB/s of DRAM traffic; a copy has 6.7) and 356 us (5.6
 // TB/s); 16383 of 2048 with six rows 98 and 200 us; one token 3.5 us. In
 // the gradient 16 warps to an SM issue in half of the clocks; the rest is the
 // latency of shared memory and of three sums over the block.
@@ -436,6 +436,9 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G, MB)
       return kStaged ? st[(3 + j) * nvec + i]
                      : __ldg(reinterpret_cast<const uint4*>(a.y) + static_cast<size_t>(row) * nvec + i);
     };
+    // up to two rows stay in registers for the weights' gradient (362 -> 356 us)
+    constexpr bool kKeep = kStaged && KMAX <= 2 && NV <= 2;
+    uint4 kept[kKeep ? KMAX : 1][NV];
     F2 c[NV][4];
     float sums[3] = {0.f, 0.f, 0.f};  // h^2, pre g_xn h, c^2
     if (a.y != nullptr) {
@@ -454,7 +457,9 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G, MB)
             const int i = gt + G * v;
             if (kFull || i < nvec) {
               F2 f[4];
-              unpack8(y_vec(j, row, i), f);
+              const uint4 yv = y_vec(j, row, i);
+              if constexpr (kKeep) kept[j][v] = yv;
+              unpack8(yv, f);
 #pragma unroll
               for (int q = 0; q < 4; ++q) c[v][q] = f32x2_fma(ww, f[q], c[v][q]);
             }
@@ -556,7 +561,8 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G, MB)
               if (kFull || i < nvec) {
                 if (g.w != nullptr) {
                   F2 f[4];
-                  unpack8(y_vec(j, row, i), f);
+                  if constexpr (kKeep) unpack8(kept[j & 1][v], f);
+                  else unpack8(y_vec(j, row, i), f);
 #pragma unroll
                   for (int q = 0; q < 4; ++q) d = f32x2_fma(G8[v][q], f[q], d);
                 }
@@ -726,9 +732,9 @@ cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st) {
   return launch_fwd<512, 4, 2, 1>(a, num_sms, st);
 }
 
-// As above, for the gradient. 4096 wide, two rows: 256 x 2, two blocks 362 us (a loop
-// over k that is not unrolled 391, three blocks' registers 483); 512 x 1, one block
-// 643; 128 x 2 with rows in registers instead of shared memory 480. 2048 wide, six
+// As above, for the gradient. 4096 wide, two rows: 256 x 2, two blocks 356 us (rows
+// read again from shared memory 362; a loop over k that is not unrolled 391, three
+// blocks' registers 483); 512 x 1, one block 643; 128 x 2 with rows in registers instead of shared memory 480. 2048 wide, six
 // rows: 256 x 1, up to three blocks' registers 200, four 215; 128 x 2 218. 1024 wide,
 // eight rows: 128 x 1 118, a warp with four vectors to a thread 204. Rows beyond 8192
 // are left in L2 (40 % of the copy's rate; a block holds 1024 threads' sums).
