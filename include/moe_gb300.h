@@ -557,7 +557,10 @@ MOE_API moe_status moe_block_norm_workspace_size(int64_t T, int64_t H, size_t* b
  *   out: grad_residual [T,H] bf16; grad_y [rows,H] bf16, the rows that dest_row
  *        names (others are left as they were); grad_topk_w [T,k] fp32 (0 at
  *        dropped slots); grad_post, grad_pre [H] fp32; grad_gate [T] fp32.
- *        Each may be NULL. dest_row names a row once at most.
+ *        Each may be NULL. dest_row names a row once at most. (With post_norm
+ *        the weight of a token's only row scales what is normalised: its
+ *        gradient is 0 but for eps, and grad_topk_w then holds the fp32
+ *        rounding of terms that cancel.)
  * ws, needed for grad_post and grad_pre alone: moe_block_norm_workspace_size.
  * grad_residual may be grad_out itself; nothing else may overlap. The same
  * inputs give the same bits. */

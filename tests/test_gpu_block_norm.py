@@ -344,3 +344,34 @@ def test_far_rows():
     ref = (x[-4:].double() * y[dest[last, 0].long()].double()).sum(1)
     size = (x[-4:].double() * y[dest[last, 0].long()].double()).abs().sum(1)
     assert ((gw[-4:, 0].double() - ref).abs() <= 2.0 ** -18 * size).all()
+
+
+def test_device_refusals():
+    """Strided, mistyped, misaligned and undersized tensors are refused before a launch."""
+    cfg = moe.BlockConfig.make()
+    bf = lambda *n: torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    x, y, out = bf(4, 64), bf(8, 64), torch.full((4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    dest = torch.arange(8, dtype=torch.int32, device=DEV).view(4, 2)
+    w, gp = torch.ones(4, 2, device=DEV), torch.zeros(64, device=DEV)
+    fwd, bwd = moe.moe_block_norm, moe.moe_block_norm_bwd
+    for call in (lambda: fwd(cfg, bf(4, 128)[:, :64], y, out, dest_row=dest, topk_w=w),
+                 lambda: fwd(cfg, x, y.float(), out, dest_row=dest, topk_w=w),
+                 lambda: fwd(cfg, x, y, out, dest_row=dest.long(), topk_w=w),
+                 lambda: fwd(cfg, x, y, out, dest_row=dest, topk_w=w.double()),
+                 lambda: fwd(cfg, x, y, out, dest_row=dest.T.contiguous().T, topk_w=w),
+                 lambda: bwd(cfg, x, y, x.half(), out, None, dest_row=dest, topk_w=w),
+                 lambda: bwd(cfg, x, None, x, out, y)):
+        with pytest.raises(ValueError):
+            call()
+    shifted = bf(4 * 64 + 8)[4:4 + 4 * 64].view(4, 64)
+    for code, call in ((5, lambda: fwd(cfg, shifted, y, out, dest_row=dest, topk_w=w)),
+                       (2, lambda: fwd(cfg, x, y[:3], out)),
+                       (1, lambda: fwd(cfg, x, y, None, dest_row=dest, topk_w=w)),
+                       (1, lambda: bwd(cfg, x, y, x, out, None, dest_row=dest, topk_w=w, grad_post=gp)),
+                       (1, lambda: bwd(cfg, x, y, None, out, None, dest_row=dest, topk_w=w)),
+                       (4, lambda: bwd(cfg, x, y, x, out, None, dest_row=dest, topk_w=w, grad_post=gp,
+                                       ws=moe.BlockWorkspace(0, 64)))):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.code == code
+    assert (out == 7).all()

@@ -337,3 +337,36 @@ def test_streams_and_repeats():
         torch.cuda.synchronize()
         for a, b, c in zip(first, second, third):
             assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_device_refusals():
+    """Strided, misaligned, mistyped and missing tensors are refused before a launch."""
+    bf = lambda *n: torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    x, W, out, dW = bf(4, 64), bf(1, 64, 128), torch.full((4, 128), NONE, dtype=torch.bfloat16, device=DEV), bf(1, 64, 128)
+    gemm, wgrad = moe.moe_expert_gemm, moe.moe_expert_wgrad
+    wide = bf(4, 128)
+    for call in (lambda: gemm(wide[:, :64], off, W, out, dev_status=st),
+                 lambda: gemm(x, off, W.transpose(1, 2), out, transposed=True, dev_status=st),
+                 lambda: gemm(x.float(), off, W, out, dev_status=st),
+                 lambda: gemm(x, off.long(), W, out, dev_status=st),
+                 lambda: gemm(x, off[:1], W, out, dev_status=st),
+                 lambda: gemm(x, off, W, out, epilogue="gelu", pre=wide[:, :64], dev_status=st),
+                 lambda: wgrad(wide[:, :64], bf(4, 128), off, dW, dev_status=st),
+                 lambda: wgrad(x, bf(4, 128).T.contiguous().T, off, dW, dev_status=st),
+                 lambda: wgrad(x, bf(4, 128), off, dW.half(), dev_status=st)):
+        with pytest.raises(ValueError):
+            call()
+    shifted = bf(4 * 64 + 8)[4:4 + 4 * 64].view(4, 64)          # 8 bytes past an aligned address
+    for code, call in ((5, lambda: gemm(shifted, off, W, out, dev_status=st)),
+                       (5, lambda: wgrad(shifted, bf(4, 128), off, dW, dev_status=st)),
+                       (1, lambda: gemm(x, off, W, out)),
+                       (1, lambda: gemm(x, off, W, out, epilogue="gelu_grad", dev_status=st)),
+                       (2, lambda: gemm(x, off, W, out, pre=wide, dev_status=st)),
+                       (3, lambda: wgrad(x, bf(4, 128), off, dW, accumulate=True, dev_status=st)),
+                       (3, lambda: gemm(bf(4, 32), off, bf(1, 32, 128), out, dev_status=st))):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.code == code
+    assert (out == NONE).all()
