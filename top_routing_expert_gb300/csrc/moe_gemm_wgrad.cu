@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
   uint32_t* abort_flag = tmem_slot + 1;
   uint32_t* peer_issued = abort_flag + 1;
-  int* offs = reinterpret_cast<int*>(peer_issued + 1);        // [E+1]
+  volatile uint32_t* loaded = peer_issued + 1;  // stages this CTA's producer has issued
+  int* offs = reinterpret_cast<int*>(peer_issued + 2);        // [E+1]
   uint8_t* order = reinterpret_cast<uint8_t*>(offs + p.E + 1);  // [E] longest segment first
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     mbar_init(xbar, 1);
     *abort_flag = 0u;
+    *loaded = 0u;
     fence_barrier_init();
   }
   if (warp == kFirstEpi && lane == 0) {
@@ -298,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = c.lo + kb * kDepth;
             tma_load_3d_pair(sx, &tm_x, bar, 0, row, xb);
             tma_load_3d_pair(sx + kOpBytes, &tm_g, bar, 0, row, gb);
+            *loaded = static_cast<uint32_t>(issued + 1);
           }
           __syncwarp();
           ++issued;
@@ -402,7 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kFirstEpi) {
     // ------------------------------------- zeros behind a segment's end ----
     // whole 128-byte rows, which the swizzle keeps together, in the four
-    // 64-column blocks (two of each operand) of each tail stage
+    // 64-column blocks (two of each operand) of each tail stage. Between two tails
+    // there may be whole segments without one, most of the kernel's time, so the limit
+    // of this wait counts from the producer's last stage.
     int stage = 0;
     uint32_t tail_par = 0;
     bool aborted = false;
@@ -412,7 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = (stage + nk - 1) % kStages;
       stage = (stage + nk) % kStages;
       if (!is_tail(c.len, nk - 1)) continue;
-      if (!__all_sync(0xffffffffu, pair_wait(&tail_ld[s], tail_par >> s & 1u))) {
+      const bool ok = mbar_wait_progress(&tail_ld[s], tail_par >> s & 1u, wc, loaded);
+      if (!ok) st_u32_cluster(peer_abort, 1u);
+      if (!__all_sync(0xffffffffu, ok)) {
         aborted = true;
         break;
       }

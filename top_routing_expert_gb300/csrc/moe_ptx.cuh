@@ -115,6 +115,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// As mbar_wait, for a wait that lasts while another warp works through many stages:
+// `progress` (shared memory) counts them, and the limit runs anew whenever it has moved.
+__device__ __forceinline__ bool mbar_wait_progress(uint64_t* bar, uint32_t parity,
+                                                   const WaitCtl& w,
+                                                   const volatile uint32_t* progress) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = global_timer_ns();
+  uint32_t n = 0, seen = *progress;
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((++n & 15u) == 0) {
+      if (*w.abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      const uint32_t count = *progress;
+      if (count != seen) {
+        seen = count;
+        t0 = now;
+      } else if (now - t0 > w.timeout_ns) {
+        *w.abort_flag = 1u;
+        atomicOr(w.dev_status, MOE_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
 // Same, ignoring the abort flag: used while draining in-flight work before
 // the CTA exits.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity,
