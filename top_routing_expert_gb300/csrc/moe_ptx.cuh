@@ -83,6 +83,19 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
   return done != 0;
 }
 
+// One look, without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Shared state of one CTA's bounded waits: a flag in shared memory that any
 // role raises when it gives up, so that the other roles stop too.
 struct WaitCtl {
@@ -117,28 +130,34 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
 
 // As mbar_wait, for a wait that lasts while another warp works through many stages:
 // `progress` (shared memory) counts them, and the limit runs anew whenever it has moved.
+// The hardware suspends a polling thread for as long as it likes (with 1 ns as the limit
+// no wait of a 50 us kernel gave up, nor with a suspend-time hint of 0), so below kSpinNs
+// the thread only looks, and the limit holds. Not for warps that keep the pipeline going:
+// with this choice in every wait of the weights' gradient 128 experts took 844 us, not 834.
+constexpr uint64_t kSpinNs = 100000;
 __device__ __forceinline__ bool mbar_wait_progress(uint64_t* bar, uint32_t parity,
                                                    const WaitCtl& w,
                                                    const volatile uint32_t* progress) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const bool spin = w.timeout_ns < kSpinNs;
+  auto done = [&] { return spin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   uint64_t t0 = global_timer_ns();
   uint32_t n = 0, seen = *progress;
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((++n & 15u) == 0) {
-      if (*w.abort_flag) return false;
-      const uint64_t now = global_timer_ns();
-      const uint32_t count = *progress;
-      if (count != seen) {
-        seen = count;
-        t0 = now;
-      } else if (now - t0 > w.timeout_ns) {
-        *w.abort_flag = 1u;
-        atomicOr(w.dev_status, MOE_DEV_TIMEOUT);
-        return false;
-      }
+  while (!done()) {
+    if (!spin && (++n & 15u) != 0) continue;
+    if (*w.abort_flag) return false;
+    const uint64_t now = global_timer_ns();
+    const uint32_t count = *progress;
+    if (count != seen) {
+      seen = count;
+      t0 = now;
+    } else if (now - t0 > w.timeout_ns) {
+      *w.abort_flag = 1u;
+      atomicOr(w.dev_status, MOE_DEV_TIMEOUT);
+      return false;
     }
   }
+  return true;
 }
 
 // Same, ignoring the abort flag: used while draining in-flight work before
