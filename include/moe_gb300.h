@@ -554,6 +554,7 @@ MOE_API moe_status moe_block_norm_workspace_size(int64_t T, int64_t H, size_t* b
  *        norm's gradient is taken (needed with grad_xn); y, dest_row, topk_w,
  *        the weights and gate as the forward had them; grad_out, grad_xn [T,H]
  *        bf16 (NULL: no such gradient; not both NULL).
+ *        With rows 0 and dest_row, y may be NULL: every slot is dropped.
  *   out: grad_residual [T,H] bf16; grad_y [rows,H] bf16, the rows that dest_row
  *        names (others are left as they were); grad_topk_w [T,k] fp32 (0 at
  *        dropped slots); grad_post, grad_pre [H] fp32; grad_gate [T] fp32.

@@ -962,10 +962,11 @@ def _block(cfg: BlockConfig, like, name, y, dest_row, topk_w, post_weight, gate,
             raise ValueError(f"dest_row must be [{T}, k], got {list(dest_row.shape)}")
         k = dest_row.shape[1]
     f32, dev = torch.float32, _device_of(like, name)
+    dest = None if dest_row is None else _address(dest_row, torch.int32, "dest_row", dev)
     return (T, H, k), dev, (
         cfg.block(T, H, rows, k), _address(like, torch.bfloat16, name, dev),
         None if y is None else _address(y, torch.bfloat16, "y", dev),
-        None if dest_row is None else _address(dest_row, torch.int32, "dest_row", dev),
+        None if y is None else dest,   # a y of no rows has address 0 too, but slots
         _sized(topk_w, f32, "topk_w", dev, (T, k)), _sized(post_weight, f32, "post_weight", dev, (H,)),
         _sized(gate, f32, "gate", dev, (T,)), _sized(pre_weight, f32, "pre_weight", dev, (H,)))
 

@@ -1755,6 +1755,9 @@ moe_status moe_block_norm_bwd(const moe_block* b, const moe_bf16* h, const moe_b
   MOE_OPTIONAL(grad_xn);
   if (grad_xn != nullptr) MOE_REQUIRE(h);
   if (grad_xn == nullptr && grad_pre != nullptr) return MOE_ERR_NULL;
+  // a buffer of no rows may have no address: its slots name no row, so y is never read,
+  // and the gradients of what multiplies it are 0
+  if (y == nullptr && b->rows == 0 && dest_row != nullptr) y = grad_out != nullptr ? grad_out : grad_xn;
   if (y == nullptr && (grad_y || grad_topk_w || grad_post || grad_gate)) return MOE_ERR_NULL;
   BlockArgs a;
   MOE_TRY(block_args(b, y, dest_row, topk_w, post_weight, gate, pre_weight, &a));
