@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G, MB) block_kernel(BlockArgs 
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int i = gt + G * v;
-      res[v] = i < nvec ? __ldg(reinterpret_cast<const uint4*>(a.residual) + t * nvec + i)
+      // not by the read-only path: out may be the residual
+      res[v] = i < nvec ? reinterpret_cast<const uint4*>(a.residual)[t * nvec + i]
                         : make_uint4(0, 0, 0, 0);
     }
     float gate = 1.f;
