@@ -10,11 +10,11 @@ the next block's normalised input come out. Forward over T tokens:
 Backward, from the gradients of the next stream, of the next normalised input
 and of the balance loss:
   4. moe_block_norm_bwd; 3. moe_expert_gemm with the transposed weights (GELU's
-  slope in its epilogue) and moe_expert_wgrad; 2. moe_combine of the rows'
-  gradients, weights 1; 1. moe_route_grouped_bwd, and the router's own two
-  products as those of a single expert.
-Every step runs in the library's kernels on the current stream but for the sum
-of the two gradients that reach xn and that of the gate's bias; nothing synchronises with the host, so both
+  slope in its epilogue) and moe_expert_wgrad; 1. moe_route_grouped_bwd, and the
+  router's own two products as those of a single expert; 2. moe_block_norm without
+  norms adds up what reaches xn, from the router and from the token's rows.
+Every step runs in the library's kernels on the current stream but for the sum of the
+gate's bias' gradient; nothing synchronises with the host, so both
 directions can be captured in a CUDA graph. A small run of it all:
 python -m top_routing_expert_gb300.block
 """
@@ -25,8 +25,8 @@ from typing import Optional
 import torch
 
 from . import (BlockConfig, BlockWorkspace, MoeShape, RouteConfig, Workspace, _shape, moe_block_norm,
-               moe_block_norm_bwd, moe_combine, moe_expert_gemm, moe_expert_wgrad, moe_permute,
-               moe_route, moe_route_grouped, moe_route_grouped_bwd)
+               moe_block_norm_bwd, moe_expert_gemm, moe_expert_wgrad, moe_permute, moe_route,
+               moe_route_grouped, moe_route_grouped_bwd)
 
 
 class BlockWeights:
@@ -76,7 +76,7 @@ class TrainBlock:
         self.g_gate_wide = new(1, s.H, wide, dt=f32)
         self.g_router = new(s.T, s.H)
         self.one_segment = torch.tensor([0, s.T], dtype=i32, device=device)
-        self.ones = torch.ones(s.T, s.top_k, dtype=f32, device=device)
+        self.add = BlockConfig.make(post_norm=False)
         self._kept = None
 
     def forward(self, h: torch.Tensor, xn: torch.Tensor, w: BlockWeights, out: torch.Tensor,
@@ -139,19 +139,20 @@ class TrainBlock:
         moe_expert_gemm(self.g_u, self.offsets, w.W1, self.g_x, transposed=True, dev_status=st)
         moe_expert_wgrad(self.x_perm, self.g_u, self.offsets, grads.W1, accumulate=accumulate,
                          dev_status=st)
-        moe_combine(s, self.g_x, self.dest_row, self.ones, grad_xn)
         moe_route_grouped_bwd(s, self.route, self.logits, self.topk_idx, self.g_topk_w,
                               self.g_logits, grad_aux=grad_aux,
                               routed_counts=self.routed_counts if grad_aux is not None else None)
         if w.gate_bias is not None:
             torch.sum(self.g_logits, 0, out=grads.gate_bias)
         # the router is a product with a single expert, logits = xn . gate, and its
-        # gradient enters the two products in bf16 like every other operand
+        # gradient enters the two products in bf16, which they take: off by 2^-8 of each
+        # value at most, as every gradient that goes from step to step is
         self.g_scores[:, :s.E].copy_(self.g_logits)
         self.gate_wide[:, :s.E].copy_(w.gate)
         moe_expert_gemm(self.g_scores, self.one_segment, self.gate_wide[None], self.g_router,
                         transposed=True, dev_status=st)
-        grad_xn.add_(self.g_router)
+        # what reaches xn, g_router + sum_j g_x[dest_j], in fp32 and rounded once
+        moe_block_norm(self.add, self.g_router, self.g_x, grad_xn, dest_row=self.dest_row)
         moe_expert_wgrad(xn, self.g_scores, self.one_segment, self.g_gate_wide, dev_status=st)
         grads.gate.copy_(self.g_gate_wide[0, :, :s.E])
 
