@@ -56,3 +56,57 @@ def test_gradient_of_the_input_is_rounded_once(shape):
         ref, size = ref + term, size + term.abs()
     err = (gx.double() - ref).abs()
     assert (err <= 2.0 ** -8 * ref.abs() + (k + 1) * 2.0 ** -24 * size).all()
+
+
+NAMES = ("W1", "W2", "gate", "post", "pre", "gate_bias")
+
+
+def _grads(w):
+    return {n: getattr(w, n) for n in NAMES if getattr(w, n) is not None}
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("next_norm", [True, False])
+@pytest.mark.parametrize("bias", [True, False])
+def test_every_gradient_accumulates(shape, next_norm, bias):
+    """Two micro-batches, and three from a replayed graph: sums of fp32 values in the
+    batches' order, to the bit. (The products' gradients are added as whole sums.)"""
+    block, w, batches = _make(*shape, seed=5, bias=bias)
+    each = []
+    for d in batches:
+        g = BlockWeights.zeros_like(w)
+        for t in _grads(g).values():
+            t.fill_(3)                                     # written, not added
+        _step(block, w, d, g, next_norm)
+        each.append(_grads(g))
+    total = BlockWeights.zeros_like(w)
+    for d in batches:
+        _step(block, w, d, total, next_norm, accumulate="all")
+    for n, t in _grads(total).items():
+        assert torch.equal(t, each[0][n] + each[1][n]), n
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(block, w, batches[0], total, next_norm, accumulate="all")
+    want = {n: t.clone() for n, t in _grads(total).items()}
+    for _ in range(2):
+        graph.replay()
+        for n, t in _grads(total).items():
+            want[n] += each[0][n]
+            assert torch.equal(t, want[n]), n
+
+
+def test_accumulate_with_no_tokens_and_refusals():
+    block, w, _ = _make(0, 128, 4, 2, 64, 1.0, seed=1)
+    e = torch.empty(0, 128, dtype=torch.bfloat16, device=DEV)
+    grads = BlockWeights.zeros_like(w)
+    for t in _grads(grads).values():
+        t.fill_(3)
+    block.forward(e, e, w, e, e)
+    block.backward(e, e, e, e, grads, accumulate="all")
+    assert all((t == 3).all() for t in _grads(grads).values())
+    for bad in ("some", None, 2):
+        with pytest.raises(ValueError):
+            block.backward(e, e, e, e, grads, accumulate=bad)
+    block.backward(e, e, e, e, grads, accumulate=True)
+    assert (grads.W1 == 3).all() and (grads.post == 0).all()

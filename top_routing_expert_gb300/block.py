@@ -14,8 +14,9 @@ and of the balance loss:
   router's own two products as those of a single expert; 2. moe_block_norm without
   norms adds up what reaches xn, from the router and from the token's rows.
 Every step runs in the library's kernels on the current stream but for the sum of the
-gate's bias' gradient; nothing synchronises with the host, so both
-directions can be captured in a CUDA graph. A small run of it all:
+gate's bias' gradient and, accumulated, of the small weights' gradients; nothing
+synchronises with the host, so both directions can be captured in a CUDA graph. A
+small run of it all:
 python -m top_routing_expert_gb300.block
 """
 from __future__ import annotations
@@ -77,6 +78,8 @@ class TrainBlock:
         self.g_router = new(s.T, s.H)
         self.one_segment = torch.tensor([0, s.T], dtype=i32, device=device)
         self.add = BlockConfig.make(post_norm=False)
+        # one call's gradients of the small weights, where they are accumulated
+        self.g_post, self.g_pre, self.g_bias = new(s.H, dt=f32), new(s.H, dt=f32), new(s.E, dt=f32)
         self._kept = None
 
     def forward(self, h: torch.Tensor, xn: torch.Tensor, w: BlockWeights, out: torch.Tensor,
@@ -109,28 +112,36 @@ class TrainBlock:
     def backward(self, grad_out: Optional[torch.Tensor], grad_xn_next: Optional[torch.Tensor],
                  grad_h: torch.Tensor, grad_xn: torch.Tensor, grads: BlockWeights,
                  grad_token_gate: Optional[torch.Tensor] = None,
-                 grad_aux: Optional[torch.Tensor] = None, accumulate: bool = False) -> None:
-        """grad_h, grad_xn [T, H] (bf16) and the weights' gradients (fp32; those of
-        W1 and W2 added to what is there if accumulate, the others written) from
-        those of out and xn_next [T, H] (bf16; either may be None) and of aux [1]."""
+                 grad_aux: Optional[torch.Tensor] = None, accumulate=False) -> None:
+        """grad_h, grad_xn [T, H] (bf16) and the weights' gradients (fp32) from those
+        of out and xn_next [T, H] (bf16; either may be None) and of aux [1].
+        accumulate: False, the weights' gradients are written; "all", each is added
+        to what is there (every micro-batch but a step's first); True, those of W1
+        and W2 alone are added and the others written, for a caller who adds up the
+        small ones. Gradients of tokens are written in any case."""
+        if accumulate not in (False, True, "all"):
+            raise ValueError(f'accumulate must be False, True or "all", got {accumulate!r}')
+        every = accumulate == "all"
         if self._kept is None:
             raise RuntimeError("backward() without a forward()")
         s, st = self.shape, self.dev_status
         xn, w, out, token_gate = self._kept
         if s.T == 0:
-            for t in (grads.post, grads.pre, grads.gate, grads.gate_bias,
-                      None if accumulate else grads.W1, None if accumulate else grads.W2):
+            small = [] if every else [grads.post, grads.pre, grads.gate, grads.gate_bias]
+            for t in small + ([] if accumulate else [grads.W1, grads.W2]):
                 if t is not None:
                     t.zero_()
             return
+        g_post, g_pre, g_bias = ((self.g_post, self.g_pre, self.g_bias) if every else
+                                 (grads.post, grads.pre, grads.gate_bias))
         if grad_xn_next is None:
-            grads.pre.zero_()
+            g_pre.zero_()
         moe_block_norm_bwd(self.block, out, self.y_perm, grad_out, grad_h, self.g_y,
                            grad_xn=grad_xn_next, dest_row=self.dest_row, topk_w=self.topk_w,
                            post_weight=w.post, gate=token_gate, pre_weight=w.pre,
-                           grad_topk_w=self.g_topk_w, grad_post=grads.post,
+                           grad_topk_w=self.g_topk_w, grad_post=g_post,
                            grad_gate=grad_token_gate,
-                           grad_pre=grads.pre if grad_xn_next is not None else None,
+                           grad_pre=g_pre if grad_xn_next is not None else None,
                            ws=self.block_ws)
         moe_expert_gemm(self.g_y, self.offsets, w.W2, self.g_u, transposed=True,
                         epilogue="gelu_grad", pre=self.u, dev_status=st)
@@ -143,7 +154,7 @@ class TrainBlock:
                               self.g_logits, grad_aux=grad_aux,
                               routed_counts=self.routed_counts if grad_aux is not None else None)
         if w.gate_bias is not None:
-            torch.sum(self.g_logits, 0, out=grads.gate_bias)
+            torch.sum(self.g_logits, 0, out=g_bias)
         # the router is a product with a single expert, logits = xn . gate, and its
         # gradient enters the two products in bf16, which they take: off by 2^-8 of each
         # value at most, as every gradient that goes from step to step is
@@ -154,7 +165,15 @@ class TrainBlock:
         # what reaches xn, g_router + sum_j g_x[dest_j], in fp32 and rounded once
         moe_block_norm(self.add, self.g_router, self.g_x, grad_xn, dest_row=self.dest_row)
         moe_expert_wgrad(xn, self.g_scores, self.one_segment, self.g_gate_wide, dev_status=st)
-        grads.gate.copy_(self.g_gate_wide[0, :, :s.E])
+        g_gate = self.g_gate_wide[0, :, :s.E]
+        if not every:
+            grads.gate.copy_(g_gate)
+            return
+        grads.gate.add_(g_gate)
+        grads.post.add_(g_post)
+        grads.pre.add_(g_pre)
+        if w.gate_bias is not None:
+            grads.gate_bias.add_(g_bias)
 
 
 def main() -> None:
