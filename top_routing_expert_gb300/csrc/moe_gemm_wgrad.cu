@@ -4,15 +4,15 @@
 // ragged segment of rows.
 //
 // Both operands lie with the contraction as their outer dimension, so both are
-// MN-major UMMA operands: a TMA box of 128 rows x 2 blocks of 64 columns (32 KB)
+// MN-major UMMA operands: a TMA box of 64 rows x 2 blocks of 64 columns (16 KB)
 // is a CTA's share of one operand in a stage, as memory has it. A CTA pair
 // computes 256 x 256 of dW[e] (cta_group::2, M = 256, N = 256): each CTA holds
 // 128 columns of x and 128 of g, and its own 128 rows of the result.
 //
 // A segment starts at any row and its length is no multiple of anything, while
-// a box always has 128 rows: those behind the segment belong to the next expert
+// a box always has 64 rows: those behind the segment belong to the next expert
 // or to nothing, and may hold infinities or NaN. Only ceil(n / 16) of a stage's
-// eight K steps are issued, and where the last one has rows of both kinds the
+// four K steps are issued, and where the last one has rows of both kinds the
 // stage takes a longer way: its loads count on barriers of their own CTA, a
 // warp waits for them, writes zeros over the rows behind the segment in both
 // operands, and hands the stage to the issuer.
@@ -46,8 +46,8 @@ constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpi = 3;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
-constexpr uint32_t kOpBytes = kDepth * 128 * 2;      // 32 KB: 128 rows x 128 columns
-constexpr uint32_t kBlockBytes = kDepth * 128;       // 16 KB: one block of 64 columns
+constexpr uint32_t kOpBytes = kDepth * 128 * 2;      // 16 KB: 64 rows x 128 columns
+constexpr uint32_t kBlockBytes = kDepth * 128;       // 8 KB: one block of 64 columns
 constexpr uint32_t kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kOutBytes = 32 * 128;             // one warp's 32 rows x 128 bytes
 constexpr uint32_t kTmemCols = 2 * kTile;
@@ -136,7 +136,7 @@ __device__ __forceinline__ bool is_tail(int len, int kb) {
 
 // Issues a stage's K steps of 16 rows and releases it. One 128-byte row per k: a
 // step is 2 KB on in both operands (128 in a descriptor); the blocks of 64
-// columns are 16 KB apart, g's behind x's. Called by the whole warp, straight on
+// columns are 8 KB apart, g's behind x's. Called by the whole warp, straight on
 // for a full stage, so that an elected lane keeps the tensor core's queue filled
 // (a lane that issued alone in a diverged warp, its descriptors built on the way,
 // took 185 clocks per UMMA of 128: 852 us instead of 788 for 128 experts).
