@@ -738,7 +738,7 @@ cudaError_t launch_block(const BlockArgs& a, int num_sms, cudaStream_t st) {
 // blocks' registers 483); 512 x 1, one block 643; 128 x 2 with rows in registers instead of shared memory 480. 2048 wide, six
 // rows: 256 x 1, up to three blocks' registers 200, four 215; 128 x 2 218. 1024 wide,
 // eight rows: 128 x 1 118, a warp with four vectors to a thread 204. Rows beyond 8192
-// are left in L2 (40 % of the copy's rate; a block holds 1024 threads' sums).
+// are left in L2 (29 to 45 % of the copy's rate; a block holds 1024 threads' sums).
 cudaError_t launch_block_bwd(const BlockArgs& a, const BlockGrads& g, int num_sms, cudaStream_t st) {
   int groups = 0;
   cudaError_t err;
